@@ -49,7 +49,7 @@
  *   - All work is enqueued on `stream` (a cudaStream_t; NULL = the legacy
  *     default stream).  No call synchronises the host, so every call can be
  *     captured into a CUDA graph.  One kernel launch per call (the unfused
- *     comparison chain: four).  The first call
+ *     comparison chain: four; dsa_cache_fork and dsa_cache_compact: two).  The first call
  *     on a device raises the kernel's dynamic shared-memory limit there (a
  *     per-device, once-only setting); make it before capturing a graph.
  *   - Host-side checks: a bad argument returns a status other than DSA_OK and
@@ -98,6 +98,9 @@ typedef enum { DSA_ROPE_NEOX = 0, DSA_ROPE_GPTJ = 1 } dsa_rope_style;
 #define DSA_DEVERR_INTERNAL 8 /* an internal precondition failed: the logits
                                  kernel's shared-memory base was not 1024-byte
                                  aligned (never expected); nothing was written */
+#define DSA_DEVERR_ROW 16     /* a block-table row that the call may not use */
+#define DSA_DEVERR_POOL 32    /* no free page was left */
+#define DSA_DEVERR_REFS 64    /* a table entry held a page without references */
 
 /* Launch flags. */
 #define DSA_FLAG_PDL 1u /* programmatic dependent launch: the kernel may start
@@ -324,6 +327,109 @@ dsa_status dsa_indexer_mqa_logits(
     const int32_t* block_table, int64_t bt_stride, const int32_t* context_lens,
     float* logits, int64_t logits_stride, int32_t max_context,
     int32_t T, int32_t H, uint32_t flags, int32_t* err_flags, void* stream);
+
+/*
+ * Upkeep of a paged cache's pages: copy, fork, free, compact.
+ *
+ * A pool is num_pages pages and three caller-owned int32 arrays on the device:
+ *   page_refs [num_pages]      how many block-table entries hold the page;
+ *                              0 = free.
+ *   block_table [rows, bt_stride >= bt_cols]
+ *                              entry j of a row: the page of its tokens
+ *                              [j * page_size, (j + 1) * page_size); -1 =
+ *                              absent.  Only a row's first
+ *                              ceil(context_lens[row] / page_size) entries
+ *                              count; later ones may hold anything and are
+ *                              neither read nor written.
+ *   context_lens [rows]        tokens of each row; 0 = an unused row.
+ * One pool serves n_caches caches at once (every layer's index-K cache, K
+ * cache, V cache): `caches` and `page_bytes` are HOST arrays, read during the
+ * call, of each cache's base pointer (4-byte aligned) and bytes per page (a
+ * multiple of 4, at most 2^30; 16-byte aligned pages move 16 bytes at a time);
+ * page p of cache c is bytes [p * page_bytes[c], (p + 1) * page_bytes[c]).
+ * Either index-K layout has page_bytes = page_size * 132.  0 <= n_caches <=
+ * DSA_MAX_CACHES; with none only the tables are kept.
+ *
+ * A page given out is always the lowest free one, so results do not depend on
+ * the order in which the GPU runs.  `flags` must be 0.  Calls on one pool must
+ * be ordered (one stream, or events).  Bad entries of the lists and tables set
+ * bits of *err_flags and are left out; they never leave the buffers.
+ */
+#define DSA_MAX_CACHES 128
+#define DSA_MAX_FORKS 1024
+
+/*
+ * Copies page src_pages[i] to page dst_pages[i] of every cache, i < n (one
+ * launch).  The destinations must be distinct and no page may be both a
+ * source and a destination, except of a pair that names one page twice (which
+ * does nothing).  A page outside the pool sets DSA_DEVERR_SLOT and its pair
+ * is skipped.
+ */
+dsa_status dsa_cache_copy_pages(
+    void* const* caches, const int64_t* page_bytes, int32_t n_caches,
+    int64_t num_pages, const int32_t* src_pages, const int32_t* dst_pages,
+    int32_t n, uint32_t flags, int32_t* err_flags, void* stream);
+
+/*
+ * Forks sequences (two launches): row children[i] becomes a copy of row
+ * parents[i].  They share the parent's whole pages (page_refs + 1 each; an
+ * absent entry stays absent); where the parent ends inside a page the child
+ * gets a free page of its own, into which that page is copied in every cache,
+ * so that both may go on writing.  A parent may have any number of children.
+ *   parents, children  int32 [n], n <= DSA_MAX_FORKS.  A child must be an
+ *                  unused row (context_lens 0), named once.
+ *   workspace      dsa_cache_fork_workspace_bytes(n) bytes, 8-byte aligned,
+ *                  contents scratch.
+ * A fork whose rows are out of range, whose child is in use or was named
+ * before, or whose parent has more blocks than bt_cols sets DSA_DEVERR_ROW and
+ * does not happen.  Free pages are given in the order of the list; a fork
+ * that finds none sets DSA_DEVERR_POOL and does not happen.
+ */
+size_t dsa_cache_fork_workspace_bytes(int32_t n);
+
+dsa_status dsa_cache_fork(
+    void* const* caches, const int64_t* page_bytes, int32_t n_caches,
+    int64_t num_pages, int32_t* page_refs, int32_t* block_table,
+    int32_t bt_cols, int64_t bt_stride, int32_t* context_lens, int32_t rows,
+    int32_t page_size, const int32_t* parents, const int32_t* children,
+    int32_t n, uint32_t flags, void* workspace, size_t workspace_bytes,
+    int32_t* err_flags, void* stream);
+
+/*
+ * Gives pages of the rows which[0..n) back (one launch): their entries become
+ * -1 and their page_refs one less.  A row may be listed twice.
+ *   window == 0    the whole row; its context_lens becomes 0.
+ *   window > 0     only the pages that hold neither one of the row's first
+ *                  `sinks` tokens nor one of its last `window` tokens: what
+ *                  dsa_paged_attention with this window and these sinks will
+ *                  not read again.  context_lens stays.
+ * An entry whose page has no reference sets DSA_DEVERR_REFS; its count stays
+ * 0.  Rows out of range, or longer than the table, set DSA_DEVERR_ROW.
+ */
+dsa_status dsa_cache_free(
+    int64_t num_pages, int32_t* page_refs, int32_t* block_table,
+    int32_t bt_cols, int64_t bt_stride, int32_t* context_lens, int32_t rows,
+    int32_t page_size, const int32_t* which, int32_t n, int32_t window,
+    int32_t sinks, uint32_t flags, int32_t* err_flags, void* stream);
+
+/*
+ * Packs the pool (two launches): with L pages in use (page_refs > 0), those at
+ * or above page L move into the free pages below it, lowest to lowest, in
+ * every cache; page_refs and the tables follow, and *live_pages (device) = L.
+ * Pages L and above are free afterwards (their bytes stay).  num_pages <= 2^20.
+ *   workspace      dsa_cache_compact_workspace_bytes(num_pages) bytes, 4-byte
+ *                  aligned, contents scratch.
+ * A table entry whose page has no reference and lies above the border becomes
+ * -1 and sets DSA_DEVERR_REFS.
+ */
+size_t dsa_cache_compact_workspace_bytes(int64_t num_pages);
+
+dsa_status dsa_cache_compact(
+    void* const* caches, const int64_t* page_bytes, int32_t n_caches,
+    int64_t num_pages, int32_t* page_refs, int32_t* block_table,
+    int32_t bt_cols, int64_t bt_stride, const int32_t* context_lens,
+    int32_t rows, int32_t page_size, int32_t* live_pages, uint32_t flags,
+    void* workspace, size_t workspace_bytes, int32_t* err_flags, void* stream);
 
 /* A static, NUL-terminated description of a status code. */
 const char* dsa_status_string(dsa_status status);

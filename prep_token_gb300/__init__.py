@@ -25,12 +25,14 @@ from ._build import LIB_PATH
 
 __all__ = [
     "DsaError", "NEOX", "GPTJ", "HEAD_DIM", "DEVERR_POSITION", "DEVERR_SLOT", "DEVERR_TIMEOUT",
-    "DEVERR_INTERNAL",
+    "DEVERR_INTERNAL", "DEVERR_ROW", "DEVERR_POOL", "DEVERR_REFS",
     "FLAG_PDL", "FLAG_PIPELINE", "FLAG_DIRECT", "FLAG_PDL_EARLY_ROPE", "FLAG_CACHE_TOKEN_MAJOR",
     "FLAG_HADAMARD", "FLAG_PDL_EARLY_INDEX",
     "dsa_indexer_qk_prepare_store", "dsa_indexer_k_prepare_store", "dsa_status_string",
     "dsa_indexer_qk_prepare_store_unfused", "dsa_unfused_workspace_bytes",
     "dsa_indexer_qk_prepare_store_unfused_noalloc", "dsa_indexer_mqa_logits",
+    "dsa_cache_copy_pages", "dsa_cache_fork", "dsa_cache_free", "dsa_cache_compact",
+    "dsa_cache_fork_workspace_bytes", "dsa_cache_compact_workspace_bytes",
     "library", "cache_bytes", "cache_views",
     "PreparedCall", "prepare_qk_prepare_store", "prepare_k_prepare_store",
 ]
@@ -38,6 +40,7 @@ __all__ = [
 NEOX, GPTJ = 0, 1
 HEAD_DIM = 128
 DEVERR_POSITION, DEVERR_SLOT, DEVERR_TIMEOUT, DEVERR_INTERNAL = 1, 2, 4, 8
+DEVERR_ROW, DEVERR_POOL, DEVERR_REFS = 16, 32, 64
 FLAG_PDL, FLAG_PIPELINE, FLAG_DIRECT, FLAG_PDL_EARLY_ROPE = 1, 2, 4, 8
 FLAG_CACHE_TOKEN_MAJOR = 16
 FLAG_HADAMARD = 32
@@ -92,6 +95,21 @@ def library() -> ctypes.CDLL:
         lib.dsa_indexer_mqa_logits.argtypes = [
             P, P, P, I64, I32, P, I64, P, P, I64, I32, I32, I32, U32, P, P]
         lib.dsa_indexer_mqa_logits.restype = ctypes.c_int
+        lib.dsa_cache_copy_pages.argtypes = [P, P, I32, I64, P, P, I32, U32, P, P]
+        lib.dsa_cache_copy_pages.restype = ctypes.c_int
+        lib.dsa_cache_fork_workspace_bytes.argtypes = [I32]
+        lib.dsa_cache_fork_workspace_bytes.restype = SZ
+        lib.dsa_cache_fork.argtypes = [
+            P, P, I32, I64, P, P, I32, I64, P, I32, I32, P, P, I32, U32, P, SZ, P, P]
+        lib.dsa_cache_fork.restype = ctypes.c_int
+        lib.dsa_cache_free.argtypes = [
+            I64, P, P, I32, I64, P, I32, I32, P, I32, I32, I32, U32, P, P]
+        lib.dsa_cache_free.restype = ctypes.c_int
+        lib.dsa_cache_compact_workspace_bytes.argtypes = [I64]
+        lib.dsa_cache_compact_workspace_bytes.restype = SZ
+        lib.dsa_cache_compact.argtypes = [
+            P, P, I32, I64, P, P, I32, I64, P, I32, I32, P, U32, P, SZ, P, P]
+        lib.dsa_cache_compact.restype = ctypes.c_int
         lib.dsa_status_string.argtypes = [ctypes.c_int]
         lib.dsa_status_string.restype = ctypes.c_char_p
         lib.dsa_prep_version.argtypes = []
@@ -508,3 +526,149 @@ def dsa_indexer_mqa_logits(q_fp8, weights, index_k_cache, page_size, block_table
     if st != 0:
         raise DsaError(st, "dsa_indexer_mqa_logits")
     return logits[:, :max_context]
+
+
+# ------------------------------------------------------- pages of a paged cache
+
+def _cache_arrays(caches, num_pages: int, device):
+    """The host arrays of base pointers and page sizes of the caches of a pool."""
+    n = len(caches)
+    bases, sizes = [0] * n, [0] * n
+    for i, t in enumerate(caches):
+        if t.device != device or not t.is_contiguous():
+            raise ValueError(f"caches[{i}] must be a contiguous tensor on {device}")
+        nbytes = t.nbytes
+        if nbytes % num_pages or not nbytes:
+            raise ValueError(f"caches[{i}] is not {num_pages} pages of equal size")
+        bases[i], sizes[i] = t.data_ptr(), nbytes // num_pages
+    return (ctypes.c_void_p * n)(*bases), (ctypes.c_int64 * n)(*sizes), n
+
+
+def _pool(page_refs, block_table, context_lens):
+    """Checks a pool's tables; returns their device and the C arguments
+    (num_pages, page_refs, block_table, columns, stride, context_lens, rows)."""
+    _need(page_refs, "page_refs", torch.int32, 1)
+    dev = page_refs.device
+    _need(block_table, "block_table", torch.int32, 2, dev)
+    _need(context_lens, "context_lens", torch.int32, 1, dev)
+    rows, cols = block_table.shape
+    if context_lens.shape[0] < rows:
+        raise ValueError(f"context_lens has fewer than {rows} entries")
+    if page_refs.shape[0] < 1:
+        raise ValueError("page_refs must hold at least one page")
+    if rows > 1 and block_table.stride(0) < cols:
+        raise ValueError("block_table's rows overlap")
+    return dev, page_refs.shape[0], (page_refs.data_ptr(), block_table.data_ptr(), cols,
+                                     max(block_table.stride(0), cols), context_lens.data_ptr(),
+                                     rows)
+
+
+def _list(t, name, dev):
+    _need(t, name, torch.int32, 1, dev)
+    return t.data_ptr()
+
+
+def _scratch(workspace, need, dev):
+    """A given workspace checked, or one allocated: (keep, pointer, bytes)."""
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    if not isinstance(workspace, torch.Tensor) or workspace.device != dev \
+            or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return workspace, workspace.data_ptr(), workspace.nbytes
+
+
+def dsa_cache_copy_pages(caches, num_pages, src_pages, dst_pages, *, err_flags=None, stream=None):
+    """Copies page src_pages[i] to page dst_pages[i] of every cache (in place,
+    one launch).  caches: contiguous CUDA tensors of ``num_pages`` equal pages
+    each (a layer's index-K, K or V cache, whatever their types and page
+    sizes); src_pages, dst_pages [n] int32.  Destinations are distinct and no
+    page is both a source and a destination."""
+    _need(src_pages, "src_pages", torch.int32, 1)
+    dev = src_pages.device
+    dst = _list(dst_pages, "dst_pages", dev)
+    if dst_pages.shape[0] != src_pages.shape[0]:
+        raise ValueError("src_pages and dst_pages differ in length")
+    if int(num_pages) < 1:
+        raise ValueError("num_pages must be at least 1")
+    bases, sizes, n = _cache_arrays(caches, int(num_pages), dev)
+    with _on(dev):
+        st = library().dsa_cache_copy_pages(
+            bases, sizes, n, int(num_pages), src_pages.data_ptr(), dst, src_pages.shape[0], 0,
+            _err_ptr(err_flags, dev), _stream(stream, dev))
+    if st != 0:
+        raise DsaError(st, "dsa_cache_copy_pages")
+
+
+def dsa_cache_fork_workspace_bytes(n: int) -> int:
+    return int(library().dsa_cache_fork_workspace_bytes(int(n)))
+
+
+def dsa_cache_fork(caches, page_refs, block_table, context_lens, page_size, parents, children, *,
+                   workspace=None, err_flags=None, stream=None):
+    """Row children[i] of the block table becomes a copy of row parents[i]: it
+    shares the parent's whole pages and gets the lowest free page for a copy
+    of the parent's last, partly filled one, in every cache (in place, two
+    launches).  caches: contiguous CUDA tensors of page_refs.numel() equal
+    pages each; page_refs [pages], block_table [rows, blocks], context_lens
+    [rows], parents and children [n] int32.  Children are unused rows
+    (context_lens 0), each named once."""
+    dev, num_pages, pool = _pool(page_refs, block_table, context_lens)
+    parents_ptr, children_ptr = _list(parents, "parents", dev), _list(children, "children", dev)
+    n = parents.shape[0]
+    if children.shape[0] != n:
+        raise ValueError("parents and children differ in length")
+    bases, sizes, n_caches = _cache_arrays(caches, num_pages, dev)
+    keep, ws, ws_bytes = _scratch(workspace, 8 * n, dev)
+    with _on(dev):
+        st = library().dsa_cache_fork(
+            bases, sizes, n_caches, num_pages, *pool, int(page_size), parents_ptr, children_ptr, n,
+            0, ws, ws_bytes, _err_ptr(err_flags, dev), _stream(stream, dev))
+    if st != 0:
+        raise DsaError(st, "dsa_cache_fork")
+
+
+def dsa_cache_free(page_refs, block_table, context_lens, page_size, rows, *, window=0, sinks=0,
+                   err_flags=None, stream=None):
+    """Gives pages of the listed rows back (in place, one launch): with
+    ``window`` 0 all of a row's pages, and its context length becomes 0; with
+    a window the pages that hold neither one of the row's first ``sinks``
+    tokens nor one of its last ``window`` ones.  rows [n] int32; a row may be
+    listed twice."""
+    dev, num_pages, pool = _pool(page_refs, block_table, context_lens)
+    rows_ptr = _list(rows, "rows", dev)
+    with _on(dev):
+        st = library().dsa_cache_free(
+            num_pages, *pool, int(page_size), rows_ptr, rows.shape[0], int(window), int(sinks), 0,
+            _err_ptr(err_flags, dev), _stream(stream, dev))
+    if st != 0:
+        raise DsaError(st, "dsa_cache_free")
+
+
+def dsa_cache_compact_workspace_bytes(num_pages: int) -> int:
+    return int(library().dsa_cache_compact_workspace_bytes(int(num_pages)))
+
+
+def dsa_cache_compact(caches, page_refs, block_table, context_lens, page_size, *, live_pages=None,
+                      workspace=None, err_flags=None, stream=None):
+    """Packs the pool (in place, two launches): the pages in use move into the
+    lowest ones, in every cache, and page_refs and the block table follow.
+    Returns live_pages, an int32 [1] CUDA tensor with the number of pages in
+    use; the pages from there on are free."""
+    dev, num_pages, pool = _pool(page_refs, block_table, context_lens)
+    bases, sizes, n_caches = _cache_arrays(caches, num_pages, dev)
+    if live_pages is None:
+        live_pages = torch.empty(1, dtype=torch.int32, device=dev)
+    _list(live_pages, "live_pages", dev)
+    if live_pages.numel() < 1:
+        raise ValueError("live_pages must hold one int32")
+    lib = library()
+    keep, ws, ws_bytes = _scratch(
+        workspace, lib.dsa_cache_compact_workspace_bytes(num_pages), dev)
+    with _on(dev):
+        st = lib.dsa_cache_compact(
+            bases, sizes, n_caches, num_pages, *pool, int(page_size), live_pages.data_ptr(), 0, ws,
+            ws_bytes, _err_ptr(err_flags, dev), _stream(stream, dev))
+    if st != 0:
+        raise DsaError(st, "dsa_cache_compact")
+    return live_pages
