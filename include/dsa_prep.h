@@ -49,7 +49,8 @@
  *   - All work is enqueued on `stream` (a cudaStream_t; NULL = the legacy
  *     default stream).  No call synchronises the host, so every call can be
  *     captured into a CUDA graph.  One kernel launch per call (the unfused
- *     comparison chain: four; dsa_cache_fork and dsa_cache_compact: two).  The first call
+ *     comparison chain: four; dsa_cache_fork and dsa_cache_compact: two;
+ *     dsa_paged_attention: one or two).  The first call
  *     on a device raises the kernel's dynamic shared-memory limit there (a
  *     per-device, once-only setting); make it before capturing a graph.
  *   - Host-side checks: a bad argument returns a status other than DSA_OK and
@@ -88,6 +89,8 @@ typedef enum {
 } dsa_status;
 
 typedef enum { DSA_ROPE_NEOX = 0, DSA_ROPE_GPTJ = 1 } dsa_rope_style;
+
+typedef enum { DSA_DTYPE_BF16 = 0, DSA_DTYPE_FP16 = 1 } dsa_dtype;
 
 #define DSA_HEAD_DIM 128
 
@@ -327,6 +330,71 @@ dsa_status dsa_indexer_mqa_logits(
     const int32_t* block_table, int64_t bt_stride, const int32_t* context_lens,
     float* logits, int64_t logits_stride, int32_t max_context,
     int32_t T, int32_t H, uint32_t flags, int32_t* err_flags, void* stream);
+
+/*
+ * Attention of new tokens over a paged K/V cache: the dense attention of a
+ * DSA model's layers while a context is short of the indexer's top-k, and of
+ * sliding-window layers.  A batch of B sequences mixes chunks of prompts and
+ * single tokens.  With G = H / Hkv, query i of sequence b (row query_start[b]
+ * + i of q, n_b of them) is the token at
+ *   pos = context_lens[b] - n_b + i,
+ * its keys and values already in the cache, and head h of it sees kv head
+ * h / G:
+ *   s_j = scale * q . k_j,  out = sum_j e^(s_j) v_j / sum_j e^(s_j),
+ *   lse = log(sum_j e^(s_j))
+ * over the keys j <= pos with (window == 0 or j > pos - window or j < sinks).
+ * A row that sees no key gets out 0 and lse -inf.
+ *
+ *   q              bf16 or fp16 (dtype) [T, H, head_dim], strides q_stride_t,
+ *                  q_stride_h.
+ *   k_cache,       the same type, [num_pages, page_size, Hkv, head_dim] with
+ *   v_cache        any positive strides for pages, tokens and heads (K and V
+ *                  may be slices of one buffer, heads may come before tokens).
+ *   block_table    int32 [B, bt_stride], bt_stride >= ceil(max_context /
+ *                  page_size): entry j holds keys [j * page_size, (j + 1) *
+ *                  page_size).  Only entries with a visible key are read.
+ *   query_start    int32 [B + 1], non-decreasing, query_start[B] <= T.  Rows
+ *                  of q behind the last sequence are left out: their out and
+ *                  lse are not written.  Empty sequences are allowed.
+ *   context_lens   int32 [B], keys of each sequence, the new tokens included;
+ *                  at most max_context (a longer one is clamped).
+ *   window, sinks  0: the whole context.  sinks counts only with a window.
+ *   out            dtype [T, H, head_dim], strides out_stride_t, out_stride_h.
+ *   lse            fp32 [T, H] contiguous, natural logarithm; may be NULL.
+ *   workspace      dsa_paged_attention_workspace_bytes(T, B, H, Hkv, head_dim,
+ *                  max_context) bytes, 16-byte aligned (0 bytes: may be
+ *                  NULL), contents scratch; calls that may run at the same
+ *                  time need one each.
+ *   head_dim 64 or 128; G <= 128; page_size 8, 16, 32 or a multiple of 64;
+ *   scale finite and > 0; flags may hold DSA_FLAG_PDL.  q, k_cache, v_cache
+ *   and out are 16-byte aligned and their strides multiples of 8; the
+ *   innermost dimension is contiguous.
+ * Scores, sums and the accumulation are fp32; the probabilities are rounded to
+ * dtype for their product with the values.  One launch, or two where the keys
+ * are split over CTAs; results do not depend on the order in which CTAs run.
+ * A visible key whose block-table entry is outside [0, num_pages) sets
+ * DSA_DEVERR_SLOT and makes the rows that see it NaN.  Cache contents that no
+ * query sees (behind a context, before a window) may be anything, NaN
+ * included; a non-finite value or key that some query sees makes out
+ * unspecified for the queries of its sequence.
+ */
+size_t dsa_paged_attention_workspace_bytes(int32_t T, int32_t B, int32_t H,
+                                           int32_t Hkv, int32_t head_dim,
+                                           int32_t max_context);
+
+dsa_status dsa_paged_attention(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h,
+    const void* k_cache, const void* v_cache,
+    int64_t k_stride_page, int64_t k_stride_token, int64_t k_stride_head,
+    int64_t v_stride_page, int64_t v_stride_token, int64_t v_stride_head,
+    int64_t num_pages, int32_t page_size,
+    const int32_t* block_table, int64_t bt_stride, const int32_t* query_start,
+    const int32_t* context_lens, int32_t max_context, float scale,
+    int32_t window, int32_t sinks,
+    void* out, int64_t out_stride_t, int64_t out_stride_h, float* lse,
+    int32_t T, int32_t B, int32_t H, int32_t Hkv, int32_t head_dim,
+    int32_t dtype, uint32_t flags, void* workspace, size_t workspace_bytes,
+    int32_t* err_flags, void* stream);
 
 /*
  * Upkeep of a paged cache's pages: copy, fork, free, compact.

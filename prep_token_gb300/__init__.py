@@ -31,6 +31,7 @@ __all__ = [
     "dsa_indexer_qk_prepare_store", "dsa_indexer_k_prepare_store", "dsa_status_string",
     "dsa_indexer_qk_prepare_store_unfused", "dsa_unfused_workspace_bytes",
     "dsa_indexer_qk_prepare_store_unfused_noalloc", "dsa_indexer_mqa_logits",
+    "dsa_paged_attention", "dsa_paged_attention_workspace_bytes",
     "dsa_cache_copy_pages", "dsa_cache_fork", "dsa_cache_free", "dsa_cache_compact",
     "dsa_cache_fork_workspace_bytes", "dsa_cache_compact_workspace_bytes",
     "library", "cache_bytes", "cache_views",
@@ -95,6 +96,12 @@ def library() -> ctypes.CDLL:
         lib.dsa_indexer_mqa_logits.argtypes = [
             P, P, P, I64, I32, P, I64, P, P, I64, I32, I32, I32, U32, P, P]
         lib.dsa_indexer_mqa_logits.restype = ctypes.c_int
+        lib.dsa_paged_attention_workspace_bytes.argtypes = [I32] * 6
+        lib.dsa_paged_attention_workspace_bytes.restype = SZ
+        lib.dsa_paged_attention.argtypes = [
+            P, I64, I64, P, P, I64, I64, I64, I64, I64, I64, I64, I32, P, I64, P, P, I32, F32, I32,
+            I32, P, I64, I64, P, I32, I32, I32, I32, I32, I32, U32, P, SZ, P, P]
+        lib.dsa_paged_attention.restype = ctypes.c_int
         lib.dsa_cache_copy_pages.argtypes = [P, P, I32, I64, P, P, I32, U32, P, P]
         lib.dsa_cache_copy_pages.restype = ctypes.c_int
         lib.dsa_cache_fork_workspace_bytes.argtypes = [I32]
@@ -526,6 +533,86 @@ def dsa_indexer_mqa_logits(q_fp8, weights, index_k_cache, page_size, block_table
     if st != 0:
         raise DsaError(st, "dsa_indexer_mqa_logits")
     return logits[:, :max_context]
+
+
+# ------------------------------------------------------- attention over a paged cache
+
+_ATTENTION_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def dsa_paged_attention_workspace_bytes(T: int, B: int, H: int, Hkv: int, head_dim: int,
+                                        max_context: int) -> int:
+    """Workspace that dsa_paged_attention needs for these sizes (0: none)."""
+    return int(library().dsa_paged_attention_workspace_bytes(
+        int(T), int(B), int(H), int(Hkv), int(head_dim), int(max_context)))
+
+
+def dsa_paged_attention(q, k_cache, v_cache, block_table, query_start, context_lens, max_context, *,
+                        scale=None, window=0, sinks=0, out=None, lse=None, workspace=None,
+                        err_flags=None, pdl=False, stream=None):
+    """Attention of new tokens over a paged K/V cache on the tensor cores.
+
+    q [T, H, D] bf16 or fp16 (D 64 or 128); k_cache, v_cache
+    [num_pages, page_size, Hkv, D] views of any strides; block_table [B, n]
+    int32 with n >= ceil(max_context / page_size); query_start [B + 1] int32:
+    rows query_start[b] .. query_start[b + 1] of q are the last tokens of
+    sequence b, which has context_lens[b] (int32) keys in the cache, theirs
+    included.  Each sees the keys up to itself or, with a ``window``, the last
+    ``window`` of them (itself counted) and the first ``sinks`` ones.
+    ``scale`` defaults to D ** -0.5.  ``workspace``: a CUDA uint8 tensor of at
+    least dsa_paged_attention_workspace_bytes(...) bytes, allocated here when
+    not given.  Returns (out [T, H, D], lse [T, H] fp32); rows that belong to
+    no sequence are left as they are."""
+    _need(q, "q", (torch.bfloat16, torch.float16), 3)
+    dev = q.device
+    _need(k_cache, "k_cache", q.dtype, 4, dev)
+    _need(v_cache, "v_cache", q.dtype, 4, dev)
+    _need(block_table, "block_table", torch.int32, 2, dev)
+    _need(query_start, "query_start", torch.int32, 1, dev)
+    _need(context_lens, "context_lens", torch.int32, 1, dev)
+    T, H, D = q.shape
+    num_pages, page_size, Hkv, k_dim = k_cache.shape
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache differ in shape")
+    if k_dim != D:
+        raise ValueError(f"q has head_dim {D}, the caches {k_dim}")
+    if Hkv < 1 or H % Hkv:
+        raise ValueError("H must be a multiple of the caches' heads")
+    B = query_start.shape[0] - 1
+    max_context = int(max_context)
+    if B < 0:
+        raise ValueError("query_start must hold B + 1 entries")
+    if block_table.shape[0] < B or block_table.shape[1] * page_size < max_context:
+        raise ValueError("block_table must be [B, >= ceil(max_context / page_size)]")
+    if context_lens.shape[0] < B:
+        raise ValueError(f"context_lens has fewer than {B} entries")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=q.dtype, device=dev)
+    _need(out, "out", q.dtype, 3, dev)
+    if out.shape[0] < T or out.shape[1:] != q.shape[1:]:
+        raise ValueError("out must be [T, H, D]")
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    _need(lse, "lse", torch.float32, 2, dev)
+    if not lse.is_contiguous() or lse.shape[0] < T or lse.shape[1] != H:
+        raise ValueError("lse must be contiguous [T, H]")
+    lib = library()
+    need = lib.dsa_paged_attention_workspace_bytes(T, B, H, Hkv, D, max_context)
+    keep, ws, ws_bytes = _scratch(workspace, need, dev) if need or workspace is not None \
+        else (None, None, 0)
+    with _on(dev):
+        st = lib.dsa_paged_attention(
+            q.data_ptr(), q.stride(0), q.stride(1), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_cache.stride(0), k_cache.stride(1), k_cache.stride(2), v_cache.stride(0),
+            v_cache.stride(1), v_cache.stride(2), num_pages, page_size, block_table.data_ptr(),
+            max(block_table.stride(0), block_table.shape[1]), query_start.data_ptr(),
+            context_lens.data_ptr(), max_context, D ** -0.5 if scale is None else float(scale),
+            int(window), int(sinks), out.data_ptr(), out.stride(0), out.stride(1), lse.data_ptr(),
+            T, B, H, Hkv, D, _ATTENTION_DTYPES[q.dtype], FLAG_PDL if pdl else 0, ws, ws_bytes,
+            _err_ptr(err_flags, dev), _stream(stream, dev))
+    if st != 0:
+        raise DsaError(st, "dsa_paged_attention")
+    return out, lse
 
 
 # ------------------------------------------------------- pages of a paged cache

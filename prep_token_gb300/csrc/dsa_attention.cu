@@ -1,0 +1,1069 @@
+// Attention of new tokens over a paged K/V cache on the 5th-generation tensor
+// cores: a chunk of a prompt, single tokens, or both in one call, over the
+// whole context or a sliding window with the first tokens kept visible.
+//
+// With G = H / Hkv query heads per kv head, query i of sequence b is the token
+// at pos = context_lens[b] - n_b + i, and for each of its heads
+//   s_j = scale * q . k_j,  out = sum_j e^(s_j) v_j / sum_j e^(s_j),
+//   lse = log(sum_j e^(s_j)),
+// over the visible keys: j <= pos and (no window, or j > pos - window, or
+// j < sinks).  The keys are taken in blocks of 128 with the running maximum m
+// and sum l of a softmax, so S never leaves the chip:
+//   p_j = 2^(c s_j - c m) with c = scale * log2(e);  O += P V;  l += sum p.
+//
+// A work item is 128 rows (floor(128 / G) tokens, their G heads of one kv
+// head packed token by token) of one sequence; a single token fills G of them.
+//   * warp 0 loads: the query tile, then per key block the 16 KB units of K
+//     (128 keys x 64 dims) and V (128 * 64 / D keys x D dims) into one ring,
+//     by 4-D TMA boxes of min(page, 64) keys with the 128-byte swizzle; lane l
+//     looks up and issues box l of the block.
+//   * warp 1 (one lane) issues S = Q K^T (M = N = 128, both operands in shared
+//     memory) and O += P V (A = P in TMEM over the columns of S, B = V in
+//     shared memory, read MN-major), and commits them to the mbarriers.
+//   * warps 2..5 own one row per thread: S from TMEM, the masks (in blocks at
+//     an edge only), the maximum, the exponentials, P back to TMEM.  O is
+//     rescaled only when a maximum has grown by more than 2^8: until then P
+//     may exceed 1, at most by that factor, which fp32 and both 16-bit types
+//     hold.  P is rounded to the values' type for the matrix product (at most
+//     2^-8 of it in bf16, 2^-11 in fp16); the sum l takes it unrounded.  In
+//     fp16 P, O and l carry a factor of 2^7, so that a p down to 2^-21 keeps
+//     all its bits and the largest one, 2^(8 + 7), still fits.
+// Two CTAs share an SM, so one's softmax runs beside the other's products.
+//
+// Bound: a chunk by the tensor cores (4 D flops per row and visible key),
+// single tokens by the cache's bytes.  With few items the key blocks of all
+// items are laid end to end and cut into equal shares, one per CTA; an item
+// that a cut divides leaves partial (O, m, l) in the workspace, which a second
+// kernel joins in a fixed order.
+//
+// Every wait is bounded in time; TMEM is always released before exit.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "dsa_common.cuh"
+#include "dsa_prep.h"
+
+namespace {
+
+using namespace dsa_dev;
+
+constexpr int kRows = 128;          // MMA M: rows of a query tile
+constexpr int kKeys = 128;          // keys of a block
+constexpr int kUnitBytes = 16384;   // of the K/V ring
+constexpr int kAThreads = 6 * 32;   // loads, MMA, 4 softmax warps
+constexpr int kTmemCols = 256;      // S / P: 128, O: D
+constexpr int kSplitCtas = 304;     // two CTAs on each of 152 SMs
+constexpr float kRescaleLog2 = 8.0f;
+constexpr float kLn2 = 0.693147180559945309f;
+
+struct AParams {
+  const int* block_table;
+  const int* query_start;
+  const int* context_lens;
+  void* out;
+  float* lse;
+  long long bt_stride, out_stride_t, out_stride_h;
+  int num_pages, page, box;  // box: keys per TMA box, min(page, 64)
+  int T, B, Hkv, G, tile_tokens;
+  int max_context;
+  int window, sinks;  // window 0: none
+  float c;            // scale * log2(e)
+  int split;          // 1: equal shares of the key blocks; 0: one item per CTA
+  int4* meta;         // split: [kSplitCtas] the item that CTA leaves to later ones
+  float2* ml;         // split: [2 * kSplitCtas][kRows] (log2 of the scale, l) of a part
+  float* part;        // split: [2 * kSplitCtas][kRows][D] O of a part
+  int* err;
+};
+
+// ---------------------------------------------------------------- PTX wrappers
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                            int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                            int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// Shared-memory matrix descriptor of 128-byte-swizzled rows: 8-row groups of
+// 1024 bytes (the stride offset).  `lead` is the distance of 64-element panels
+// of an MN-major operand (unused K-major).
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t smem_addr, uint32_t lead) {
+  uint64_t d = static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((lead >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;  // version
+  d |= static_cast<uint64_t>(2) << 61;  // 128-byte swizzle
+  return d;
+}
+
+// Instruction descriptor: D fp32, A and B fp16 or bf16, A K-major.
+__host__ __device__ constexpr uint32_t mma_idesc(bool bf16, bool b_mn_major, int n) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn_major ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+               ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Nothing may use values that a tcgen05.ld brings before its wait: an empty
+// statement that seems to change them keeps the compiler to that order.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(float (&v)[N]) {
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+
+// 32 consecutive fp32 columns of this warp's 32 TMEM lanes; the values may be
+// used after tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+      " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr) : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0],"
+      " {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+        "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+        "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+        "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if (BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// ---------------------------------------------------------------- work items
+
+// One query tile of a sequence and the key blocks that some row of it sees.
+struct Tile {
+  int token0, tokens;  // in q; tokens of the tile
+  int pos0;            // position of its first token
+  int hi, lo;          // keys seen by some row: [lo, hi) and [0, min(sinks, hi))
+  int sink_blocks, main_block, blocks;
+
+  __device__ __forceinline__ int block(int k) const {  // the k-th block's first key / 128
+    return k < sink_blocks ? k : main_block + k - sink_blocks;
+  }
+};
+
+__device__ __forceinline__ Tile make_tile(const AParams& p, int q0, int n, int ctx, int t) {
+  Tile r;
+  const int i0 = t * p.tile_tokens;
+  r.token0 = q0 + i0;
+  r.tokens = min(p.tile_tokens, n - i0);
+  r.pos0 = ctx - n + i0;
+  r.hi = max(0, r.pos0 + r.tokens);
+  r.lo = p.window ? max(0, r.pos0 - p.window + 1) : 0;
+  r.main_block = r.lo / kKeys;
+  r.sink_blocks = min((min(p.sinks, r.hi) + kKeys - 1) / kKeys, r.main_block);
+  // a tile that sees nothing still has one block, all masked: its rows are 0
+  r.blocks = max(1, r.sink_blocks + (r.hi + kKeys - 1) / kKeys - r.main_block);
+  return r;
+}
+
+struct Seq {
+  int q0, n, ctx, tiles;
+};
+
+// Sequence b, its numbers held to the tensors' sizes.
+__device__ __forceinline__ Seq load_seq(const AParams& p, int b) {
+  Seq s;
+  s.q0 = max(0, min(__ldg(p.query_start + b), p.T));
+  s.n = max(0, min(__ldg(p.query_start + b + 1), p.T) - s.q0);
+  s.ctx = max(0, min(__ldg(p.context_lens + b), p.max_context));
+  s.tiles = (s.n + p.tile_tokens - 1) / p.tile_tokens;
+  return s;
+}
+
+// Key blocks of all tiles of a sequence, for one kv head.  A whole warp calls
+// it with each lane's own sequence.
+__device__ __forceinline__ long long seq_blocks(const AParams& p, const Seq& s) {
+  const int lane = threadIdx.x & 31;
+  long long mine = 0;
+  const bool few = s.tiles <= 2;
+  if (few)
+    for (int t = 0; t < s.tiles; ++t) mine += make_tile(p, s.q0, s.n, s.ctx, t).blocks;
+  for (unsigned todo = __ballot_sync(kFull, !few); todo; todo &= todo - 1) {
+    const int src = __ffs(todo) - 1;
+    const int n = __shfl_sync(kFull, s.n, src), ctx = __shfl_sync(kFull, s.ctx, src);
+    const int tiles = __shfl_sync(kFull, s.tiles, src);
+    long long sum = 0;
+    for (int t = lane; t < tiles; t += 32) sum += make_tile(p, 0, n, ctx, t).blocks;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if (lane == src) mine = sum;
+  }
+  return mine;
+}
+
+__device__ __forceinline__ long long warp_inclusive(long long v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(kFull, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
+// Where a CTA is in its work: the tile, and the key blocks [begin, end) of it.
+struct Cursor {
+  int b, h, t;
+  Seq s;
+  Tile tile;
+  int begin, end;
+  long long left;  // key blocks after this segment (split) or 0
+};
+
+__device__ __forceinline__ void take_tile(const AParams& p, Cursor& c, int begin, long long budget) {
+  c.tile = make_tile(p, c.s.q0, c.s.n, c.s.ctx, c.t);
+  c.begin = begin;
+  const long long most = begin + budget;
+  c.end = most < c.tile.blocks ? static_cast<int>(most) : c.tile.blocks;
+  c.left = budget - (c.end - c.begin);
+}
+
+// The next tile, kv head or sequence with tokens.  Only called when blocks are left.
+__device__ __forceinline__ bool next_segment(const AParams& p, Cursor& c) {
+  if (c.left <= 0) return false;
+  if (++c.t == c.s.tiles) {
+    c.t = 0;
+    if (++c.h == p.Hkv) {
+      c.h = 0;
+      do {
+        if (++c.b >= p.B) return false;
+        c.s = load_seq(p, c.b);
+      } while (c.s.tiles == 0);
+    }
+  }
+  take_tile(p, c, 0, c.left);
+  return true;
+}
+
+// Split work: key blocks in the order sequence, kv head, tile.  CTA g of
+// `ctas` takes [total * g / ctas, total * (g + 1) / ctas).
+struct Share {
+  long long total, begin, end;
+  int ctas;
+};
+
+__device__ __forceinline__ Share my_share(const AParams& p) {
+  const int lane = threadIdx.x & 31;
+  long long sum = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    Seq s = {0, 0, 0, 0};
+    if (b0 + lane < p.B) s = load_seq(p, b0 + lane);
+    sum += seq_blocks(p, s);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  Share r;
+  r.total = sum * p.Hkv;
+  r.ctas = r.total < static_cast<long long>(gridDim.x) ? static_cast<int>(r.total)
+                                                       : static_cast<int>(gridDim.x);
+  const long long g = blockIdx.x;
+  r.begin = g < r.ctas ? r.total * g / r.ctas : 0;
+  r.end = g < r.ctas ? r.total * (g + 1) / r.ctas : 0;
+  return r;
+}
+
+// The CTA's first segment.  A whole warp calls it; every lane gets the same.
+__device__ __forceinline__ bool first_segment(const AParams& p, Cursor& c, Share& share) {
+  const int lane = threadIdx.x & 31;
+  long long want = blockIdx.x;  // an item, or a key block
+  if (p.split) {
+    share = my_share(p);
+    if (share.begin >= share.end) return false;
+    want = share.begin;
+  }
+  long long before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    Seq s = {0, 0, 0, 0};
+    if (b0 + lane < p.B) s = load_seq(p, b0 + lane);
+    const long long per_head = p.split ? seq_blocks(p, s) : s.tiles;
+    const long long upto = before + warp_inclusive(per_head * p.Hkv);
+    const unsigned past = __ballot_sync(kFull, upto > want);
+    if (past) {
+      const int src = __ffs(past) - 1;
+      const long long one = __shfl_sync(kFull, per_head, src);
+      const long long rest = want - (__shfl_sync(kFull, upto, src) - one * p.Hkv);
+      c.b = b0 + src;
+      c.s = load_seq(p, c.b);
+      c.h = static_cast<int>(rest / one);
+      const int r = static_cast<int>(rest % one);
+      if (!p.split) {
+        c.t = c.s.tiles - 1 - r;  // the last tiles of a chunk see the most keys: first
+        take_tile(p, c, 0, 1LL << 40);
+        c.left = 0;
+        return true;
+      }
+      int seen = 0;  // key blocks of the tiles before
+      for (int t0 = 0;; t0 += 32) {
+        const int t = t0 + lane;
+        const int n = t < c.s.tiles ? make_tile(p, 0, c.s.n, c.s.ctx, t).blocks : 0;
+        const int up = seen + static_cast<int>(warp_inclusive(n));
+        const unsigned over = __ballot_sync(kFull, up > r);
+        if (over) {
+          const int at = __ffs(over) - 1;
+          c.t = t0 + at;
+          take_tile(p, c, r - __shfl_sync(kFull, up - n, at), share.end - share.begin);
+          return true;
+        }
+        seen = __shfl_sync(kFull, up, 31);
+      }
+    }
+    before = __shfl_sync(kFull, upto, 31);
+  }
+  return false;
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int D>
+struct ASmem {
+  static constexpr int kPanels = D / 64;                    // 128-byte panels of a row
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr int kStages = (114688 - kQBytes) / kUnitBytes;  // 5 or 6 units
+  static constexpr int kVKeys = kKeys / kPanels;            // keys of a V unit
+  static constexpr int kOffRing = kQBytes;
+  static constexpr int kOffBar = kOffRing + kStages * kUnitBytes;
+  // barriers: full[S], empty[S], qfull, qempty, sfull, pready, ofull, drain
+  static constexpr int kBars = 2 * kStages + 6;
+  static constexpr int kOffTmem = kOffBar + 8 * kBars;
+  static constexpr int kOffAbort = kOffTmem + 4;
+  static constexpr int kBytes = kOffAbort + 4;
+};
+
+// The shared-memory rows of the keys of box l of a block, `rows` of 128 bytes
+// in each of `panels` panels, set to `word` by the whole warp.
+__device__ __forceinline__ void fill_rows(uint32_t at, int rows, uint32_t word) {
+  for (int i = threadIdx.x & 31; i < rows * 8; i += 32)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + 16 * i), "r"(word)
+                 : "memory");
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kAThreads, 2)
+    dsa_paged_attention_kernel(const __grid_constant__ CUtensorMap tq,
+                               const __grid_constant__ CUtensorMap tk,
+                               const __grid_constant__ CUtensorMap tv, const AParams p) {
+  using L = ASmem<D>;
+  constexpr int S = L::kStages;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023u) {  // the swizzled tiles need this alignment
+    if (threadIdx.x == 0 && p.err) atomicOr(p.err, DSA_DEVERR_INTERNAL);
+    return;
+  }
+  const uint32_t bar0 = sbase + L::kOffBar;
+  auto full = [&](int s) { return bar0 + 8 * s; };
+  auto empty = [&](int s) { return bar0 + 8 * (S + s); };
+  const uint32_t qfull = bar0 + 8 * (2 * S), qempty = bar0 + 8 * (2 * S + 1);
+  const uint32_t sfull = bar0 + 8 * (2 * S + 2), pready = bar0 + 8 * (2 * S + 3);
+  const uint32_t ofull = bar0 + 8 * (2 * S + 4), drain = bar0 + 8 * (2 * S + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffAbort);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(qfull, 1);
+    mbar_init(qempty, 1);
+    mbar_init(sfull, 1);
+    mbar_init(pready, 4);  // the softmax warps
+    mbar_init(ofull, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 ::"r"(sbase + L::kOffTmem), "n"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kOffTmem);
+  const uint32_t tmem_o = tmem + kKeys;
+
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  auto give_up = [&]() {  // a wait ran out of time
+    *abort_flag = 1;
+    if (p.err) atomicOr(p.err, DSA_DEVERR_TIMEOUT);
+  };
+
+  Cursor c;
+  Share share = {0, 0, 0, 0};
+  bool more = first_segment(p, c, share);
+  if (p.split && threadIdx.x == 64) p.meta[blockIdx.x].x = -1;
+
+  if (warp == 0) {
+    // ------------------------------------------------ loads
+    const int boxes = kKeys / p.box;
+    const uint32_t box_bytes = static_cast<uint32_t>(p.box) * 128u;  // of one panel
+    int unit = 0, seg = 0;
+    bool ok = true;
+    // waits until the ring's next unit may be written
+    auto acquire = [&]() {
+      const int s = unit % S;
+      ok = ok && (unit < S || mbar_wait(empty(s), ((unit / S) & 1) ^ 1, abort_flag));
+      ok = __all_sync(kFull, ok);
+      return s;
+    };
+    for (; more && ok; more = next_segment(p, c), ++seg) {
+      const Tile& tile = c.tile;
+      // box l of a block: its page, -1 if no row sees any of its keys, -2 if
+      // the table names no page of the pool for it
+      const int* table = p.block_table + c.b * p.bt_stride;
+      auto lookup = [&](int k) {
+        const int key = tile.block(k) * kKeys + lane * p.box;
+        if (lane >= boxes || key >= tile.hi || (key + p.box <= tile.lo && key >= p.sinks)) return -1;
+        const int page = __ldg(table + key / p.page);
+        return page >= 0 && page < p.num_pages ? page : -2;
+      };
+      int page = lookup(c.begin);
+      if (seg > 0) ok = __all_sync(kFull, mbar_wait(qempty, (seg & 1) ^ 1, abort_flag));
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(qfull, L::kPanels * p.G * p.tile_tokens * 128);
+        for (int pn = 0; pn < L::kPanels; ++pn)
+          tma_load_3d(sbase + pn * kRows * 128, &tq, pn * 64, c.h * p.G, tile.token0, qfull);
+      }
+      for (int k = c.begin; k < c.end && ok; ++k) {
+        const int in_page = (tile.block(k) * kKeys + lane * p.box) % p.page;
+        const int next = k + 1 < c.end ? lookup(k + 1) : -1;
+        const unsigned loaded = __ballot_sync(kFull, page >= 0);
+        const unsigned bad = __ballot_sync(kFull, page == -2);
+        const unsigned gone = ~loaded & (boxes == 32 ? kFull : (1u << boxes) - 1u);
+        if (bad && lane == 0 && p.err) atomicOr(p.err, DSA_DEVERR_SLOT);
+        for (int pn = 0; pn < L::kPanels; ++pn, ++unit) {  // K: 64 dims of all 128 keys
+          const int s = acquire();
+          if (!ok) break;
+          const uint32_t at = sbase + L::kOffRing + s * kUnitBytes;
+          if (bad && pn == 0) {  // NaN keys, so the rows that see them become NaN
+            for (unsigned m = bad; m; m &= m - 1)
+              fill_rows(at + (__ffs(m) - 1) * box_bytes, p.box, 0x7fff7fffu);
+            fence_async_shared();
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive_expect_tx(full(s), __popc(loaded) * box_bytes);
+          __syncwarp();
+          if (page >= 0)
+            tma_load_4d(at + lane * box_bytes, &tk, pn * 64, in_page, c.h, page, full(s));
+        }
+        for (int u = 0; u < L::kPanels && ok; ++u, ++unit) {  // V: all dims of kVKeys keys
+          const int s = acquire();
+          if (!ok) break;
+          const uint32_t at = sbase + L::kOffRing + s * kUnitBytes;
+          const int per = L::kVKeys / p.box;  // boxes of the unit
+          const unsigned here = (per == 32 ? kFull : (1u << per) - 1u) << (u * per);
+          if (gone & here) {  // P is 0 there, and 0 * V must not be NaN
+            for (unsigned m = gone & here; m; m &= m - 1)
+              for (int pn = 0; pn < L::kPanels; ++pn)
+                fill_rows(at + pn * L::kVKeys * 128 + (__ffs(m) - 1 - u * per) * box_bytes, p.box, 0u);
+            fence_async_shared();
+            __syncwarp();
+          }
+          if (lane == 0)
+            mbar_arrive_expect_tx(full(s), L::kPanels * __popc(loaded & here) * box_bytes);
+          __syncwarp();
+          if (page >= 0 && lane / per == u)
+            for (int pn = 0; pn < L::kPanels; ++pn)
+              tma_load_4d(at + pn * L::kVKeys * 128 + (lane - u * per) * box_bytes, &tv, pn * 64,
+                          in_page, c.h, page, full(s));
+        }
+        page = next;
+      }
+    }
+    if (!ok && lane == 0) give_up();
+    // stay until every load issued has landed
+    volatile int never = 0;
+    for (int d = (unit > S ? unit - S : 0); d < unit; ++d)
+      mbar_wait(full(d % S), (d / S) & 1, &never);
+    if (seg > 0) mbar_wait(qfull, (seg - 1) & 1, &never);
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer
+    constexpr uint32_t idesc_s = mma_idesc(BF16, false, kKeys);
+    constexpr uint32_t idesc_o = mma_idesc(BF16, true, D);
+    int unit = 0, seg = 0, blk = 0;
+    bool ok = true;
+    for (; more && ok; more = next_segment(p, c), ++seg) {
+      if (lane == 0) {
+        ok = mbar_wait(qfull, seg & 1, abort_flag);
+        for (int k = c.begin; k < c.end && ok; ++k, ++blk) {
+          for (int pn = 0; pn < L::kPanels && ok; ++pn, ++unit) {
+            const int s = unit % S;
+            ok = mbar_wait(full(s), (unit / S) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t a = sw128_desc(sbase + pn * kRows * 128, 0);
+            const uint64_t b = sw128_desc(sbase + L::kOffRing + s * kUnitBytes, 0);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_ss(tmem, a + 2 * ks, b + 2 * ks, idesc_s, pn + ks > 0 ? 1u : 0u);
+            mma_commit(empty(s));
+          }
+          if (!ok) break;
+          mma_commit(sfull);
+          if (k + 1 == c.end) mma_commit(qempty);
+          ok = mbar_wait(pready, blk & 1, abort_flag);
+          for (int u = 0; u < L::kPanels && ok; ++u, ++unit) {
+            const int s = unit % S;
+            ok = mbar_wait(full(s), (unit / S) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t b = sw128_desc(sbase + L::kOffRing + s * kUnitBytes, L::kVKeys * 128);
+#pragma unroll
+            for (int ks = 0; ks < L::kVKeys / 16; ++ks)
+              mma_ts(tmem_o, tmem + (u * L::kVKeys + ks * 16) / 2, b + ks * (2048 >> 4), idesc_o,
+                     (k > c.begin || u + ks > 0) ? 1u : 0u);
+            mma_commit(empty(s));
+          }
+        }
+        if (ok) mma_commit(ofull);
+      }
+      ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
+    }
+    if (lane == 0) {
+      if (!ok) give_up();
+      // every MMA issued must finish before TMEM is released
+      mma_commit(drain);
+      volatile int never = 0;
+      mbar_wait(drain, 0, &never);
+    }
+  } else {
+    // ------------------------------------------------ softmax (warps 2..5)
+    const int sub = warp & 3;           // the TMEM lanes this warp may touch
+    const int row = 32 * sub + lane;    // of the tile
+    const uint32_t t_s = tmem + (static_cast<uint32_t>(32 * sub) << 16);
+    const uint32_t t_o = tmem_o + (static_cast<uint32_t>(32 * sub) << 16);
+    // what the exponents are taken against, in powers of two
+    auto reference = [&](float m) { return (m == -INFINITY ? 0.0f : m * p.c) - (BF16 ? 0.0f : 7.0f); };
+    const int tok = row / p.G, head = row - tok * p.G;
+    int seg = 0, blk = 0;
+    bool ok = true;
+    for (; more && ok; more = next_segment(p, c), ++seg) {
+      const Tile& tile = c.tile;
+      const bool mine = tok < tile.tokens;                 // this row exists
+      const bool busy = 32 * sub < tile.tokens * p.G;      // some row of the warp does
+      const int pos = tile.pos0 + tok;
+      const int hi = mine ? pos + 1 : 0;                   // keys [lo, hi) and [0, sinks)
+      const int lo = p.window ? max(0, pos - p.window + 1) : 0;
+      // keys that every existing row of the warp sees
+      const int hi_all = __reduce_min_sync(kFull, mine ? hi : 0x7fffffff);
+      const int lo_all = __reduce_max_sync(kFull, mine ? lo : 0);
+      float m = -INFINITY, l = 0.0f;  // m is the maximum that P and O are scaled by
+      for (int k = c.begin; k < c.end; ++k, ++blk) {
+        const int key0 = tile.block(k) * kKeys;
+        ok = __all_sync(kFull, mbar_wait(sfull, blk & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        if (busy) {
+          float s[kKeys];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(t_s + 32 * i, s + 32 * i);
+          tmem_wait_ld(s);
+          const bool all = key0 + kKeys <= hi_all && (key0 >= lo_all || key0 + kKeys <= p.sinks);
+          if (!all) {
+            const int to = hi - key0, from = lo - key0, sink = p.sinks - key0;
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i)
+              s[i] = i < to && (i >= from || i < sink) ? s[i] : -INFINITY;
+          }
+          float mx[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mx[i] = s[i];
+#pragma unroll
+          for (int i = 8; i < kKeys; i += 16)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              mx[j] = i + 8 + j < kKeys ? max3f(mx[j], s[i + j], s[i + 8 + j]) : fmaxf(mx[j], s[i + j]);
+          const float top = fmaxf(max3f(max3f(mx[0], mx[1], mx[2]), mx[3], mx[4]),
+                                  max3f(mx[5], mx[6], mx[7]));
+          const float m_new = fmaxf(m, top);
+          // -inf - -inf is NaN and compares false: nothing was summed yet
+          const bool grown = (m_new - m) * p.c > kRescaleLog2;
+          if (k == c.begin) {
+            m = m_new;
+          } else if (__any_sync(kFull, grown)) {
+            const float f = grown ? exp2_approx((m - m_new) * p.c) : 1.0f;
+            m = grown ? m_new : m;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              float o[32];
+              tmem_ld32(t_o + 32 * i, o);
+              tmem_wait_ld(o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] *= f;
+              tmem_st32(t_o + 32 * i, reinterpret_cast<uint32_t*>(o));
+            }
+          }
+          const float mc = reference(m);
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          uint32_t w[kKeys / 2];
+#pragma unroll
+          for (int i = 0; i < kKeys; i += 2) {
+            const float a = exp2_approx(fmaf(s[i], p.c, -mc));
+            const float b = exp2_approx(fmaf(s[i + 1], p.c, -mc));
+            sum[i & 2] += a;
+            sum[(i & 2) + 1] += b;
+            w[i / 2] = pack2<BF16>(a, b);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st32(t_s, w);
+          tmem_st32(t_s + 32, w + 32);
+          tmem_wait_st();
+        }
+        // V rows of a loaded page that no row of the tile sees (behind the
+        // context, before the window): whatever they hold, 0 * it must be 0.
+        const bool inside = key0 + kKeys <= tile.hi && (key0 >= tile.lo || key0 + kKeys <= p.sinks);
+        if (!inside) {
+          const int key = key0 + row;
+          if (!(key < tile.hi && (key >= tile.lo || key < p.sinks))) {
+            const int unit = (2 * blk + 1) * L::kPanels + row / L::kVKeys;
+            ok = mbar_wait(full(unit % S), (unit / S) & 1, abort_flag);
+            const uint32_t at = sbase + L::kOffRing + (unit % S) * kUnitBytes +
+                                (row % L::kVKeys) * 128;
+#pragma unroll
+            for (int pn = 0; pn < L::kPanels; ++pn)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};"
+                             ::"r"(at + pn * L::kVKeys * 128 + 16 * i), "r"(0) : "memory");
+            fence_async_shared();
+          }
+          ok = __all_sync(kFull, ok);
+          if (!ok) break;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pready);
+      }
+      if (ok) ok = __all_sync(kFull, mbar_wait(ofull, seg & 1, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      const bool whole = c.begin == 0 && c.end == c.tile.blocks;
+      if (busy) {
+        const int slot = 2 * blockIdx.x + (c.begin == 0 ? 1 : 0);
+        const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+        const long long token = tile.token0 + tok;
+        const int h = c.h * p.G + head;
+        uint16_t* out = static_cast<uint16_t*>(p.out) + token * p.out_stride_t + h * p.out_stride_h;
+        float* part = p.part + (static_cast<long long>(slot) * kRows + row) * D;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          float o[32];
+          tmem_ld32(t_o + 32 * i, o);
+          tmem_wait_ld(o);
+          if (!mine) continue;
+          if (whole) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              uint4 v;
+              v.x = pack2<BF16>(o[j] * inv, o[j + 1] * inv);
+              v.y = pack2<BF16>(o[j + 2] * inv, o[j + 3] * inv);
+              v.z = pack2<BF16>(o[j + 4] * inv, o[j + 5] * inv);
+              v.w = pack2<BF16>(o[j + 6] * inv, o[j + 7] * inv);
+              if (l == 0.0f) v = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(out + 32 * i + j) = v;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<float4*>(part + 32 * i + j) =
+                  make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+          }
+        }
+        if (mine) {
+          if (!whole)
+            p.ml[static_cast<long long>(slot) * kRows + row] = make_float2(l == 0.0f ? -INFINITY : reference(m), l);
+          else if (p.lse)
+            p.lse[token * (p.Hkv * p.G) + h] = l == 0.0f ? -INFINITY : reference(m) * kLn2 + logf(l);
+        }
+      }
+      // the item starts here and goes on in later CTAs: the second kernel
+      // joins the parts, this CTA's first
+      if (!whole && c.begin == 0 && threadIdx.x == 64) {
+        const long long last = share.end - 1 + (c.tile.blocks - c.end);  // its last key block
+        const int cta = static_cast<int>(((last + 1) * share.ctas - 1) / share.total);
+        p.meta[blockIdx.x] = make_int4(cta, tile.token0, c.h, tile.tokens);
+      }
+    }
+    if (!ok && lane == 0) give_up();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
+                 ::"r"(tmem), "n"(kTmemCols) : "memory");
+}
+
+// Joins the parts of the item that starts in CTA blockIdx.x of the first
+// kernel: with M the largest m, out = sum 2^(m - M) O / sum 2^(m - M) l.  One
+// warp per row, the parts in their order.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(128) dsa_attention_join_kernel(const AParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int4 meta = p.meta[blockIdx.x];
+  if (meta.x < 0) return;
+  const int lane = threadIdx.x & 31;
+  const int first = blockIdx.x, parts = meta.x - first + 1;
+  auto slot = [&](int i) { return i == 0 ? 2LL * first + 1 : 2LL * (first + i); };
+  for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); row < meta.w * p.G; row += gridDim.y * 4) {
+    float top = -INFINITY;
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.ml[slot(i) * kRows + row].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float acc[D / 32] = {};
+    float l = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+      const float2 ml = p.ml[slot(i) * kRows + row];
+      const float f = exp2_approx(ml.x - ref);
+      const float* o = p.part + (slot(i) * kRows + row) * D;
+      l = fmaf(f, ml.y, l);
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) acc[j] = fmaf(f, o[j * 32 + lane], acc[j]);
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const long long token = meta.y + row / p.G;
+    const int h = meta.z * p.G + row % p.G;
+    uint16_t* out = static_cast<uint16_t*>(p.out) + token * p.out_stride_t + h * p.out_stride_h;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j)
+      out[j * 32 + lane] = static_cast<uint16_t>(pack2<BF16>(l == 0.0f ? 0.0f : acc[j] * inv, 0.0f));
+    if (lane == 0 && p.lse)
+      p.lse[token * (p.Hkv * p.G) + h] =
+          l == 0.0f ? -INFINITY : ref * kLn2 + logf(l);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+bool misaligned(const void* ptr, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) != 0;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  std::call_once(g_encode_once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  return g_encode;
+}
+
+std::mutex g_ready_mu;
+bool g_ready[64];
+
+template <int D, bool BF16>
+cudaError_t prepare_one() {
+  cudaError_t e = cudaFuncSetAttribute(dsa_paged_attention_kernel<D, BF16>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       ASmem<D>::kBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(dsa_paged_attention_kernel<D, BF16>,
+                             cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+  return e;
+}
+
+// Once per device.
+cudaError_t prepare_device() {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(g_ready_mu);
+  if (g_ready[dev]) return cudaSuccess;
+  e = prepare_one<64, false>();
+  if (e == cudaSuccess) e = prepare_one<64, true>();
+  if (e == cudaSuccess) e = prepare_one<128, false>();
+  if (e == cudaSuccess) e = prepare_one<128, true>();
+  g_ready[dev] = e == cudaSuccess;
+  return e;
+}
+
+long long max_items(int T, int B, int Hkv, int tile_tokens) {
+  return (static_cast<long long>(T) / tile_tokens + B) * Hkv;
+}
+
+// Few items: cut the key blocks into equal shares.  From four items per
+// resident CTA on, one item per CTA, longest first, leaves less than a quarter
+// of a wave idle, needs no joining, and keeps CTAs that run together on the
+// same kv head, whose keys they then share in L2.
+bool use_split(int T, int B, int Hkv, int tile_tokens, int max_context) {
+  return max_context > kKeys && max_items(T, B, Hkv, tile_tokens) < 4LL * kSplitCtas;
+}
+
+bool encode_map(CUtensorMap* map, bool bf16, const void* base, int rank, const cuuint64_t* dims,
+                const cuuint64_t* strides, const cuuint32_t* box) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return encode && encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                          rank, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool BF16>
+cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                   const AParams& p, long long grid, bool pdl, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kAThreads);
+  cfg.dynamicSmemBytes = ASmem<D>::kBytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, dsa_paged_attention_kernel<D, BF16>, tq, tk, tv, p);
+  if (e != cudaSuccess || !p.split) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 4);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, dsa_attention_join_kernel<D, BF16>, p);
+}
+
+constexpr size_t kMetaBytes = kSplitCtas * sizeof(int4);
+constexpr size_t kMlBytes = 2 * kSplitCtas * kRows * sizeof(float2);
+
+}  // namespace
+
+extern "C" {
+
+size_t dsa_paged_attention_workspace_bytes(int32_t T, int32_t B, int32_t H, int32_t Hkv,
+                                           int32_t head_dim, int32_t max_context) {
+  if (T < 1 || B < 1 || Hkv < 1 || H < Hkv || H % Hkv || H / Hkv > kRows || head_dim < 1) return 0;
+  if (!use_split(T, B, Hkv, kRows / (H / Hkv), max_context)) return 0;
+  return kMetaBytes + kMlBytes +
+         2 * kSplitCtas * kRows * static_cast<size_t>(head_dim) * sizeof(float);
+}
+
+dsa_status dsa_paged_attention(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_cache,
+    const void* v_cache, int64_t k_stride_page, int64_t k_stride_token, int64_t k_stride_head,
+    int64_t v_stride_page, int64_t v_stride_token, int64_t v_stride_head, int64_t num_pages,
+    int32_t page_size, const int32_t* block_table, int64_t bt_stride, const int32_t* query_start,
+    const int32_t* context_lens, int32_t max_context, float scale, int32_t window, int32_t sinks,
+    void* out, int64_t out_stride_t, int64_t out_stride_h, float* lse, int32_t T, int32_t B,
+    int32_t H, int32_t Hkv, int32_t head_dim, int32_t dtype, uint32_t flags, void* workspace,
+    size_t workspace_bytes, int32_t* err_flags, void* stream) {
+  if (T < 0 || B < 0 || H < 1 || Hkv < 1 || H % Hkv || max_context < 0 || bt_stride < 0 ||
+      num_pages < 1 || num_pages > 0x7fffffffLL || window < 0 || sinks < 0)
+    return DSA_ERR_SHAPE;
+  const int G = H / Hkv;
+  if (head_dim != 64 && head_dim != 128) return DSA_ERR_UNSUPPORTED;
+  if (dtype != DSA_DTYPE_BF16 && dtype != DSA_DTYPE_FP16) return DSA_ERR_UNSUPPORTED;
+  if (G > kRows) return DSA_ERR_UNSUPPORTED;
+  if (page_size < 8 || (page_size < 64 ? 64 % page_size : page_size % 64) != 0)
+    return DSA_ERR_UNSUPPORTED;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return DSA_ERR_UNSUPPORTED;
+  if (flags & ~static_cast<uint32_t>(DSA_FLAG_PDL)) return DSA_ERR_UNSUPPORTED;
+  // every row of the table covers max_context keys
+  if (bt_stride < (static_cast<long long>(max_context) + page_size - 1) / page_size)
+    return DSA_ERR_SHAPE;
+  // positions and grids are 32-bit
+  if (max_context > (1 << 30) || T > (1 << 30) || static_cast<long long>(T) * H > 0x7fffffffLL)
+    return DSA_ERR_SHAPE;
+  const int tile_tokens = kRows / G;
+  const long long items = max_items(T, B, Hkv, tile_tokens);
+  if (items > 0x7fffffffLL) return DSA_ERR_SHAPE;
+  if (T == 0 || B == 0) return DSA_OK;
+  if (!q || !k_cache || !v_cache || !query_start || !context_lens || !out ||
+      (!block_table && max_context > 0))
+    return DSA_ERR_NULL;
+  // TMA: 16-byte aligned bases, strides that are multiples of 16 bytes, below 2^40
+  auto bad_stride = [](int64_t stride, int64_t extent) {
+    return extent > 1 && (stride % 8 != 0);
+  };
+  auto bad_size = [](int64_t stride, int64_t extent) {
+    return extent > 1 && (stride < 1 || stride >= (1LL << 39));
+  };
+  if (bad_size(q_stride_t, T) || bad_size(q_stride_h, H) || bad_size(k_stride_page, num_pages) ||
+      bad_size(k_stride_token, page_size) || bad_size(k_stride_head, Hkv) ||
+      bad_size(v_stride_page, num_pages) || bad_size(v_stride_token, page_size) ||
+      bad_size(v_stride_head, Hkv) || bad_size(out_stride_t, T) || bad_size(out_stride_h, H))
+    return DSA_ERR_SHAPE;
+  if (bad_stride(q_stride_t, T) || bad_stride(q_stride_h, H) ||
+      bad_stride(k_stride_page, num_pages) || bad_stride(k_stride_token, page_size) ||
+      bad_stride(k_stride_head, Hkv) || bad_stride(v_stride_page, num_pages) ||
+      bad_stride(v_stride_token, page_size) || bad_stride(v_stride_head, Hkv) ||
+      bad_stride(out_stride_t, T) || bad_stride(out_stride_h, H))
+    return DSA_ERR_ALIGN;
+  if (misaligned(q, 16) || misaligned(k_cache, 16) || misaligned(v_cache, 16) ||
+      misaligned(out, 16) || misaligned(block_table, 4) || misaligned(query_start, 4) ||
+      misaligned(context_lens, 4) || misaligned(lse, 4) || misaligned(err_flags, 4))
+    return DSA_ERR_ALIGN;
+  const size_t need = dsa_paged_attention_workspace_bytes(T, B, H, Hkv, head_dim, max_context);
+  if (need) {
+    if (!workspace) return DSA_ERR_NULL;
+    if (misaligned(workspace, 16)) return DSA_ERR_ALIGN;
+    if (workspace_bytes < need) return DSA_ERR_SHAPE;
+  }
+  if (prepare_device() != cudaSuccess) return DSA_ERR_LAUNCH;
+
+  const bool bf16 = dtype == DSA_DTYPE_BF16;
+  const cuuint64_t D = static_cast<cuuint64_t>(head_dim);
+  // the stride of a dimension of one entry is never used, but has to be valid
+  auto bytes = [&](int64_t stride, int64_t extent) {
+    return static_cast<cuuint64_t>(extent > 1 ? stride : head_dim) * 2;
+  };
+  alignas(64) CUtensorMap tq, tk, tv;
+  const int box = page_size < 64 ? page_size : 64;
+  {
+    const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T)};
+    const cuuint64_t strides[2] = {bytes(q_stride_h, H), bytes(q_stride_t, T)};
+    const cuuint32_t b[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(tile_tokens)};
+    if (!encode_map(&tq, bf16, q, 3, dims, strides, b)) return DSA_ERR_LAUNCH;
+  }
+  auto cache_map = [&](CUtensorMap* map, const void* base, int64_t sp, int64_t st, int64_t sh) {
+    const cuuint64_t dims[4] = {D, static_cast<cuuint64_t>(page_size),
+                                static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(num_pages)};
+    const cuuint64_t strides[3] = {bytes(st, page_size), bytes(sh, Hkv), bytes(sp, num_pages)};
+    const cuuint32_t b[4] = {64, static_cast<cuuint32_t>(box), 1, 1};
+    return encode_map(map, bf16, base, 4, dims, strides, b);
+  };
+  if (!cache_map(&tk, k_cache, k_stride_page, k_stride_token, k_stride_head) ||
+      !cache_map(&tv, v_cache, v_stride_page, v_stride_token, v_stride_head))
+    return DSA_ERR_LAUNCH;
+
+  AParams p = {};
+  p.block_table = block_table;
+  p.query_start = query_start;
+  p.context_lens = context_lens;
+  p.out = out;
+  p.lse = lse;
+  p.bt_stride = bt_stride;
+  p.out_stride_t = out_stride_t;
+  p.out_stride_h = out_stride_h;
+  p.num_pages = static_cast<int>(num_pages);
+  p.page = page_size;
+  p.box = box;
+  p.T = T;
+  p.B = B;
+  p.Hkv = Hkv;
+  p.G = G;
+  p.tile_tokens = tile_tokens;
+  p.max_context = max_context;
+  p.window = window < max_context ? window : 0;  // such a window hides nothing
+  p.sinks = p.window ? (sinks < max_context ? sinks : max_context) : 0;
+  p.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  p.split = need ? 1 : 0;
+  p.meta = static_cast<int4*>(workspace);
+  p.ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + kMetaBytes);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kMetaBytes + kMlBytes);
+  p.err = err_flags;
+  const long long grid = p.split ? kSplitCtas : items;
+  const bool pdl = (flags & DSA_FLAG_PDL) != 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (head_dim == 64)
+    e = bf16 ? launch<64, true>(tq, tk, tv, p, grid, pdl, s)
+             : launch<64, false>(tq, tk, tv, p, grid, pdl, s);
+  else
+    e = bf16 ? launch<128, true>(tq, tk, tv, p, grid, pdl, s)
+             : launch<128, false>(tq, tk, tv, p, grid, pdl, s);
+  return e == cudaSuccess ? DSA_OK : DSA_ERR_LAUNCH;
+}
+
+}  // extern "C"

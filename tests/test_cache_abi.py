@@ -111,3 +111,39 @@ def test_binding_rejects_cpu_tensors():
                  lambda: dp.dsa_cache_compact(c, i, t, i, 4)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def _att(lib, **over):
+    a = dict(q=A, qst=1024, qsh=128, k=A, v=A, ksp=16384, kst=256, ksh=128, vsp=16384, vst=256,
+             vsh=128, pages=8, ps=64, bt=A, bts=4, start=A, lens=A, maxc=256, scale=0.1, window=0,
+             sinks=0, out=A, ost=1024, osh=128, lse=A, T=4, B=2, H=8, Hkv=2, D=128, dtype=0,
+             flags=0, ws=A, wsb=1 << 30, err=None, stream=None)
+    a.update(over)
+    return lib.dsa_paged_attention(*a.values())
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(T=-1), 3), (dict(B=-1), 3), (dict(H=0), 3), (dict(Hkv=0), 3), (dict(H=9), 3),
+    (dict(maxc=-1), 3), (dict(bts=3), 3), (dict(pages=0), 3), (dict(window=-1), 3),
+    (dict(sinks=-1), 3), (dict(D=96), 4), (dict(dtype=2), 4), (dict(H=129, Hkv=1), 4),
+    (dict(ps=4), 4), (dict(ps=24), 4), (dict(ps=96), 4), (dict(scale=0.0), 4),
+    (dict(scale=-1.0), 4), (dict(scale=float("inf")), 4), (dict(flags=2), 4),
+    (dict(q=None), 1), (dict(k=None), 1), (dict(v=None), 1), (dict(bt=None), 1),
+    (dict(start=None), 1), (dict(lens=None), 1), (dict(out=None), 1), (dict(ws=None), 1),
+    (dict(q=A + 8), 2), (dict(k=A + 8), 2), (dict(v=A + 8), 2), (dict(out=A + 8), 2),
+    (dict(qst=1028), 2), (dict(ksp=16388), 2), (dict(vsh=124), 2), (dict(osh=132), 2),
+    (dict(lse=A + 2), 2), (dict(ws=A + 8), 2), (dict(wsb=1 << 20), 3), (dict(kst=0), 3),
+    (dict(ksp=-16384), 3), (dict(T=1 << 29, H=8), 3),
+    (dict(T=0, q=None, out=None), 0), (dict(B=0, start=None), 0)])
+def test_attention_validation(lib, over, status):
+    assert _att(lib, **over) == status
+
+
+def test_attention_workspace(lib):
+    f = lib.dsa_paged_attention_workspace_bytes
+    one = f(1, 1, 64, 8, 128, 4096)
+    assert one == 304 * 16 + 608 * 128 * (8 + 4 * 128)
+    assert f(64, 64, 64, 8, 64, 4096) == 304 * 16 + 608 * 128 * (8 + 4 * 64)
+    assert f(1, 1, 64, 8, 128, 128) == 0      # one block: nothing to cut
+    assert f(8192, 1, 64, 8, 128, 8192) == 0  # items enough
+    assert f(0, 1, 64, 8, 128, 4096) == f(1, 1, 64, 7, 128, 4096) == 0
