@@ -31,10 +31,10 @@
 // Two CTAs share an SM, so one's softmax runs beside the other's products.
 //
 // Bound: a chunk by the tensor cores (4 D flops per row and visible key),
-// single tokens by the cache's bytes.  With few items the key blocks of all
-// items are laid end to end and cut into equal shares, one per CTA; an item
-// that a cut divides leaves partial (O, m, l) in the workspace, which a second
-// kernel joins in a fixed order.
+// single tokens by the cache's bytes.  The key blocks of all items are laid end
+// to end and cut into equal shares, one per CTA; an item that a cut divides
+// leaves partial (O, m, l) in the workspace, which a second kernel joins in a
+// fixed order.  (use_split says when CTAs take whole items instead.)
 //
 // Every wait is bounded in time; TMEM is always released before exit.
 #include <cuda.h>
@@ -73,7 +73,7 @@ struct AParams {
   int max_context;
   int window, sinks;  // window 0: none
   float c;            // scale * log2(e)
-  int split;          // 1: equal shares of the key blocks; 0: one item per CTA
+  int split;          // 1: equal shares of the key blocks; 0: whole items, gridDim.x apart
   int4* meta;         // split: [kSplitCtas] the item that CTA leaves to later ones
   float2* ml;         // split: [2 * kSplitCtas][kRows] (log2 of the scale, l) of a part
   float* part;        // split: [2 * kSplitCtas][kRows][D] O of a part
@@ -98,6 +98,26 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       " [%0], [%1, {%2, %3, %4, %5}], [%6];"
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
+// mbar_wait with probes that the hardware ends early: the softmax and the
+// matrix products hand over to each other three times per key block, and a
+// thread that asked for a long sleep wakes late.
+__device__ __forceinline__ bool wait_soon(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  for (int i = 0; i < 64; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    if (ok) return true;
+  }
+  return mbar_wait_slow(bar, parity, abort_flag);
 }
 
 // Shared-memory matrix descriptor of 128-byte-swizzled rows: 8-row groups of
@@ -209,6 +229,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
+// The n lowest of 64 bits.
+__device__ __forceinline__ uint64_t below(int n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+
 // ---------------------------------------------------------------- work items
 
 // One query tile of a sequence and the key blocks that some row of it sees.
@@ -289,7 +314,8 @@ struct Cursor {
   Seq s;
   Tile tile;
   int begin, end;
-  long long left;  // key blocks after this segment (split) or 0
+  long long left;  // split: key blocks after this segment
+  long long item;  // not split: the item
 };
 
 __device__ __forceinline__ void take_tile(const AParams& p, Cursor& c, int begin, long long budget) {
@@ -300,21 +326,10 @@ __device__ __forceinline__ void take_tile(const AParams& p, Cursor& c, int begin
   c.left = budget - (c.end - c.begin);
 }
 
-// The next tile, kv head or sequence with tokens.  Only called when blocks are left.
-__device__ __forceinline__ bool next_segment(const AParams& p, Cursor& c) {
-  if (c.left <= 0) return false;
-  if (++c.t == c.s.tiles) {
-    c.t = 0;
-    if (++c.h == p.Hkv) {
-      c.h = 0;
-      do {
-        if (++c.b >= p.B) return false;
-        c.s = load_seq(p, c.b);
-      } while (c.s.tiles == 0);
-    }
-  }
-  take_tile(p, c, 0, c.left);
-  return true;
+__device__ __forceinline__ long long mul_div(long long total, int g, int of) {
+  if (total < (1 << 22))  // 304 shares: the product fits 32 bits
+    return static_cast<uint32_t>(total) * static_cast<uint32_t>(g) / static_cast<uint32_t>(of);
+  return total * g / of;
 }
 
 // Split work: key blocks in the order sequence, kv head, tile.  CTA g of
@@ -338,21 +353,48 @@ __device__ __forceinline__ Share my_share(const AParams& p) {
   r.total = sum * p.Hkv;
   r.ctas = r.total < static_cast<long long>(gridDim.x) ? static_cast<int>(r.total)
                                                        : static_cast<int>(gridDim.x);
-  const long long g = blockIdx.x;
-  r.begin = g < r.ctas ? r.total * g / r.ctas : 0;
-  r.end = g < r.ctas ? r.total * (g + 1) / r.ctas : 0;
+  const int g = blockIdx.x;
+  r.begin = g < r.ctas ? mul_div(r.total, g, r.ctas) : 0;
+  r.end = g < r.ctas ? mul_div(r.total, g + 1, r.ctas) : 0;
   return r;
 }
 
-// The CTA's first segment.  A whole warp calls it; every lane gets the same.
-__device__ __forceinline__ bool first_segment(const AParams& p, Cursor& c, Share& share) {
-  const int lane = threadIdx.x & 31;
-  long long want = blockIdx.x;  // an item, or a key block
-  if (p.split) {
-    share = my_share(p);
-    if (share.begin >= share.end) return false;
-    want = share.begin;
+__device__ __forceinline__ bool seek(const AParams& p, Cursor& c, const Share& share, long long want);
+
+// The next tile, kv head or sequence with tokens, while key blocks are left;
+// or the CTA's next whole item.  A whole warp calls it.
+__device__ __forceinline__ bool next_segment(const AParams& p, Cursor& c, const Share& share) {
+  if (!p.split) {
+    c.item += gridDim.x;
+    return seek(p, c, share, c.item);
   }
+  if (c.left <= 0) return false;
+  if (++c.t == c.s.tiles) {
+    c.t = 0;
+    if (++c.h == p.Hkv) {
+      c.h = 0;
+      do {
+        if (++c.b >= p.B) return false;
+        c.s = load_seq(p, c.b);
+      } while (c.s.tiles == 0);
+    }
+  }
+  take_tile(p, c, 0, c.left);
+  return true;
+}
+
+// The CTA's first segment.
+__device__ __forceinline__ bool first_segment(const AParams& p, Cursor& c, Share& share) {
+  c.item = blockIdx.x;
+  if (!p.split) return seek(p, c, share, c.item);
+  share = my_share(p);
+  return share.begin < share.end && seek(p, c, share, share.begin);
+}
+
+// Puts the cursor at key block `want` (split) or item `want`.  A whole warp
+// calls it; every lane gets the same.
+__device__ __forceinline__ bool seek(const AParams& p, Cursor& c, const Share& share, long long want) {
+  const int lane = threadIdx.x & 31;
   long long before = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     Seq s = {0, 0, 0, 0};
@@ -366,12 +408,18 @@ __device__ __forceinline__ bool first_segment(const AParams& p, Cursor& c, Share
       const long long rest = want - (__shfl_sync(kFull, upto, src) - one * p.Hkv);
       c.b = b0 + src;
       c.s = load_seq(p, c.b);
-      c.h = static_cast<int>(rest / one);
-      const int r = static_cast<int>(rest % one);
+      c.h = 0;
+      int r = 0;
+      if (rest < (1LL << 31) && one < (1LL << 31)) {
+        c.h = static_cast<int>(rest) / static_cast<int>(one);
+        r = static_cast<int>(rest) - c.h * static_cast<int>(one);
+      } else {
+        c.h = static_cast<int>(rest / one);
+        r = static_cast<int>(rest - c.h * one);
+      }
       if (!p.split) {
         c.t = c.s.tiles - 1 - r;  // the last tiles of a chunk see the most keys: first
         take_tile(p, c, 0, 1LL << 40);
-        c.left = 0;
         return true;
       }
       int seen = 0;  // key blocks of the tiles before
@@ -404,8 +452,8 @@ struct ASmem {
   static constexpr int kVKeys = kKeys / kPanels;            // keys of a V unit
   static constexpr int kOffRing = kQBytes;
   static constexpr int kOffBar = kOffRing + kStages * kUnitBytes;
-  // barriers: full[S], empty[S], qfull, qempty, sfull, pready, ofull, drain
-  static constexpr int kBars = 2 * kStages + 6;
+  // barriers: full[S], empty[S], qfull, qempty, sfull, pready[2], ofull, drain
+  static constexpr int kBars = 2 * kStages + 7;
   static constexpr int kOffTmem = kOffBar + 8 * kBars;
   static constexpr int kOffAbort = kOffTmem + 4;
   static constexpr int kBytes = kOffAbort + 4;
@@ -436,12 +484,18 @@ __global__ void __launch_bounds__(kAThreads, 2)
   auto full = [&](int s) { return bar0 + 8 * s; };
   auto empty = [&](int s) { return bar0 + 8 * (S + s); };
   const uint32_t qfull = bar0 + 8 * (2 * S), qempty = bar0 + 8 * (2 * S + 1);
-  const uint32_t sfull = bar0 + 8 * (2 * S + 2), pready = bar0 + 8 * (2 * S + 3);
-  const uint32_t ofull = bar0 + 8 * (2 * S + 4), drain = bar0 + 8 * (2 * S + 5);
+  const uint32_t sfull = bar0 + 8 * (2 * S + 2);
+  auto pready = [&](int half) { return bar0 + 8 * (2 * S + 3 + half); };
+  const uint32_t ofull = bar0 + 8 * (2 * S + 5), drain = bar0 + 8 * (2 * S + 6);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffAbort);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
+  if (threadIdx.x == 32) {
+    prefetch_map(&tq);
+    prefetch_map(&tk);
+    prefetch_map(&tv);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full(s), 1);
@@ -450,7 +504,7 @@ __global__ void __launch_bounds__(kAThreads, 2)
     mbar_init(qfull, 1);
     mbar_init(qempty, 1);
     mbar_init(sfull, 1);
-    mbar_init(pready, 4);  // the softmax warps
+    for (int h = 0; h < 2; ++h) mbar_init(pready(h), 4);  // the softmax warps
     mbar_init(ofull, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -489,11 +543,11 @@ __global__ void __launch_bounds__(kAThreads, 2)
     // waits until the ring's next unit may be written
     auto acquire = [&]() {
       const int s = unit % S;
-      ok = ok && (unit < S || mbar_wait(empty(s), ((unit / S) & 1) ^ 1, abort_flag));
+      ok = ok && (unit < S || wait_soon(empty(s), ((unit / S) & 1) ^ 1, abort_flag));
       ok = __all_sync(kFull, ok);
       return s;
     };
-    for (; more && ok; more = next_segment(p, c), ++seg) {
+    for (; more && ok; more = next_segment(p, c, share), ++seg) {
       const Tile& tile = c.tile;
       // box l of a block: its page, -1 if no row sees any of its keys, -2 if
       // the table names no page of the pool for it
@@ -504,14 +558,14 @@ __global__ void __launch_bounds__(kAThreads, 2)
         const int page = __ldg(table + key / p.page);
         return page >= 0 && page < p.num_pages ? page : -2;
       };
-      int page = lookup(c.begin);
-      if (seg > 0) ok = __all_sync(kFull, mbar_wait(qempty, (seg & 1) ^ 1, abort_flag));
+      if (seg > 0) ok = __all_sync(kFull, wait_soon(qempty, (seg & 1) ^ 1, abort_flag));
       if (!ok) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(qfull, L::kPanels * p.G * p.tile_tokens * 128);
         for (int pn = 0; pn < L::kPanels; ++pn)
           tma_load_3d(sbase + pn * kRows * 128, &tq, pn * 64, c.h * p.G, tile.token0, qfull);
       }
+      int page = lookup(c.begin);
       for (int k = c.begin; k < c.end && ok; ++k) {
         const int in_page = (tile.block(k) * kKeys + lane * p.box) % p.page;
         const int next = k + 1 < c.end ? lookup(k + 1) : -1;
@@ -570,13 +624,13 @@ __global__ void __launch_bounds__(kAThreads, 2)
     constexpr uint32_t idesc_o = mma_idesc(BF16, true, D);
     int unit = 0, seg = 0, blk = 0;
     bool ok = true;
-    for (; more && ok; more = next_segment(p, c), ++seg) {
+    for (; more && ok; more = next_segment(p, c, share), ++seg) {
       if (lane == 0) {
-        ok = mbar_wait(qfull, seg & 1, abort_flag);
+        ok = wait_soon(qfull, seg & 1, abort_flag);
         for (int k = c.begin; k < c.end && ok; ++k, ++blk) {
           for (int pn = 0; pn < L::kPanels && ok; ++pn, ++unit) {
             const int s = unit % S;
-            ok = mbar_wait(full(s), (unit / S) & 1, abort_flag);
+            ok = wait_soon(full(s), (unit / S) & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
             const uint64_t a = sw128_desc(sbase + pn * kRows * 128, 0);
@@ -589,19 +643,23 @@ __global__ void __launch_bounds__(kAThreads, 2)
           if (!ok) break;
           mma_commit(sfull);
           if (k + 1 == c.end) mma_commit(qempty);
-          ok = mbar_wait(pready, blk & 1, abort_flag);
-          for (int u = 0; u < L::kPanels && ok; ++u, ++unit) {
-            const int s = unit % S;
-            ok = mbar_wait(full(s), (unit / S) & 1, abort_flag);
+          for (int half = 0; half < 2 && ok; ++half) {  // of the block's keys
+            const int u = half * L::kPanels / 2;        // its V unit of the block
+            const int s = (unit + u) % S;
+            ok = wait_soon(pready(half), blk & 1, abort_flag) &&
+                 wait_soon(full(s), ((unit + u) / S) & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t b = sw128_desc(sbase + L::kOffRing + s * kUnitBytes, L::kVKeys * 128);
+            const int row = half * (kKeys / 2) - u * L::kVKeys;  // its first key in the unit
+            const uint64_t b = sw128_desc(sbase + L::kOffRing + s * kUnitBytes + row * 128,
+                                          L::kVKeys * 128);
 #pragma unroll
-            for (int ks = 0; ks < L::kVKeys / 16; ++ks)
-              mma_ts(tmem_o, tmem + (u * L::kVKeys + ks * 16) / 2, b + ks * (2048 >> 4), idesc_o,
-                     (k > c.begin || u + ks > 0) ? 1u : 0u);
-            mma_commit(empty(s));
+            for (int ks = 0; ks < kKeys / 32; ++ks)
+              mma_ts(tmem_o, tmem + half * (kKeys / 4) + ks * 8, b + ks * (2048 >> 4), idesc_o,
+                     (k > c.begin || half + ks > 0) ? 1u : 0u);
+            if (L::kPanels == 2 || half == 1) mma_commit(empty(s));
           }
+          unit += L::kPanels;
         }
         if (ok) mma_commit(ofull);
       }
@@ -625,7 +683,7 @@ __global__ void __launch_bounds__(kAThreads, 2)
     const int tok = row / p.G, head = row - tok * p.G;
     int seg = 0, blk = 0;
     bool ok = true;
-    for (; more && ok; more = next_segment(p, c), ++seg) {
+    for (; more && ok; more = next_segment(p, c, share), ++seg) {
       const Tile& tile = c.tile;
       const bool mine = tok < tile.tokens;                 // this row exists
       const bool busy = 32 * sub < tile.tokens * p.G;      // some row of the warp does
@@ -638,32 +696,43 @@ __global__ void __launch_bounds__(kAThreads, 2)
       float m = -INFINITY, l = 0.0f;  // m is the maximum that P and O are scaled by
       for (int k = c.begin; k < c.end; ++k, ++blk) {
         const int key0 = tile.block(k) * kKeys;
-        ok = __all_sync(kFull, mbar_wait(sfull, blk & 1, abort_flag));
+        ok = __all_sync(kFull, wait_soon(sfull, blk & 1, abort_flag));
         if (!ok) break;
         tc_fence_after();
-        if (busy) {
-          float s[kKeys];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(t_s + 32 * i, s + 32 * i);
+        // S in halves of 64 keys, read twice: for the maximum, then for P.
+        // (All 128 values at once do not fit in the 168 registers that two
+        // CTAs per SM leave a thread.)
+        const bool all = key0 + kKeys <= hi_all && (key0 >= lo_all || key0 + kKeys <= p.sinks);
+        float s[kKeys / 2];
+        auto load_half = [&](int half) {
+          tmem_ld32(t_s + half * 64, s);
+          tmem_ld32(t_s + half * 64 + 32, s + 32);
           tmem_wait_ld(s);
-          const bool all = key0 + kKeys <= hi_all && (key0 >= lo_all || key0 + kKeys <= p.sinks);
           if (!all) {
-            const int to = hi - key0, from = lo - key0, sink = p.sinks - key0;
+            const int at = key0 + half * 64;
+            const uint64_t seen = below(hi - at) & (~below(lo - at) | below(p.sinks - at));
+            const uint32_t bits[2] = {static_cast<uint32_t>(seen), static_cast<uint32_t>(seen >> 32)};
 #pragma unroll
-            for (int i = 0; i < kKeys; ++i)
-              s[i] = i < to && (i >= from || i < sink) ? s[i] : -INFINITY;
+            for (int i = 0; i < kKeys / 2; ++i)
+              s[i] = bits[i / 32] & (1u << (i % 32)) ? s[i] : -INFINITY;
           }
-          float mx[8];
+        };
+        float mc = 0.0f;
+        if (busy) {
+          float m_new = m;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) mx[i] = s[i];
+          for (int half = 0; half < 2; ++half) {
+            load_half(half);
+            float mx[4];
 #pragma unroll
-          for (int i = 8; i < kKeys; i += 16)
+            for (int j = 0; j < 4; ++j) mx[j] = s[j];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              mx[j] = i + 8 + j < kKeys ? max3f(mx[j], s[i + j], s[i + 8 + j]) : fmaxf(mx[j], s[i + j]);
-          const float top = fmaxf(max3f(max3f(mx[0], mx[1], mx[2]), mx[3], mx[4]),
-                                  max3f(mx[5], mx[6], mx[7]));
-          const float m_new = fmaxf(m, top);
+            for (int i = 4; i < kKeys / 2; i += 8)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                mx[j] = i + 4 < kKeys / 2 ? max3f(mx[j], s[i + j], s[i + 4 + j]) : fmaxf(mx[j], s[i + j]);
+            m_new = max3f(m_new, fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          }
           // -inf - -inf is NaN and compares false: nothing was summed yet
           const bool grown = (m_new - m) * p.c > kRescaleLog2;
           if (k == c.begin) {
@@ -682,21 +751,7 @@ __global__ void __launch_bounds__(kAThreads, 2)
               tmem_st32(t_o + 32 * i, reinterpret_cast<uint32_t*>(o));
             }
           }
-          const float mc = reference(m);
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          uint32_t w[kKeys / 2];
-#pragma unroll
-          for (int i = 0; i < kKeys; i += 2) {
-            const float a = exp2_approx(fmaf(s[i], p.c, -mc));
-            const float b = exp2_approx(fmaf(s[i + 1], p.c, -mc));
-            sum[i & 2] += a;
-            sum[(i & 2) + 1] += b;
-            w[i / 2] = pack2<BF16>(a, b);
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tmem_st32(t_s, w);
-          tmem_st32(t_s + 32, w + 32);
-          tmem_wait_st();
+          mc = reference(m);
         }
         // V rows of a loaded page that no row of the tile sees (behind the
         // context, before the window): whatever they hold, 0 * it must be 0.
@@ -705,7 +760,7 @@ __global__ void __launch_bounds__(kAThreads, 2)
           const int key = key0 + row;
           if (!(key < tile.hi && (key >= tile.lo || key < p.sinks))) {
             const int unit = (2 * blk + 1) * L::kPanels + row / L::kVKeys;
-            ok = mbar_wait(full(unit % S), (unit / S) & 1, abort_flag);
+            ok = wait_soon(full(unit % S), (unit / S) & 1, abort_flag);
             const uint32_t at = sbase + L::kOffRing + (unit % S) * kUnitBytes +
                                 (row % L::kVKeys) * 128;
 #pragma unroll
@@ -719,11 +774,30 @@ __global__ void __launch_bounds__(kAThreads, 2)
           ok = __all_sync(kFull, ok);
           if (!ok) break;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(pready);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (busy) {
+            load_half(half);
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            uint32_t w[kKeys / 4];
+#pragma unroll
+            for (int i = 0; i < kKeys / 2; i += 2) {
+              const float a = exp2_approx(fmaf(s[i], p.c, -mc));
+              const float b = exp2_approx(fmaf(s[i + 1], p.c, -mc));
+              sum[i & 2] += a;
+              sum[(i & 2) + 1] += b;
+              w[i / 2] = pack2<BF16>(a, b);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_st32(t_s + 32 * half, w);  // over S of the keys read before
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pready(half));
+        }
       }
-      if (ok) ok = __all_sync(kFull, mbar_wait(ofull, seg & 1, abort_flag));
+      if (ok) ok = __all_sync(kFull, wait_soon(ofull, seg & 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
       const bool whole = c.begin == 0 && c.end == c.tile.blocks;
@@ -785,18 +859,39 @@ __global__ void __launch_bounds__(kAThreads, 2)
 }
 
 // Joins the parts of the item that starts in CTA blockIdx.x of the first
-// kernel: with M the largest m, out = sum 2^(m - M) O / sum 2^(m - M) l.  One
-// warp per row, the parts in their order.
+// kernel: with M the largest m, out = sum 2^(m - M) O / sum 2^(m - M) l.  The
+// eight warps take a row each where the parts are few, else all one row, an
+// eighth of its parts each; every sum is in the order of the parts or warps.
+constexpr int kJoinWarps = 8, kJoinGroups = 8;
+
+template <int N>
+struct Vec;
+template <>
+struct Vec<2> {
+  using type = float2;
+};
+template <>
+struct Vec<4> {
+  using type = float4;
+};
+
 template <int D, bool BF16>
-__global__ void __launch_bounds__(128) dsa_attention_join_kernel(const AParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) dsa_attention_join_kernel(const AParams p) {
+  __shared__ float sums[kJoinWarps][D + 1];
   grid_dependency_wait();
   grid_launch_dependents();
   const int4 meta = p.meta[blockIdx.x];
   if (meta.x < 0) return;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int first = blockIdx.x, parts = meta.x - first + 1;
+  const bool few = parts <= kJoinWarps;
+  const int step = few ? 1 : kJoinWarps, from = few ? 0 : warp;
   auto slot = [&](int i) { return i == 0 ? 2LL * first + 1 : 2LL * (first + i); };
-  for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); row < meta.w * p.G; row += gridDim.y * 4) {
+  using V = typename Vec<D / 32>::type;
+  for (int r0 = blockIdx.y * (few ? kJoinWarps : 1); r0 < meta.w * p.G;
+       r0 += kJoinGroups * (few ? kJoinWarps : 1)) {
+    const int row = r0 + (few ? warp : 0);
+    if (few && row >= meta.w * p.G) return;
     float top = -INFINITY;
     for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.ml[slot(i) * kRows + row].x);
 #pragma unroll
@@ -804,25 +899,42 @@ __global__ void __launch_bounds__(128) dsa_attention_join_kernel(const AParams p
     const float ref = top == -INFINITY ? 0.0f : top;
     float acc[D / 32] = {};
     float l = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
+#pragma unroll 8
+    for (int i = from; i < parts; i += step) {
       const float2 ml = p.ml[slot(i) * kRows + row];
+      const V o = *reinterpret_cast<const V*>(p.part + (slot(i) * kRows + row) * D + lane * (D / 32));
       const float f = exp2_approx(ml.x - ref);
-      const float* o = p.part + (slot(i) * kRows + row) * D;
       l = fmaf(f, ml.y, l);
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) acc[j] = fmaf(f, o[j * 32 + lane], acc[j]);
+      for (int j = 0; j < D / 32; ++j) acc[j] = fmaf(f, reinterpret_cast<const float*>(&o)[j], acc[j]);
+    }
+    if (!few) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) sums[warp][lane * (D / 32) + j] = acc[j];
+      if (lane == 0) sums[warp][D] = l;
+      __syncthreads();
+      if (warp != 0) continue;
+      l = 0.0f;
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) acc[j] = 0.0f;
+      for (int w = 0; w < kJoinWarps; ++w) {
+        l += sums[w][D];
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) acc[j] += sums[w][lane * (D / 32) + j];
+      }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const long long token = meta.y + row / p.G;
     const int h = meta.z * p.G + row % p.G;
-    uint16_t* out = static_cast<uint16_t*>(p.out) + token * p.out_stride_t + h * p.out_stride_h;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
+                                                token * p.out_stride_t + h * p.out_stride_h) +
+                    lane * (D / 64);
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j)
-      out[j * 32 + lane] = static_cast<uint16_t>(pack2<BF16>(l == 0.0f ? 0.0f : acc[j] * inv, 0.0f));
+    for (int j = 0; j < D / 32; j += 2)
+      out[j / 2] = l == 0.0f ? 0u : pack2<BF16>(acc[j] * inv, acc[j + 1] * inv);
     if (lane == 0 && p.lse)
-      p.lse[token * (p.Hkv * p.G) + h] =
-          l == 0.0f ? -INFINITY : ref * kLn2 + logf(l);
+      p.lse[token * (p.Hkv * p.G) + h] = l == 0.0f ? -INFINITY : ref * kLn2 + logf(l);
   }
 }
 
@@ -882,12 +994,15 @@ long long max_items(int T, int B, int Hkv, int tile_tokens) {
   return (static_cast<long long>(T) / tile_tokens + B) * Hkv;
 }
 
-// Few items: cut the key blocks into equal shares.  From four items per
-// resident CTA on, one item per CTA, longest first, leaves less than a quarter
-// of a wave idle, needs no joining, and keeps CTAs that run together on the
-// same kv head, whose keys they then share in L2.
-bool use_split(int T, int B, int Hkv, int tile_tokens, int max_context) {
-  return max_context > kKeys && max_items(T, B, Hkv, tile_tokens) < 4LL * kSplitCtas;
+// The key blocks are cut into equal shares unless tiles of one sequence share
+// keys that L2 cannot hold: a share's place in the keys differs from CTA to
+// CTA, so all keys of the call are in use at once, while whole items taken in
+// order keep the CTAs on one kv head.  That needs items enough for a balance.
+bool use_split(int T, int B, int Hkv, int D, int tile_tokens, int max_context) {
+  const bool shared = T / tile_tokens >= 2LL * B;
+  const double bytes = 4.0 * D * Hkv * max_context * B;
+  return max_context > kKeys &&
+         !(shared && bytes > 9.6e7 && max_items(T, B, Hkv, tile_tokens) >= 4LL * kSplitCtas);
 }
 
 bool encode_map(CUtensorMap* map, bool bf16, const void* base, int rank, const cuuint64_t* dims,
@@ -917,8 +1032,8 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   cfg.numAttrs = pdl ? 1 : 0;
   cudaError_t e = cudaLaunchKernelEx(&cfg, dsa_paged_attention_kernel<D, BF16>, tq, tk, tv, p);
   if (e != cudaSuccess || !p.split) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 4);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(kSplitCtas, kJoinGroups);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, dsa_attention_join_kernel<D, BF16>, p);
@@ -934,7 +1049,7 @@ extern "C" {
 size_t dsa_paged_attention_workspace_bytes(int32_t T, int32_t B, int32_t H, int32_t Hkv,
                                            int32_t head_dim, int32_t max_context) {
   if (T < 1 || B < 1 || Hkv < 1 || H < Hkv || H % Hkv || H / Hkv > kRows || head_dim < 1) return 0;
-  if (!use_split(T, B, Hkv, kRows / (H / Hkv), max_context)) return 0;
+  if (!use_split(T, B, Hkv, head_dim, kRows / (H / Hkv), max_context)) return 0;
   return kMetaBytes + kMlBytes +
          2 * kSplitCtas * kRows * static_cast<size_t>(head_dim) * sizeof(float);
 }
@@ -1053,7 +1168,7 @@ dsa_status dsa_paged_attention(
   p.ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + kMetaBytes);
   p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kMetaBytes + kMlBytes);
   p.err = err_flags;
-  const long long grid = p.split ? kSplitCtas : items;
+  const long long grid = p.split || items > kSplitCtas ? kSplitCtas : items;
   const bool pdl = (flags & DSA_FLAG_PDL) != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;

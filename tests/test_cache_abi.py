@@ -145,5 +145,6 @@ def test_attention_workspace(lib):
     assert one == 304 * 16 + 608 * 128 * (8 + 4 * 128)
     assert f(64, 64, 64, 8, 64, 4096) == 304 * 16 + 608 * 128 * (8 + 4 * 64)
     assert f(1, 1, 64, 8, 128, 128) == 0      # one block: nothing to cut
-    assert f(8192, 1, 64, 8, 128, 8192) == 0  # items enough
+    assert f(8192, 1, 64, 8, 128, 8192) == one   # keys that L2 holds
+    assert f(8192, 1, 64, 8, 128, 65536) == 0    # whole items, one kv head at a time
     assert f(0, 1, 64, 8, 128, 4096) == f(1, 1, 64, 7, 128, 4096) == 0

@@ -71,11 +71,18 @@ def test_more_sequences_than_a_warp_scans_at_once():
     go(new, ctx, 8, 1, 64, page=16)
 
 
-def test_many_items_one_per_cta():
-    """More items than the split takes: the kernel runs one per CTA."""
+def test_many_sequences_and_kv_heads():
     new = [1 + i % 3 for i in range(160)]
     go(new, [n + (i * 37) % 300 for i, n in enumerate(new)], 32, 16, 64, page=32)
-    go([700, 513], [900, 600], 16, 16, 64, page=64)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (300, 70)])
+def test_whole_items(window, sinks):
+    """Many tiles over contexts that may pass L2: the CTAs take whole items."""
+    import prep_token_gb300 as dp
+    assert dp.dsa_paged_attention_workspace_bytes(10000, 3, 16, 16, 64, 200000) == 0
+    go([6000, 0, 4000], [6100, 0, 4000], 16, 16, 64, max_context=200000, window=window,
+       sinks=sinks, seed=20)
 
 
 @pytest.mark.parametrize("window,sinks", [(1, 0), (2, 1), (64, 0), (100, 4), (128, 128), (129, 300),
