@@ -20,7 +20,7 @@
 //   * warp 1 (one lane) issues S = Q K^T (M = N = 128, both operands in shared
 //     memory) and O += P V (A = P in TMEM over the columns of S, B = V in
 //     shared memory, read MN-major), and commits them to the mbarriers.
-//   * warps 2..5 own one row per thread: S from TMEM, the masks (in blocks at
+//   * one warpgroup per query tile owns one row per thread: S from TMEM, the masks (in blocks at
 //     an edge only), the maximum, the exponentials, P back to TMEM.  O is
 //     rescaled only when a maximum has grown by more than 2^8: until then P
 //     may exceed 1, at most by that factor, which fp32 and both 16-bit types
@@ -55,9 +55,21 @@ using namespace dsa_dev;
 constexpr int kRows = 128;          // MMA M: rows of a query tile
 constexpr int kKeys = 128;          // keys of a block
 constexpr int kUnitBytes = 16384;   // of the K/V ring
-constexpr int kAThreads = 6 * 32;   // loads, MMA, 4 softmax warps
-constexpr int kTmemCols = 256;      // S / P: 128, O: D
-constexpr int kSplitCtas = 304;     // two CTAs on each of 152 SMs
+constexpr int kSms = 152;
+// A CTA works on QT query tiles of 128 rows that share the loaded keys: one
+// tile and two CTAs per SM, or two tiles and one CTA.  Either way an SM holds
+// 256 rows.
+template <int QT>
+struct Shape {
+  static constexpr int kThreads = (1 + QT) * 128;  // loads, MMA, 2 idle warps; softmax
+  // Registers: the launch's share per thread is 128 (two CTAs of 256 threads)
+  // or 168 (one of 384); the first warpgroup gives some to the others.
+  static constexpr int kRegsFew = QT == 1 ? 64 : 88;
+  static constexpr int kRegsMany = QT == 1 ? 192 : 208;
+  static_assert(kRegsFew + QT * kRegsMany <= (1 + QT) * (QT == 1 ? 128 : 168), "registers");
+  static constexpr int kCtas = 2 / QT * kSms;
+  static constexpr int kTmemCols = 256 * QT;          // per tile: S / P 128, O D
+};
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLn2 = 0.693147180559945309f;
 
@@ -69,14 +81,16 @@ struct AParams {
   float* lse;
   long long bt_stride, out_stride_t, out_stride_h;
   int num_pages, page, box;  // box: keys per TMA box, min(page, 64)
-  int T, B, Hkv, G, tile_tokens;
+  int T, B, Hkv, G;
+  int q_tokens;     // tokens of a query tile, floor(128 / G)
+  int tile_tokens;  // tokens of a work item, QT * q_tokens
   int max_context;
   int window, sinks;  // window 0: none
   float c;            // scale * log2(e)
   int split;          // 1: equal shares of the key blocks; 0: whole items, gridDim.x apart
-  int4* meta;         // split: [kSplitCtas] the item that CTA leaves to later ones
-  float2* ml;         // split: [2 * kSplitCtas][kRows] (log2 of the scale, l) of a part
-  float* part;        // split: [2 * kSplitCtas][kRows][D] O of a part
+  int4* meta;         // split: [CTAs] the item that CTA leaves to later ones
+  float2* ml;         // split: [2 * CTAs][QT * kRows] (log2 of the scale, l) of a part
+  float* part;        // split: [2 * CTAs][QT * kRows][D] O of a part
   int* err;
 };
 
@@ -104,11 +118,13 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
-// mbar_wait with probes that the hardware ends early: the softmax and the
+// mbar_wait, with probes that the hardware ends early (the softmax and the
 // matrix products hand over to each other three times per key block, and a
-// thread that asked for a long sleep wakes late.
+// thread that asked for a long sleep wakes late) and without a function call,
+// across which the registers of a row would have to be saved.
 __device__ __forceinline__ bool wait_soon(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  for (int i = 0; i < 64; ++i) {
+  unsigned long long t0 = 0;
+  for (unsigned i = 1;; ++i) {
     uint32_t ok;
     asm volatile(
         "{\n .reg .pred p;\n"
@@ -116,20 +132,31 @@ __device__ __forceinline__ bool wait_soon(uint32_t bar, uint32_t parity, volatil
         " selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     if (ok) return true;
+    if (i % 64 == 0) {
+      const unsigned long long t = global_ns();
+      if (t0 == 0) t0 = t;
+      if (*abort_flag || t - t0 > kWaitLimitNs) return false;
+    }
   }
-  return mbar_wait_slow(bar, parity, abort_flag);
 }
 
 // Shared-memory matrix descriptor of 128-byte-swizzled rows: 8-row groups of
 // 1024 bytes (the stride offset).  `lead` is the distance of 64-element panels
 // of an MN-major operand (unused K-major).
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t smem_addr, uint32_t lead) {
-  uint64_t d = static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>((lead >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;  // version
-  d |= static_cast<uint64_t>(2) << 61;  // 128-byte swizzle
-  return d;
+// The low word moves with the address, 16 bytes to a step; the high one does not.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr, uint32_t lead) {
+  return ((smem_addr >> 4) & 0x3FFFu) | ((lead >> 4) & 0x3FFFu) << 16;
+}
+__device__ __forceinline__ uint64_t make_desc(uint32_t lo) {
+  constexpr uint32_t hi = (1024 >> 4) | 1u << 14 /* version */ | 2u << 29 /* swizzle */;
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(is));
+  return is != 0;
 }
 
 // Instruction descriptor: D fp32, A and B fp16 or bf16, A K-major.
@@ -200,16 +227,24 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
       : "r"(taddr) : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0],"
-      " {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+      " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr) : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
+      " {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
       ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
         "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
-        "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
-        "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 
@@ -236,7 +271,7 @@ __device__ __forceinline__ uint64_t below(int n) {
 
 // ---------------------------------------------------------------- work items
 
-// One query tile of a sequence and the key blocks that some row of it sees.
+// One work item of a sequence and the key blocks that some row of it sees.
 struct Tile {
   int token0, tokens;  // in q; tokens of the tile
   int pos0;            // position of its first token
@@ -444,36 +479,55 @@ __device__ __forceinline__ bool seek(const AParams& p, Cursor& c, const Share& s
 
 // ---------------------------------------------------------------- the kernel
 
-template <int D>
+// What the load warp tells the others about a segment, in shared memory.
+struct Segment {
+  int begin, end;  // key blocks of the tile; end -1: there is no more work
+  int sink_blocks, main_block, blocks;
+  int hi, lo;
+  int pos0, tokens, token0, h;
+  int last_cta;    // of an item that starts here and goes on, else -1
+};
+// The load warp is at most two segments ahead of the slowest reader: it
+// passes on when the last scores of a segment are done, and those of the next
+// one wait for the softmax of this one.
+constexpr int kSegments = 4;
+
+template <int D, int QT>
 struct ASmem {
   static constexpr int kPanels = D / 64;                    // 128-byte panels of a row
-  static constexpr int kQBytes = kRows * D * 2;
-  static constexpr int kStages = (114688 - kQBytes) / kUnitBytes;  // 5 or 6 units
+  static constexpr int kTileBytes = kRows * D * 2;          // a query tile
+  static constexpr int kQBytes = QT * kTileBytes;
+  // units of the ring: 5 or 6 with two CTAs per SM, 10 or 12 with one
+  static constexpr int kStages = ((QT == 1 ? 114688 : 229376) - kQBytes) / kUnitBytes;
   static constexpr int kVKeys = kKeys / kPanels;            // keys of a V unit
   static constexpr int kOffRing = kQBytes;
-  static constexpr int kOffBar = kOffRing + kStages * kUnitBytes;
-  // barriers: full[S], empty[S], qfull, qempty, sfull, pready[2], ofull, drain
-  static constexpr int kBars = 2 * kStages + 7;
+  static constexpr int kOffSeg = kOffRing + kStages * kUnitBytes;
+  static constexpr int kOffBar = kOffSeg + kSegments * static_cast<int>(sizeof(Segment));
+  // barriers: full[S], empty[S], qfull, qempty, drain, segment[4], then per
+  // query tile sfull, pready[2], ofull
+  static constexpr int kBars = 2 * kStages + 3 + kSegments + 4 * QT;
   static constexpr int kOffTmem = kOffBar + 8 * kBars;
   static constexpr int kOffAbort = kOffTmem + 4;
   static constexpr int kBytes = kOffAbort + 4;
+  static_assert(kBytes <= (QT == 1 ? 115712 : 232448), "shared memory of an SM");
 };
 
-// The shared-memory rows of the keys of box l of a block, `rows` of 128 bytes
-// in each of `panels` panels, set to `word` by the whole warp.
+// `rows` shared-memory rows of 128 bytes from `at` set to `word` by a warp.
 __device__ __forceinline__ void fill_rows(uint32_t at, int rows, uint32_t word) {
   for (int i = threadIdx.x & 31; i < rows * 8; i += 32)
     asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + 16 * i), "r"(word)
                  : "memory");
 }
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kAThreads, 2)
+template <int D, bool BF16, int QT>
+__global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
     dsa_paged_attention_kernel(const __grid_constant__ CUtensorMap tq,
                                const __grid_constant__ CUtensorMap tk,
-                               const __grid_constant__ CUtensorMap tv, const AParams p) {
-  using L = ASmem<D>;
+                               const __grid_constant__ CUtensorMap tv,
+                               const __grid_constant__ AParams p) {
+  using L = ASmem<D, QT>;
   constexpr int S = L::kStages;
+  constexpr int kP = L::kPanels;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {  // the swizzled tiles need this alignment
@@ -484,10 +538,14 @@ __global__ void __launch_bounds__(kAThreads, 2)
   auto full = [&](int s) { return bar0 + 8 * s; };
   auto empty = [&](int s) { return bar0 + 8 * (S + s); };
   const uint32_t qfull = bar0 + 8 * (2 * S), qempty = bar0 + 8 * (2 * S + 1);
-  const uint32_t sfull = bar0 + 8 * (2 * S + 2);
-  auto pready = [&](int half) { return bar0 + 8 * (2 * S + 3 + half); };
-  const uint32_t ofull = bar0 + 8 * (2 * S + 5), drain = bar0 + 8 * (2 * S + 6);
+  const uint32_t drain = bar0 + 8 * (2 * S + 2);
+  auto segment_ready = [&](int i) { return bar0 + 8 * (2 * S + 3 + i % kSegments); };
+  constexpr int kB = 2 * S + 3 + kSegments;
+  auto sfull = [&](int j) { return bar0 + 8 * (kB + 4 * j); };
+  auto pready = [&](int j, int half) { return bar0 + 8 * (kB + 1 + 4 * j + half); };
+  auto ofull = [&](int j) { return bar0 + 8 * (kB + 3 + 4 * j); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffAbort);
+  Segment* const segments = reinterpret_cast<Segment*>(smem + L::kOffSeg);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
@@ -503,23 +561,27 @@ __global__ void __launch_bounds__(kAThreads, 2)
     }
     mbar_init(qfull, 1);
     mbar_init(qempty, 1);
-    mbar_init(sfull, 1);
-    for (int h = 0; h < 2; ++h) mbar_init(pready(h), 4);  // the softmax warps
-    mbar_init(ofull, 1);
     mbar_init(drain, 1);
+    for (int i = 0; i < kSegments; ++i) mbar_init(segment_ready(i), 1);
+    for (int j = 0; j < QT; ++j) {
+      mbar_init(sfull(j), 1);
+      for (int h = 0; h < 2; ++h) mbar_init(pready(j, h), 4);  // the tile's softmax warps
+      mbar_init(ofull(j), 1);
+    }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                 ::"r"(sbase + L::kOffTmem), "n"(kTmemCols) : "memory");
+                 ::"r"(sbase + L::kOffTmem), "n"(Shape<QT>::kTmemCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kOffTmem);
-  const uint32_t tmem_o = tmem + kKeys;
+  auto tmem_s = [&](int j) { return tmem + j * kKeys; };
+  auto tmem_o = [&](int j) { return tmem + QT * kKeys + j * D; };
 
   grid_dependency_wait();
   grid_launch_dependents();
@@ -529,242 +591,261 @@ __global__ void __launch_bounds__(kAThreads, 2)
     if (p.err) atomicOr(p.err, DSA_DEVERR_TIMEOUT);
   };
 
-  Cursor c;
-  Share share = {0, 0, 0, 0};
-  bool more = first_segment(p, c, share);
-  if (p.split && threadIdx.x == 64) p.meta[blockIdx.x].x = -1;
-
-  if (warp == 0) {
-    // ------------------------------------------------ loads
-    const int boxes = kKeys / p.box;
-    const uint32_t box_bytes = static_cast<uint32_t>(p.box) * 128u;  // of one panel
-    int unit = 0, seg = 0;
-    bool ok = true;
-    // waits until the ring's next unit may be written
-    auto acquire = [&]() {
-      const int s = unit % S;
-      ok = ok && (unit < S || wait_soon(empty(s), ((unit / S) & 1) ^ 1, abort_flag));
-      ok = __all_sync(kFull, ok);
-      return s;
-    };
-    for (; more && ok; more = next_segment(p, c, share), ++seg) {
-      const Tile& tile = c.tile;
-      // box l of a block: its page, -1 if no row sees any of its keys, -2 if
-      // the table names no page of the pool for it
-      const int* table = p.block_table + c.b * p.bt_stride;
-      auto lookup = [&](int k) {
-        const int key = tile.block(k) * kKeys + lane * p.box;
-        if (lane >= boxes || key >= tile.hi || (key + p.box <= tile.lo && key >= p.sinks)) return -1;
-        const int page = __ldg(table + key / p.page);
-        return page >= 0 && page < p.num_pages ? page : -2;
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape<QT>::kRegsFew));
+    if (warp == 0) {
+      // ---------------------------------------------- loads
+      Cursor c = {};
+      Share share = {0, 0, 0, 0};
+      bool more = first_segment(p, c, share);
+      if (p.split && lane == 0) p.meta[blockIdx.x].x = -1;
+      const int boxes = kKeys / p.box;
+      const uint32_t box_bytes = static_cast<uint32_t>(p.box) * 128u;  // of one panel
+      int slot = 0, units = 0, queries = 0;  // the ring's next place; what was loaded
+      uint32_t phase = 1;                    // parity of the place's last release
+      bool ok = true;
+      // waits until the ring's next unit may be written, and passes on
+      auto acquire = [&]() {
+        const int s = slot;
+        ok = ok && (units < S || wait_soon(empty(s), phase, abort_flag));
+        ok = __all_sync(kFull, ok);
+        if (ok) {
+          ++units;
+          if (++slot == S) slot = 0, phase ^= 1;
+        }
+        return s;
       };
-      if (seg > 0) ok = __all_sync(kFull, wait_soon(qempty, (seg & 1) ^ 1, abort_flag));
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(qfull, L::kPanels * p.G * p.tile_tokens * 128);
-        for (int pn = 0; pn < L::kPanels; ++pn)
-          tma_load_3d(sbase + pn * kRows * 128, &tq, pn * 64, c.h * p.G, tile.token0, qfull);
-      }
-      int page = lookup(c.begin);
-      for (int k = c.begin; k < c.end && ok; ++k) {
-        const int in_page = (tile.block(k) * kKeys + lane * p.box) % p.page;
-        const int next = k + 1 < c.end ? lookup(k + 1) : -1;
-        const unsigned loaded = __ballot_sync(kFull, page >= 0);
-        const unsigned bad = __ballot_sync(kFull, page == -2);
-        const unsigned gone = ~loaded & (boxes == 32 ? kFull : (1u << boxes) - 1u);
-        if (bad && lane == 0 && p.err) atomicOr(p.err, DSA_DEVERR_SLOT);
-        for (int pn = 0; pn < L::kPanels; ++pn, ++unit) {  // K: 64 dims of all 128 keys
-          const int s = acquire();
-          if (!ok) break;
-          const uint32_t at = sbase + L::kOffRing + s * kUnitBytes;
-          if (bad && pn == 0) {  // NaN keys, so the rows that see them become NaN
-            for (unsigned m = bad; m; m &= m - 1)
-              fill_rows(at + (__ffs(m) - 1) * box_bytes, p.box, 0x7fff7fffu);
-            fence_async_shared();
-            __syncwarp();
+      for (int seg = 0;; ++seg) {
+        if (seg > 0) ok = __all_sync(kFull, wait_soon(qempty, (seg & 1) ^ 1, abort_flag));
+        if (!ok) break;
+        const Tile& tile = c.tile;
+        if (lane == 0) {
+          Segment& g = segments[seg % kSegments];
+          g.begin = c.begin;
+          g.end = more ? c.end : -1;
+          g.sink_blocks = tile.sink_blocks;
+          g.main_block = tile.main_block;
+          g.blocks = tile.blocks;
+          g.hi = tile.hi;
+          g.lo = tile.lo;
+          g.pos0 = tile.pos0;
+          g.tokens = tile.tokens;
+          g.token0 = tile.token0;
+          g.h = c.h;
+          g.last_cta = -1;
+          if (more && p.split && c.begin == 0 && c.end < tile.blocks) {
+            const long long last = share.end - 1 + (tile.blocks - c.end);  // its last key block
+            g.last_cta = static_cast<int>(((last + 1) * share.ctas - 1) / share.total);
           }
-          if (lane == 0) mbar_arrive_expect_tx(full(s), __popc(loaded) * box_bytes);
-          __syncwarp();
-          if (page >= 0)
-            tma_load_4d(at + lane * box_bytes, &tk, pn * 64, in_page, c.h, page, full(s));
-        }
-        for (int u = 0; u < L::kPanels && ok; ++u, ++unit) {  // V: all dims of kVKeys keys
-          const int s = acquire();
-          if (!ok) break;
-          const uint32_t at = sbase + L::kOffRing + s * kUnitBytes;
-          const int per = L::kVKeys / p.box;  // boxes of the unit
-          const unsigned here = (per == 32 ? kFull : (1u << per) - 1u) << (u * per);
-          if (gone & here) {  // P is 0 there, and 0 * V must not be NaN
-            for (unsigned m = gone & here; m; m &= m - 1)
-              for (int pn = 0; pn < L::kPanels; ++pn)
-                fill_rows(at + pn * L::kVKeys * 128 + (__ffs(m) - 1 - u * per) * box_bytes, p.box, 0u);
-            fence_async_shared();
-            __syncwarp();
+          mbar_arrive(segment_ready(seg));
+          if (more) {
+            mbar_arrive_expect_tx(qfull, QT * kP * p.G * p.q_tokens * 128);
+            for (int j = 0; j < QT; ++j)
+              for (int pn = 0; pn < kP; ++pn)
+                tma_load_3d(sbase + j * L::kTileBytes + pn * kRows * 128, &tq, pn * 64, c.h * p.G,
+                            tile.token0 + j * p.q_tokens, qfull);
           }
-          if (lane == 0)
-            mbar_arrive_expect_tx(full(s), L::kPanels * __popc(loaded & here) * box_bytes);
-          __syncwarp();
-          if (page >= 0 && lane / per == u)
-            for (int pn = 0; pn < L::kPanels; ++pn)
-              tma_load_4d(at + pn * L::kVKeys * 128 + (lane - u * per) * box_bytes, &tv, pn * 64,
-                          in_page, c.h, page, full(s));
         }
-        page = next;
-      }
-    }
-    if (!ok && lane == 0) give_up();
-    // stay until every load issued has landed
-    volatile int never = 0;
-    for (int d = (unit > S ? unit - S : 0); d < unit; ++d)
-      mbar_wait(full(d % S), (d / S) & 1, &never);
-    if (seg > 0) mbar_wait(qfull, (seg - 1) & 1, &never);
-  } else if (warp == 1) {
-    // ------------------------------------------------ MMA issuer
-    constexpr uint32_t idesc_s = mma_idesc(BF16, false, kKeys);
-    constexpr uint32_t idesc_o = mma_idesc(BF16, true, D);
-    int unit = 0, seg = 0, blk = 0;
-    bool ok = true;
-    for (; more && ok; more = next_segment(p, c, share), ++seg) {
-      if (lane == 0) {
-        ok = wait_soon(qfull, seg & 1, abort_flag);
-        for (int k = c.begin; k < c.end && ok; ++k, ++blk) {
-          for (int pn = 0; pn < L::kPanels && ok; ++pn, ++unit) {
-            const int s = unit % S;
-            ok = wait_soon(full(s), (unit / S) & 1, abort_flag);
+        __syncwarp();
+        if (!more) break;
+        ++queries;
+        // box l of a block: its page, -1 if no row sees any of its keys, -2 if
+        // the table names no page of the pool for it
+        const int* table = p.block_table + c.b * p.bt_stride;
+        auto lookup = [&](int k) {
+          const int key = tile.block(k) * kKeys + lane * p.box;
+          if (lane >= boxes || key >= tile.hi || (key + p.box <= tile.lo && key >= p.sinks))
+            return -1;
+          const int page = __ldg(table + key / p.page);
+          return page >= 0 && page < p.num_pages ? page : -2;
+        };
+        int page = lookup(c.begin);
+        for (int k = c.begin; k < c.end && ok; ++k) {
+          const int in_page = (tile.block(k) * kKeys + lane * p.box) % p.page;
+          const int next = k + 1 < c.end ? lookup(k + 1) : -1;
+          const unsigned loaded = __ballot_sync(kFull, page >= 0);
+          const unsigned bad = __ballot_sync(kFull, page == -2);
+          const unsigned gone = ~loaded & ((1u << boxes) - 1u);
+          if (bad && lane == 0 && p.err) atomicOr(p.err, DSA_DEVERR_SLOT);
+          for (int pn = 0; pn < kP; ++pn) {  // K: 64 dims of all 128 keys
+            const int s = acquire();
             if (!ok) break;
-            tc_fence_after();
-            const uint64_t a = sw128_desc(sbase + pn * kRows * 128, 0);
-            const uint64_t b = sw128_desc(sbase + L::kOffRing + s * kUnitBytes, 0);
+            const uint32_t at = sbase + L::kOffRing + s * kUnitBytes;
+            if (bad && pn == 0) {  // NaN keys, so the rows that see them become NaN
+              for (unsigned m = bad; m; m &= m - 1)
+                fill_rows(at + (__ffs(m) - 1) * box_bytes, p.box, 0x7fff7fffu);
+              fence_async_shared();
+              __syncwarp();
+            }
+            if (lane == 0) mbar_arrive_expect_tx(full(s), __popc(loaded) * box_bytes);
+            __syncwarp();
+            if (page >= 0)
+              tma_load_4d(at + lane * box_bytes, &tk, pn * 64, in_page, c.h, page, full(s));
+          }
+          for (int u = 0; u < kP && ok; ++u) {  // V: all dims of kVKeys keys
+            const int s = acquire();
+            if (!ok) break;
+            const uint32_t at = sbase + L::kOffRing + s * kUnitBytes;
+            const int per = L::kVKeys / p.box;  // boxes of the unit
+            const unsigned here = ((1u << per) - 1u) << (u * per);
+            if (gone & here) {  // P is 0 there, and 0 * V must not be NaN
+              for (unsigned m = gone & here; m; m &= m - 1)
+                for (int pn = 0; pn < kP; ++pn)
+                  fill_rows(at + pn * L::kVKeys * 128 + (__ffs(m) - 1 - u * per) * box_bytes, p.box,
+                            0u);
+              fence_async_shared();
+              __syncwarp();
+            }
+            if (lane == 0) mbar_arrive_expect_tx(full(s), kP * __popc(loaded & here) * box_bytes);
+            __syncwarp();
+            if (page >= 0 && lane / per == u)
+              for (int pn = 0; pn < kP; ++pn)
+                tma_load_4d(at + pn * L::kVKeys * 128 + (lane - u * per) * box_bytes, &tv, pn * 64,
+                            in_page, c.h, page, full(s));
+          }
+          page = next;
+        }
+        if (!ok) break;
+        more = next_segment(p, c, share);
+      }
+      if (!ok && lane == 0) give_up();
+      volatile int never = 0;  // stay until every load issued has landed
+      for (int d = units > S ? units - S : 0; d < units; ++d)
+        wait_soon(full(d % S), (d / S) & 1, &never);
+      if (queries > 0) wait_soon(qfull, (queries - 1) & 1, &never);
+    } else if (warp == 1) {
+      // ---------------------------------------------- MMA issuer
+      // Query tile j's scores of block k + 1 follow its P V of block k at once:
+      // the other tile's softmax runs meanwhile.  Products issued by one thread
+      // are carried out in their order, so S may be overwritten behind P V.  The
+      // warp stays together, one lane issues, and the ring's places are counted,
+      // not divided: at three hand-overs a block this code's own time counts.
+      constexpr uint32_t idesc_s = mma_idesc(BF16, false, kKeys);
+      constexpr uint32_t idesc_o = mma_idesc(BF16, true, D);
+      const bool leader = elect_one();
+      const uint32_t q_lo = desc_lo(sbase, 0);
+      const uint32_t k_lo = desc_lo(sbase + L::kOffRing, 0);
+      const uint32_t v_lo = desc_lo(sbase + L::kOffRing, L::kVKeys * 128);
+      int slot = 0;                        // ring place of the block's first K unit
+      uint32_t phase = 0, parity = 0;      // its parity; the blocks' parity
+      bool ok = true;
+      auto arrived = [&](int unit) {       // the unit-th one from the block's first
+        int s = slot + unit;
+        uint32_t ph = phase;
+        if (s >= S) s -= S, ph ^= 1;
+        ok = wait_soon(full(s), ph, abort_flag) && ok;
+        return s;
+      };
+      auto scores = [&](int j, int unit) {  // S_j = Q_j K^T
+#pragma unroll
+        for (int pn = 0; pn < kP; ++pn) {
+          const int s = arrived(unit + pn);
+          tc_fence_after();
+          if (leader && ok) {
+            const uint32_t a = q_lo + ((j * L::kTileBytes + pn * kRows * 128) >> 4);
+            const uint32_t b = k_lo + s * (kUnitBytes >> 4);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_ss(tmem, a + 2 * ks, b + 2 * ks, idesc_s, pn + ks > 0 ? 1u : 0u);
-            mma_commit(empty(s));
+              mma_ss(tmem_s(j), make_desc(a + 2 * ks), make_desc(b + 2 * ks), idesc_s,
+                     pn + ks > 0 ? 1u : 0u);
+            if (j + 1 == QT) mma_commit(empty(s));
           }
-          if (!ok) break;
-          mma_commit(sfull);
-          if (k + 1 == c.end) mma_commit(qempty);
-          for (int half = 0; half < 2 && ok; ++half) {  // of the block's keys
-            const int u = half * L::kPanels / 2;        // its V unit of the block
-            const int s = (unit + u) % S;
-            ok = wait_soon(pready(half), blk & 1, abort_flag) &&
-                 wait_soon(full(s), ((unit + u) / S) & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            const int row = half * (kKeys / 2) - u * L::kVKeys;  // its first key in the unit
-            const uint64_t b = sw128_desc(sbase + L::kOffRing + s * kUnitBytes + row * 128,
-                                          L::kVKeys * 128);
-#pragma unroll
-            for (int ks = 0; ks < kKeys / 32; ++ks)
-              mma_ts(tmem_o, tmem + half * (kKeys / 4) + ks * 8, b + ks * (2048 >> 4), idesc_o,
-                     (k > c.begin || half + ks > 0) ? 1u : 0u);
-            if (L::kPanels == 2 || half == 1) mma_commit(empty(s));
-          }
-          unit += L::kPanels;
         }
-        if (ok) mma_commit(ofull);
+        if (leader && ok) mma_commit(sfull(j));
+      };
+      for (int seg = 0; ok; ++seg) {
+        ok = __all_sync(kFull, wait_soon(segment_ready(seg), (seg / kSegments) & 1, abort_flag));
+        const int begin = segments[seg % kSegments].begin, end = segments[seg % kSegments].end;
+        if (!ok || end < 0) break;
+        ok = wait_soon(qfull, seg & 1, abort_flag);
+#pragma unroll
+        for (int j = 0; j < QT; ++j) scores(j, 0);
+        if (leader && ok && begin + 1 == end) mma_commit(qempty);
+        for (int k = begin; k < end; ++k) {
+#pragma unroll
+          for (int j = 0; j < QT; ++j) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {   // of the block's keys
+              const int u = half * kP / 2;           // its V unit of the block
+              ok = wait_soon(pready(j, half), parity, abort_flag) && ok;
+              const int s = arrived(kP + u);
+              tc_fence_after();
+              if (leader && ok) {
+                const int row = half * (kKeys / 2) - u * L::kVKeys;  // its first key in the unit
+                const uint32_t b = v_lo + s * (kUnitBytes >> 4) + (row * 128 >> 4);
+#pragma unroll
+                for (int ks = 0; ks < kKeys / 32; ++ks)
+                  mma_ts(tmem_o(j), tmem_s(j) + half * (kKeys / 4) + ks * 8,
+                         make_desc(b + ks * (2048 >> 4)), idesc_o,
+                         (k > begin || half + ks > 0) ? 1u : 0u);
+                if (j + 1 == QT && (kP == 2 || half == 1)) mma_commit(empty(s));
+              }
+            }
+            if (k + 1 < end)
+              scores(j, 2 * kP);
+            else if (leader && ok)
+              mma_commit(ofull(j));
+          }
+          if (leader && ok && k + 2 == end) mma_commit(qempty);
+          parity ^= 1;
+          slot += 2 * kP;
+          if (slot >= S) slot -= S, phase ^= 1;
+          ok = __all_sync(kFull, ok);
+          if (!ok) break;
+        }
       }
-      ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
-    }
-    if (lane == 0) {
-      if (!ok) give_up();
-      // every MMA issued must finish before TMEM is released
-      mma_commit(drain);
+      if (!ok && lane == 0) give_up();
+      if (leader) mma_commit(drain);  // every MMA issued must finish before TMEM is released
       volatile int never = 0;
-      mbar_wait(drain, 0, &never);
+      wait_soon(drain, 0, &never);
     }
   } else {
-    // ------------------------------------------------ softmax (warps 2..5)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Shape<QT>::kRegsMany));
+    // ------------------------------------------------ softmax
+    const int j = QT == 1 ? 0 : (warp - 4) >> 2;  // the query tile
     const int sub = warp & 3;           // the TMEM lanes this warp may touch
-    const int row = 32 * sub + lane;    // of the tile
-    const uint32_t t_s = tmem + (static_cast<uint32_t>(32 * sub) << 16);
-    const uint32_t t_o = tmem_o + (static_cast<uint32_t>(32 * sub) << 16);
+    const int row = 32 * sub + lane;    // of the query tile
+    const uint32_t t_s = tmem_s(j) + (static_cast<uint32_t>(32 * sub) << 16);
+    const uint32_t t_o = tmem_o(j) + (static_cast<uint32_t>(32 * sub) << 16);
     // what the exponents are taken against, in powers of two
     auto reference = [&](float m) { return (m == -INFINITY ? 0.0f : m * p.c) - (BF16 ? 0.0f : 7.0f); };
-    const int tok = row / p.G, head = row - tok * p.G;
-    int seg = 0, blk = 0;
+    const int tok = j * p.q_tokens + row / p.G;   // of the item
+    int slot = kP;                      // ring place of the block's first V unit
+    uint32_t phase = 0, parity = 0;     // its parity; the blocks' parity
     bool ok = true;
-    for (; more && ok; more = next_segment(p, c, share), ++seg) {
-      const Tile& tile = c.tile;
-      const bool mine = tok < tile.tokens;                 // this row exists
-      const bool busy = 32 * sub < tile.tokens * p.G;      // some row of the warp does
-      const int pos = tile.pos0 + tok;
+    for (int seg = 0; ok; ++seg) {
+      ok = __all_sync(kFull, wait_soon(segment_ready(seg), (seg / kSegments) & 1, abort_flag));
+      const Segment& g = segments[seg % kSegments];
+      if (!ok || g.end < 0) break;
+      const int tokens = min(p.q_tokens, g.tokens - j * p.q_tokens);  // of the query tile
+      const bool mine = row < tokens * p.G;                // this row exists
+      const bool busy = 32 * sub < tokens * p.G;           // some row of the warp does
+      const int pos = g.pos0 + tok;
       const int hi = mine ? pos + 1 : 0;                   // keys [lo, hi) and [0, sinks)
       const int lo = p.window ? max(0, pos - p.window + 1) : 0;
       // keys that every existing row of the warp sees
       const int hi_all = __reduce_min_sync(kFull, mine ? hi : 0x7fffffff);
       const int lo_all = __reduce_max_sync(kFull, mine ? lo : 0);
       float m = -INFINITY, l = 0.0f;  // m is the maximum that P and O are scaled by
-      for (int k = c.begin; k < c.end; ++k, ++blk) {
-        const int key0 = tile.block(k) * kKeys;
-        ok = __all_sync(kFull, wait_soon(sfull, blk & 1, abort_flag));
+      const int begin = g.begin, end = g.end;
+      for (int k = begin; k < end; ++k) {
+        const int key0 = (k < g.sink_blocks ? k : g.main_block + k - g.sink_blocks) * kKeys;
+        ok = __all_sync(kFull, wait_soon(sfull(j), parity, abort_flag));
         if (!ok) break;
         tc_fence_after();
-        // S in halves of 64 keys, read twice: for the maximum, then for P.
-        // (All 128 values at once do not fit in the 168 registers that two
-        // CTAs per SM leave a thread.)
-        const bool all = key0 + kKeys <= hi_all && (key0 >= lo_all || key0 + kKeys <= p.sinks);
-        float s[kKeys / 2];
-        auto load_half = [&](int half) {
-          tmem_ld32(t_s + half * 64, s);
-          tmem_ld32(t_s + half * 64 + 32, s + 32);
-          tmem_wait_ld(s);
-          if (!all) {
-            const int at = key0 + half * 64;
-            const uint64_t seen = below(hi - at) & (~below(lo - at) | below(p.sinks - at));
-            const uint32_t bits[2] = {static_cast<uint32_t>(seen), static_cast<uint32_t>(seen >> 32)};
-#pragma unroll
-            for (int i = 0; i < kKeys / 2; ++i)
-              s[i] = bits[i / 32] & (1u << (i % 32)) ? s[i] : -INFINITY;
-          }
-        };
-        float mc = 0.0f;
-        if (busy) {
-          float m_new = m;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            load_half(half);
-            float mx[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mx[j] = s[j];
-#pragma unroll
-            for (int i = 4; i < kKeys / 2; i += 8)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                mx[j] = i + 4 < kKeys / 2 ? max3f(mx[j], s[i + j], s[i + 4 + j]) : fmaxf(mx[j], s[i + j]);
-            m_new = max3f(m_new, fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          }
-          // -inf - -inf is NaN and compares false: nothing was summed yet
-          const bool grown = (m_new - m) * p.c > kRescaleLog2;
-          if (k == c.begin) {
-            m = m_new;
-          } else if (__any_sync(kFull, grown)) {
-            const float f = grown ? exp2_approx((m - m_new) * p.c) : 1.0f;
-            m = grown ? m_new : m;
-            l *= f;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-              float o[32];
-              tmem_ld32(t_o + 32 * i, o);
-              tmem_wait_ld(o);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] *= f;
-              tmem_st32(t_o + 32 * i, reinterpret_cast<uint32_t*>(o));
-            }
-          }
-          mc = reference(m);
-        }
-        // V rows of a loaded page that no row of the tile sees (behind the
+        // V rows of a loaded page that no row of the item sees (behind the
         // context, before the window): whatever they hold, 0 * it must be 0.
-        const bool inside = key0 + kKeys <= tile.hi && (key0 >= tile.lo || key0 + kKeys <= p.sinks);
-        if (!inside) {
+        // Tile 0's P V comes first, and waits for this.
+        if (j == 0 && !(key0 + kKeys <= g.hi && (key0 >= g.lo || key0 + kKeys <= p.sinks))) {
           const int key = key0 + row;
-          if (!(key < tile.hi && (key >= tile.lo || key < p.sinks))) {
-            const int unit = (2 * blk + 1) * L::kPanels + row / L::kVKeys;
-            ok = wait_soon(full(unit % S), (unit / S) & 1, abort_flag);
-            const uint32_t at = sbase + L::kOffRing + (unit % S) * kUnitBytes +
-                                (row % L::kVKeys) * 128;
+          if (!(key < g.hi && (key >= g.lo || key < p.sinks))) {
+            int s = slot + row / L::kVKeys;
+            uint32_t ph = phase;
+            if (s >= S) s -= S, ph ^= 1;
+            ok = wait_soon(full(s), ph, abort_flag);
+            const uint32_t at = sbase + L::kOffRing + s * kUnitBytes + (row % L::kVKeys) * 128;
 #pragma unroll
-            for (int pn = 0; pn < L::kPanels; ++pn)
+            for (int pn = 0; pn < kP; ++pn)
 #pragma unroll
               for (int i = 0; i < 8; ++i)
                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};"
@@ -774,78 +855,139 @@ __global__ void __launch_bounds__(kAThreads, 2)
           ok = __all_sync(kFull, ok);
           if (!ok) break;
         }
+        // The row's 128 scores stay in registers from the maximum to P.
+        const bool all = key0 + kKeys <= hi_all && (key0 >= lo_all || key0 + kKeys <= p.sinks);
+        float s[2][kKeys / 2];
+        float mc = 0.0f;
+        if (busy) {
+          float m_new = m;
+          tmem_ld32(t_s, s[0]);
+          tmem_ld32(t_s + 32, s[0] + 32);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            tmem_wait_ld(s[half]);
+            if (half == 0) {
+              tmem_ld32(t_s + 64, s[1]);
+              tmem_ld32(t_s + 96, s[1] + 32);
+            }
+            if (!all) {
+              const int at = key0 + half * 64;
+              const uint64_t seen = below(hi - at) & (~below(lo - at) | below(p.sinks - at));
+              const uint32_t bits[2] = {static_cast<uint32_t>(seen),
+                                        static_cast<uint32_t>(seen >> 32)};
+#pragma unroll
+              for (int i = 0; i < kKeys / 2; ++i)
+                s[half][i] = bits[i / 32] & (1u << (i % 32)) ? s[half][i] : -INFINITY;
+            }
+            float mx[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx[i] = s[half][i];
+#pragma unroll
+            for (int i = 4; i < kKeys / 2; i += 8)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                mx[q] = i + 4 < kKeys / 2 ? max3f(mx[q], s[half][i + q], s[half][i + 4 + q])
+                                          : fmaxf(mx[q], s[half][i + q]);
+            m_new = max3f(m_new, fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          }
+          // -inf - -inf is NaN and compares false: nothing was summed yet
+          const bool grown = (m_new - m) * p.c > kRescaleLog2;
+          if (k == begin) {
+            m = m_new;
+          } else if (__any_sync(kFull, grown)) {
+            const float f = grown ? exp2_approx((m - m_new) * p.c) : 1.0f;
+            m = grown ? m_new : m;
+            l *= f;
+#pragma unroll 1
+            for (int i = 0; i < D / 16; ++i) {
+              float o[16];
+              tmem_ld16(t_o + 16 * i, o);
+              tmem_wait_ld(o);
+#pragma unroll
+              for (int q = 0; q < 16; ++q) o[q] *= f;
+              tmem_st16(t_o + 16 * i, reinterpret_cast<uint32_t*>(o));
+            }
+          }
+          mc = reference(m);
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (busy) {
-            load_half(half);
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            uint32_t w[kKeys / 4];
+            const float2 c2 = make_float2(p.c, p.c), mc2 = make_float2(-mc, -mc);
+            float2 sum[2] = {};
 #pragma unroll
-            for (int i = 0; i < kKeys / 2; i += 2) {
-              const float a = exp2_approx(fmaf(s[i], p.c, -mc));
-              const float b = exp2_approx(fmaf(s[i + 1], p.c, -mc));
-              sum[i & 2] += a;
-              sum[(i & 2) + 1] += b;
-              w[i / 2] = pack2<BF16>(a, b);
+            for (int part = 0; part < 2; ++part) {
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float2 e = __ffma2_rn(make_float2(s[half][32 * part + 2 * i],
+                                                        s[half][32 * part + 2 * i + 1]), c2, mc2);
+                const float2 f = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+                sum[i % 2] = __fadd2_rn(sum[i % 2], f);
+                w[i] = pack2<BF16>(f.x, f.y);
+              }
+              tmem_st16(t_s + 32 * half + 16 * part, w);  // over S of the keys read before
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_st32(t_s + 32 * half, w);  // over S of the keys read before
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             tmem_wait_st();
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(pready(half));
+          if (lane == 0) mbar_arrive(pready(j, half));
         }
+        parity ^= 1;
+        slot += 2 * kP;
+        if (slot >= S) slot -= S, phase ^= 1;
       }
-      if (ok) ok = __all_sync(kFull, wait_soon(ofull, seg & 1, abort_flag));
+      if (ok) ok = __all_sync(kFull, wait_soon(ofull(j), seg & 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
-      const bool whole = c.begin == 0 && c.end == c.tile.blocks;
+      const bool whole = begin == 0 && end == g.blocks;
       if (busy) {
-        const int slot = 2 * blockIdx.x + (c.begin == 0 ? 1 : 0);
+        const int head = row % p.G;
+        const int slot_of = 2 * blockIdx.x + (begin == 0 ? 1 : 0);
         const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
-        const long long token = tile.token0 + tok;
-        const int h = c.h * p.G + head;
+        const long long token = g.token0 + tok;
+        const int h = g.h * p.G + head;
         uint16_t* out = static_cast<uint16_t*>(p.out) + token * p.out_stride_t + h * p.out_stride_h;
-        float* part = p.part + (static_cast<long long>(slot) * kRows + row) * D;
+        const long long at = static_cast<long long>(slot_of) * (QT * kRows) + tok * p.G + head;
+        float* part = p.part + at * D;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           float o[32];
           tmem_ld32(t_o + 32 * i, o);
           tmem_wait_ld(o);
-          if (!mine) continue;
-          if (whole) {
+          if (mine && whole) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
+            for (int q = 0; q < 32; q += 8) {
               uint4 v;
-              v.x = pack2<BF16>(o[j] * inv, o[j + 1] * inv);
-              v.y = pack2<BF16>(o[j + 2] * inv, o[j + 3] * inv);
-              v.z = pack2<BF16>(o[j + 4] * inv, o[j + 5] * inv);
-              v.w = pack2<BF16>(o[j + 6] * inv, o[j + 7] * inv);
+              v.x = pack2<BF16>(o[q] * inv, o[q + 1] * inv);
+              v.y = pack2<BF16>(o[q + 2] * inv, o[q + 3] * inv);
+              v.z = pack2<BF16>(o[q + 4] * inv, o[q + 5] * inv);
+              v.w = pack2<BF16>(o[q + 6] * inv, o[q + 7] * inv);
               if (l == 0.0f) v = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4*>(out + 32 * i + j) = v;
+              *reinterpret_cast<uint4*>(out + 32 * i + q) = v;
             }
-          } else {
+          } else if (mine) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<float4*>(part + 32 * i + j) =
-                  make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+            for (int q = 0; q < 32; q += 4)
+              *reinterpret_cast<float4*>(part + 32 * i + q) =
+                  make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
           }
+          __syncwarp();
         }
         if (mine) {
           if (!whole)
-            p.ml[static_cast<long long>(slot) * kRows + row] = make_float2(l == 0.0f ? -INFINITY : reference(m), l);
+            p.ml[at] = make_float2(l == 0.0f ? -INFINITY : reference(m), l);
           else if (p.lse)
             p.lse[token * (p.Hkv * p.G) + h] = l == 0.0f ? -INFINITY : reference(m) * kLn2 + logf(l);
         }
       }
       // the item starts here and goes on in later CTAs: the second kernel
       // joins the parts, this CTA's first
-      if (!whole && c.begin == 0 && threadIdx.x == 64) {
-        const long long last = share.end - 1 + (c.tile.blocks - c.end);  // its last key block
-        const int cta = static_cast<int>(((last + 1) * share.ctas - 1) / share.total);
-        p.meta[blockIdx.x] = make_int4(cta, tile.token0, c.h, tile.tokens);
-      }
+      if (g.last_cta >= 0 && threadIdx.x == 128)
+        p.meta[blockIdx.x] = make_int4(g.last_cta, g.token0, g.h, g.tokens);
+      __syncwarp();  // the segment's numbers have been read
     }
     if (!ok && lane == 0) give_up();
   }
@@ -855,7 +997,7 @@ __global__ void __launch_bounds__(kAThreads, 2)
   tc_fence_after();
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
-                 ::"r"(tmem), "n"(kTmemCols) : "memory");
+                 ::"r"(tmem), "n"(Shape<QT>::kTmemCols) : "memory");
 }
 
 // Joins the parts of the item that starts in CTA blockIdx.x of the first
@@ -875,8 +1017,8 @@ struct Vec<4> {
   using type = float4;
 };
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(32 * kJoinWarps) dsa_attention_join_kernel(const AParams p) {
+template <int D, bool BF16, int QT>
+__global__ void __launch_bounds__(32 * kJoinWarps) dsa_attention_join_kernel(const __grid_constant__ AParams p) {
   __shared__ float sums[kJoinWarps][D + 1];
   grid_dependency_wait();
   grid_launch_dependents();
@@ -893,7 +1035,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) dsa_attention_join_kernel(con
     const int row = r0 + (few ? warp : 0);
     if (few && row >= meta.w * p.G) return;
     float top = -INFINITY;
-    for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.ml[slot(i) * kRows + row].x);
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.ml[slot(i) * (QT * kRows) + row].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
     const float ref = top == -INFINITY ? 0.0f : top;
@@ -901,8 +1043,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) dsa_attention_join_kernel(con
     float l = 0.0f;
 #pragma unroll 8
     for (int i = from; i < parts; i += step) {
-      const float2 ml = p.ml[slot(i) * kRows + row];
-      const V o = *reinterpret_cast<const V*>(p.part + (slot(i) * kRows + row) * D + lane * (D / 32));
+      const float2 ml = p.ml[slot(i) * (QT * kRows) + row];
+      const V o = *reinterpret_cast<const V*>(p.part + (slot(i) * (QT * kRows) + row) * D + lane * (D / 32));
       const float f = exp2_approx(ml.x - ref);
       l = fmaf(f, ml.y, l);
 #pragma unroll
@@ -962,13 +1104,13 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 std::mutex g_ready_mu;
 bool g_ready[64];
 
-template <int D, bool BF16>
+template <int D, bool BF16, int QT>
 cudaError_t prepare_one() {
-  cudaError_t e = cudaFuncSetAttribute(dsa_paged_attention_kernel<D, BF16>,
+  cudaError_t e = cudaFuncSetAttribute(dsa_paged_attention_kernel<D, BF16, QT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       ASmem<D>::kBytes);
+                                       ASmem<D, QT>::kBytes);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(dsa_paged_attention_kernel<D, BF16>,
+    e = cudaFuncSetAttribute(dsa_paged_attention_kernel<D, BF16, QT>,
                              cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared);
   return e;
@@ -982,27 +1124,35 @@ cudaError_t prepare_device() {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(g_ready_mu);
   if (g_ready[dev]) return cudaSuccess;
-  e = prepare_one<64, false>();
-  if (e == cudaSuccess) e = prepare_one<64, true>();
-  if (e == cudaSuccess) e = prepare_one<128, false>();
-  if (e == cudaSuccess) e = prepare_one<128, true>();
+  e = prepare_one<64, false, 1>();
+  if (e == cudaSuccess) e = prepare_one<64, true, 1>();
+  if (e == cudaSuccess) e = prepare_one<128, false, 1>();
+  if (e == cudaSuccess) e = prepare_one<128, true, 1>();
+  if (e == cudaSuccess) e = prepare_one<64, false, 2>();
+  if (e == cudaSuccess) e = prepare_one<64, true, 2>();
+  if (e == cudaSuccess) e = prepare_one<128, false, 2>();
+  if (e == cudaSuccess) e = prepare_one<128, true, 2>();
   g_ready[dev] = e == cudaSuccess;
   return e;
 }
+
+// Query tiles of a CTA.  Two where sequences fill them: keys are then loaded
+// once for 256 rows.
+int query_tiles(int T, int B, int q_tokens) { return T / q_tokens >= 2LL * B ? 2 : 1; }
 
 long long max_items(int T, int B, int Hkv, int tile_tokens) {
   return (static_cast<long long>(T) / tile_tokens + B) * Hkv;
 }
 
-// The key blocks are cut into equal shares unless tiles of one sequence share
+// The key blocks are cut into equal shares unless items of one sequence share
 // keys that L2 cannot hold: a share's place in the keys differs from CTA to
 // CTA, so all keys of the call are in use at once, while whole items taken in
 // order keep the CTAs on one kv head.  That needs items enough for a balance.
-bool use_split(int T, int B, int Hkv, int D, int tile_tokens, int max_context) {
-  const bool shared = T / tile_tokens >= 2LL * B;
+bool use_split(int T, int B, int Hkv, int D, int q_tokens, int max_context) {
+  const int tiles = query_tiles(T, B, q_tokens);
   const double bytes = 4.0 * D * Hkv * max_context * B;
   return max_context > kKeys &&
-         !(shared && bytes > 9.6e7 && max_items(T, B, Hkv, tile_tokens) >= 4LL * kSplitCtas);
+         !(tiles == 2 && bytes > 9.6e7 && max_items(T, B, Hkv, tiles * q_tokens) >= 4 * kSms);
 }
 
 bool encode_map(CUtensorMap* map, bool bf16, const void* base, int rank, const cuuint64_t* dims,
@@ -1017,30 +1167,41 @@ bool encode_map(CUtensorMap* map, bool bf16, const void* base, int rank, const c
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, int QT>
 cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                   const AParams& p, long long grid, bool pdl, cudaStream_t s) {
+                   const AParams& p, bool pdl, cudaStream_t s) {
+  const long long items = max_items(p.T, p.B, p.Hkv, p.tile_tokens);
+  const int ctas = p.split || items > Shape<QT>::kCtas ? Shape<QT>::kCtas : static_cast<int>(items);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kAThreads);
-  cfg.dynamicSmemBytes = ASmem<D>::kBytes;
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(Shape<QT>::kThreads);
+  cfg.dynamicSmemBytes = ASmem<D, QT>::kBytes;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, dsa_paged_attention_kernel<D, BF16>, tq, tk, tv, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, dsa_paged_attention_kernel<D, BF16, QT>, tq, tk, tv, p);
   if (e != cudaSuccess || !p.split) return e;
-  cfg.gridDim = dim3(kSplitCtas, kJoinGroups);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), kJoinGroups);
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dsa_attention_join_kernel<D, BF16>, p);
+  return cudaLaunchKernelEx(&cfg, dsa_attention_join_kernel<D, BF16, QT>, p);
 }
 
-constexpr size_t kMetaBytes = kSplitCtas * sizeof(int4);
-constexpr size_t kMlBytes = 2 * kSplitCtas * kRows * sizeof(float2);
+template <int D, bool BF16>
+cudaError_t launch_tiles(int tiles, const CUtensorMap& tq, const CUtensorMap& tk,
+                         const CUtensorMap& tv, const AParams& p, bool pdl, cudaStream_t s) {
+  return tiles == 2 ? launch<D, BF16, 2>(tq, tk, tv, p, pdl, s)
+                    : launch<D, BF16, 1>(tq, tk, tv, p, pdl, s);
+}
+
+// the same for one and two query tiles
+constexpr size_t kMetaBytes = 2 * kSms * sizeof(int4);
+constexpr size_t kPartRows = 2 * 2 * kSms * kRows;
+constexpr size_t kMlBytes = kPartRows * sizeof(float2);
 
 }  // namespace
 
@@ -1050,8 +1211,7 @@ size_t dsa_paged_attention_workspace_bytes(int32_t T, int32_t B, int32_t H, int3
                                            int32_t head_dim, int32_t max_context) {
   if (T < 1 || B < 1 || Hkv < 1 || H < Hkv || H % Hkv || H / Hkv > kRows || head_dim < 1) return 0;
   if (!use_split(T, B, Hkv, head_dim, kRows / (H / Hkv), max_context)) return 0;
-  return kMetaBytes + kMlBytes +
-         2 * kSplitCtas * kRows * static_cast<size_t>(head_dim) * sizeof(float);
+  return kMetaBytes + kMlBytes + kPartRows * static_cast<size_t>(head_dim) * sizeof(float);
 }
 
 dsa_status dsa_paged_attention(
@@ -1080,9 +1240,8 @@ dsa_status dsa_paged_attention(
   // positions and grids are 32-bit
   if (max_context > (1 << 30) || T > (1 << 30) || static_cast<long long>(T) * H > 0x7fffffffLL)
     return DSA_ERR_SHAPE;
-  const int tile_tokens = kRows / G;
-  const long long items = max_items(T, B, Hkv, tile_tokens);
-  if (items > 0x7fffffffLL) return DSA_ERR_SHAPE;
+  const int q_tokens = kRows / G;
+  if (max_items(T, B, Hkv, q_tokens) > 0x7fffffffLL) return DSA_ERR_SHAPE;
   if (T == 0 || B == 0) return DSA_OK;
   if (!q || !k_cache || !v_cache || !query_start || !context_lens || !out ||
       (!block_table && max_context > 0))
@@ -1128,7 +1287,7 @@ dsa_status dsa_paged_attention(
   {
     const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T)};
     const cuuint64_t strides[2] = {bytes(q_stride_h, H), bytes(q_stride_t, T)};
-    const cuuint32_t b[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(tile_tokens)};
+    const cuuint32_t b[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(q_tokens)};
     if (!encode_map(&tq, bf16, q, 3, dims, strides, b)) return DSA_ERR_LAUNCH;
   }
   auto cache_map = [&](CUtensorMap* map, const void* base, int64_t sp, int64_t st, int64_t sh) {
@@ -1158,7 +1317,9 @@ dsa_status dsa_paged_attention(
   p.B = B;
   p.Hkv = Hkv;
   p.G = G;
-  p.tile_tokens = tile_tokens;
+  const int tiles = query_tiles(T, B, q_tokens);
+  p.q_tokens = q_tokens;
+  p.tile_tokens = tiles * q_tokens;
   p.max_context = max_context;
   p.window = window < max_context ? window : 0;  // such a window hides nothing
   p.sinks = p.window ? (sinks < max_context ? sinks : max_context) : 0;
@@ -1168,16 +1329,15 @@ dsa_status dsa_paged_attention(
   p.ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + kMetaBytes);
   p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kMetaBytes + kMlBytes);
   p.err = err_flags;
-  const long long grid = p.split || items > kSplitCtas ? kSplitCtas : items;
   const bool pdl = (flags & DSA_FLAG_PDL) != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (head_dim == 64)
-    e = bf16 ? launch<64, true>(tq, tk, tv, p, grid, pdl, s)
-             : launch<64, false>(tq, tk, tv, p, grid, pdl, s);
+    e = bf16 ? launch_tiles<64, true>(tiles, tq, tk, tv, p, pdl, s)
+             : launch_tiles<64, false>(tiles, tq, tk, tv, p, pdl, s);
   else
-    e = bf16 ? launch<128, true>(tq, tk, tv, p, grid, pdl, s)
-             : launch<128, false>(tq, tk, tv, p, grid, pdl, s);
+    e = bf16 ? launch_tiles<128, true>(tiles, tq, tk, tv, p, pdl, s)
+             : launch_tiles<128, false>(tiles, tq, tk, tv, p, pdl, s);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_LAUNCH;
 }
 
