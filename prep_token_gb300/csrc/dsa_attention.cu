@@ -20,14 +20,14 @@
 //   * warp 1 (one lane) issues S = Q K^T (M = N = 128, both operands in shared
 //     memory) and O += P V (A = P in TMEM over the columns of S, B = V in
 //     shared memory, read MN-major), and commits them to the mbarriers.
-//   * one warpgroup per query tile owns one row per thread: S from TMEM, the masks (in blocks at
-//     an edge only), the maximum, the exponentials, P back to TMEM.  O is
-//     rescaled only when a maximum has grown by more than 2^8: until then P
-//     may exceed 1, at most by that factor, which fp32 and both 16-bit types
-//     hold.  P is rounded to the values' type for the matrix product (at most
-//     2^-8 of it in bf16, 2^-11 in fp16); the sum l takes it unrounded.  In
-//     fp16 P, O and l carry a factor of 2^7, so that a p down to 2^-21 keeps
-//     all its bits and the largest one, 2^(8 + 7), still fits.
+//   * one warpgroup per query tile owns one row per thread: S from TMEM, the
+//     masks (in blocks at an edge only), the exponentials, P back to TMEM.  m
+//     need not be the maximum, only near enough for fp32 and P's type to hold
+//     p: the row's first maximum serves until a sum of P passes a limit, so
+//     that most blocks form no maximum and rescale nothing.  P is rounded to
+//     the values' type for the matrix product (at most 2^-8 of it in bf16,
+//     2^-11 in fp16); the sum l takes it unrounded.  In fp16 P, O and l carry a
+//     factor of 2^7: a p down to 2^-21 of the largest keeps all its bits.
 // Two CTAs share an SM, so one's softmax runs beside the other's products.
 //
 // Bound: a chunk by the tensor cores (4 D flops per row and visible key),
@@ -70,7 +70,10 @@ struct Shape {
   static constexpr int kCtas = 2 / QT * kSms;
   static constexpr int kTmemCols = 256 * QT;          // per tile: S / P 128, O D
 };
-constexpr float kRescaleLog2 = 8.0f;
+// A half block's sum of P above which a row's reference is renewed.  P in
+// bf16 has fp32's range; in fp16 no p may pass 65504.
+template <bool BF16>
+constexpr float kSumLimit = BF16 ? 0x1p40f : 0x1p15f;
 constexpr float kLn2 = 0.693147180559945309f;
 
 struct AParams {
@@ -264,9 +267,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
-// The n lowest of 64 bits.
-__device__ __forceinline__ uint64_t below(int n) {
-  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+// The n lowest of 32 bits.
+__device__ __forceinline__ uint32_t below(int n) {
+  return n <= 0 ? 0u : n >= 32 ? kFull : (1u << n) - 1u;
 }
 
 // ---------------------------------------------------------------- work items
@@ -312,20 +315,25 @@ __device__ __forceinline__ Seq load_seq(const AParams& p, int b) {
   return s;
 }
 
+// 64-bit only where it has to be; out of line, as it is long and rarely run.
+__device__ __noinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0)
+    return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // Key blocks of all tiles of a sequence, for one kv head.  A whole warp calls
 // it with each lane's own sequence.
-__device__ __forceinline__ long long seq_blocks(const AParams& p, const Seq& s) {
+__device__ __noinline__ long long seq_blocks(const AParams& p, int n, int ctx, int tiles) {
   const int lane = threadIdx.x & 31;
-  long long mine = 0;
-  const bool few = s.tiles <= 2;
-  if (few)
-    for (int t = 0; t < s.tiles; ++t) mine += make_tile(p, s.q0, s.n, s.ctx, t).blocks;
-  for (unsigned todo = __ballot_sync(kFull, !few); todo; todo &= todo - 1) {
+  long long mine = tiles > 0 ? make_tile(p, 0, n, ctx, 0).blocks : 0;
+  for (unsigned todo = __ballot_sync(kFull, tiles > 1); todo; todo &= todo - 1) {
     const int src = __ffs(todo) - 1;
-    const int n = __shfl_sync(kFull, s.n, src), ctx = __shfl_sync(kFull, s.ctx, src);
-    const int tiles = __shfl_sync(kFull, s.tiles, src);
+    const int n1 = __shfl_sync(kFull, n, src), ctx1 = __shfl_sync(kFull, ctx, src);
+    const int tiles1 = __shfl_sync(kFull, tiles, src);
     long long sum = 0;
-    for (int t = lane; t < tiles; t += 32) sum += make_tile(p, 0, n, ctx, t).blocks;
+#pragma unroll 1
+    for (int t = lane; t < tiles1; t += 32) sum += make_tile(p, 0, n1, ctx1, t).blocks;
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
     if (lane == src) mine = sum;
@@ -343,6 +351,41 @@ __device__ __forceinline__ long long warp_inclusive(long long v) {
   return v;
 }
 
+// Split work: key blocks in the order sequence, kv head, tile.  Each of `ctas`
+// CTAs takes `each` of them, the first `extra` CTAs one more.
+struct Share {
+  long long each, extra, begin, end;
+};
+
+// A whole warp calls it.
+__device__ __forceinline__ Share my_share(const AParams& p) {
+  const int lane = threadIdx.x & 31;
+  long long total = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    Seq s = {0, 0, 0, 0};
+    if (b0 + lane < p.B) s = load_seq(p, b0 + lane);
+    total += seq_blocks(p, s.n, s.ctx, s.tiles);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
+  total *= p.Hkv;
+  Share r;
+  r.each = divide(total, gridDim.x);
+  r.extra = total - r.each * gridDim.x;
+  const long long g = blockIdx.x;
+  r.begin = g * r.each + min(g, r.extra);
+  r.end = r.begin + r.each + (g < r.extra ? 1 : 0);
+  return r;
+}
+
+// The CTA that has key block `at`.
+__device__ __forceinline__ int cta_of(const Share& s, long long at) {
+  const long long longer = s.extra * (s.each + 1);  // blocks of the CTAs with one more
+  return static_cast<int>(at < longer ? divide(at, s.each + 1)
+                                      : s.extra + divide(at - longer, s.each));
+}
+
 // Where a CTA is in its work: the tile, and the key blocks [begin, end) of it.
 struct Cursor {
   int b, h, t;
@@ -350,59 +393,66 @@ struct Cursor {
   Tile tile;
   int begin, end;
   long long left;  // split: key blocks after this segment
-  long long item;  // not split: the item
 };
 
 __device__ __forceinline__ void take_tile(const AParams& p, Cursor& c, int begin, long long budget) {
   c.tile = make_tile(p, c.s.q0, c.s.n, c.s.ctx, c.t);
   c.begin = begin;
-  const long long most = begin + budget;
-  c.end = most < c.tile.blocks ? static_cast<int>(most) : c.tile.blocks;
+  c.end = static_cast<int>(min(static_cast<long long>(c.tile.blocks), begin + budget));
   c.left = budget - (c.end - c.begin);
 }
 
-__device__ __forceinline__ long long mul_div(long long total, int g, int of) {
-  if (total < (1 << 22))  // 304 shares: the product fits 32 bits
-    return static_cast<uint32_t>(total) * static_cast<uint32_t>(g) / static_cast<uint32_t>(of);
-  return total * g / of;
-}
-
-// Split work: key blocks in the order sequence, kv head, tile.  CTA g of
-// `ctas` takes [total * g / ctas, total * (g + 1) / ctas).
-struct Share {
-  long long total, begin, end;
-  int ctas;
-};
-
-__device__ __forceinline__ Share my_share(const AParams& p) {
+// Puts the cursor at key block `want` (split; `budget` of them are taken) or at
+// item `want`.  A whole warp calls it; every lane gets the same.
+__device__ __forceinline__ bool seek(const AParams& p, Cursor& c, long long want, long long budget) {
   const int lane = threadIdx.x & 31;
-  long long sum = 0;
+  long long before = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     Seq s = {0, 0, 0, 0};
     if (b0 + lane < p.B) s = load_seq(p, b0 + lane);
-    sum += seq_blocks(p, s);
+    const long long per_head = p.split ? seq_blocks(p, s.n, s.ctx, s.tiles) : s.tiles;
+    const long long upto = before + warp_inclusive(per_head * p.Hkv);
+    const unsigned past = __ballot_sync(kFull, upto > want);
+    if (past) {
+      const int src = __ffs(past) - 1;
+      const long long one = __shfl_sync(kFull, per_head, src);
+      const long long rest = want - (__shfl_sync(kFull, upto, src) - one * p.Hkv);
+      c.b = b0 + src;
+      c.s.q0 = __shfl_sync(kFull, s.q0, src);
+      c.s.n = __shfl_sync(kFull, s.n, src);
+      c.s.ctx = __shfl_sync(kFull, s.ctx, src);
+      c.s.tiles = __shfl_sync(kFull, s.tiles, src);
+      c.h = static_cast<int>(divide(rest, one));
+      int r = static_cast<int>(rest - c.h * one);
+      c.t = c.s.tiles - 1 - r;  // whole items: the last tiles of a chunk see the most keys
+      if (p.split) {
+        int seen = 0;  // key blocks of the tiles before
+#pragma unroll 1
+        for (int t0 = 0;; t0 += 32) {
+          const int t = t0 + lane;
+          const int n = t < c.s.tiles ? make_tile(p, 0, c.s.n, c.s.ctx, t).blocks : 0;
+          const int up = seen + static_cast<int>(warp_inclusive(n));
+          const unsigned over = __ballot_sync(kFull, up > r);
+          if (over) {
+            const int at = __ffs(over) - 1;
+            c.t = t0 + at;
+            r -= __shfl_sync(kFull, up - n, at);
+            break;
+          }
+          seen = __shfl_sync(kFull, up, 31);
+        }
+      }
+      take_tile(p, c, p.split ? r : 0, budget);
+      return true;
+    }
+    before = __shfl_sync(kFull, upto, 31);
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-  Share r;
-  r.total = sum * p.Hkv;
-  r.ctas = r.total < static_cast<long long>(gridDim.x) ? static_cast<int>(r.total)
-                                                       : static_cast<int>(gridDim.x);
-  const int g = blockIdx.x;
-  r.begin = g < r.ctas ? mul_div(r.total, g, r.ctas) : 0;
-  r.end = g < r.ctas ? mul_div(r.total, g + 1, r.ctas) : 0;
-  return r;
+  return false;
 }
 
-__device__ __forceinline__ bool seek(const AParams& p, Cursor& c, const Share& share, long long want);
-
-// The next tile, kv head or sequence with tokens, while key blocks are left;
-// or the CTA's next whole item.  A whole warp calls it.
-__device__ __forceinline__ bool next_segment(const AParams& p, Cursor& c, const Share& share) {
-  if (!p.split) {
-    c.item += gridDim.x;
-    return seek(p, c, share, c.item);
-  }
+// The next tile, kv head or sequence with tokens, while key blocks are left.
+__device__ __forceinline__ bool next_segment(const AParams& p, Cursor& c) {
   if (c.left <= 0) return false;
   if (++c.t == c.s.tiles) {
     c.t = 0;
@@ -416,65 +466,6 @@ __device__ __forceinline__ bool next_segment(const AParams& p, Cursor& c, const 
   }
   take_tile(p, c, 0, c.left);
   return true;
-}
-
-// The CTA's first segment.
-__device__ __forceinline__ bool first_segment(const AParams& p, Cursor& c, Share& share) {
-  c.item = blockIdx.x;
-  if (!p.split) return seek(p, c, share, c.item);
-  share = my_share(p);
-  return share.begin < share.end && seek(p, c, share, share.begin);
-}
-
-// Puts the cursor at key block `want` (split) or item `want`.  A whole warp
-// calls it; every lane gets the same.
-__device__ __forceinline__ bool seek(const AParams& p, Cursor& c, const Share& share, long long want) {
-  const int lane = threadIdx.x & 31;
-  long long before = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    Seq s = {0, 0, 0, 0};
-    if (b0 + lane < p.B) s = load_seq(p, b0 + lane);
-    const long long per_head = p.split ? seq_blocks(p, s) : s.tiles;
-    const long long upto = before + warp_inclusive(per_head * p.Hkv);
-    const unsigned past = __ballot_sync(kFull, upto > want);
-    if (past) {
-      const int src = __ffs(past) - 1;
-      const long long one = __shfl_sync(kFull, per_head, src);
-      const long long rest = want - (__shfl_sync(kFull, upto, src) - one * p.Hkv);
-      c.b = b0 + src;
-      c.s = load_seq(p, c.b);
-      c.h = 0;
-      int r = 0;
-      if (rest < (1LL << 31) && one < (1LL << 31)) {
-        c.h = static_cast<int>(rest) / static_cast<int>(one);
-        r = static_cast<int>(rest) - c.h * static_cast<int>(one);
-      } else {
-        c.h = static_cast<int>(rest / one);
-        r = static_cast<int>(rest - c.h * one);
-      }
-      if (!p.split) {
-        c.t = c.s.tiles - 1 - r;  // the last tiles of a chunk see the most keys: first
-        take_tile(p, c, 0, 1LL << 40);
-        return true;
-      }
-      int seen = 0;  // key blocks of the tiles before
-      for (int t0 = 0;; t0 += 32) {
-        const int t = t0 + lane;
-        const int n = t < c.s.tiles ? make_tile(p, 0, c.s.n, c.s.ctx, t).blocks : 0;
-        const int up = seen + static_cast<int>(warp_inclusive(n));
-        const unsigned over = __ballot_sync(kFull, up > r);
-        if (over) {
-          const int at = __ffs(over) - 1;
-          c.t = t0 + at;
-          take_tile(p, c, r - __shfl_sync(kFull, up - n, at), share.end - share.begin);
-          return true;
-        }
-        seen = __shfl_sync(kFull, up, 31);
-      }
-    }
-    before = __shfl_sync(kFull, upto, 31);
-  }
-  return false;
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -497,15 +488,18 @@ struct ASmem {
   static constexpr int kPanels = D / 64;                    // 128-byte panels of a row
   static constexpr int kTileBytes = kRows * D * 2;          // a query tile
   static constexpr int kQBytes = QT * kTileBytes;
-  // units of the ring: 5 or 6 with two CTAs per SM, 10 or 12 with one
-  static constexpr int kStages = ((QT == 1 ? 114688 : 229376) - kQBytes) / kUnitBytes;
+  // two tiles: 2 KB per softmax warp through which rows are turned for stores
+  static constexpr int kTurnBytes = 0;
+  // units of the ring: 5 or 6 with two CTAs per SM, 9 or 11 with one
+  static constexpr int kStages = ((QT == 1 ? 114688 : 229376) - kQBytes - kTurnBytes) / kUnitBytes;
   static constexpr int kVKeys = kKeys / kPanels;            // keys of a V unit
   static constexpr int kOffRing = kQBytes;
-  static constexpr int kOffSeg = kOffRing + kStages * kUnitBytes;
+  static constexpr int kOffTurn = kOffRing + kStages * kUnitBytes;
+  static constexpr int kOffSeg = kOffTurn + kTurnBytes;
   static constexpr int kOffBar = kOffSeg + kSegments * static_cast<int>(sizeof(Segment));
   // barriers: full[S], empty[S], qfull, qempty, drain, segment[4], then per
-  // query tile sfull, pready[2], ofull
-  static constexpr int kBars = 2 * kStages + 3 + kSegments + 4 * QT;
+  // query tile sfull, pready[2], odone[2]
+  static constexpr int kBars = 2 * kStages + 3 + kSegments + 5 * QT;
   static constexpr int kOffTmem = kOffBar + 8 * kBars;
   static constexpr int kOffAbort = kOffTmem + 4;
   static constexpr int kBytes = kOffAbort + 4;
@@ -541,9 +535,11 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
   const uint32_t drain = bar0 + 8 * (2 * S + 2);
   auto segment_ready = [&](int i) { return bar0 + 8 * (2 * S + 3 + i % kSegments); };
   constexpr int kB = 2 * S + 3 + kSegments;
-  auto sfull = [&](int j) { return bar0 + 8 * (kB + 4 * j); };
-  auto pready = [&](int j, int half) { return bar0 + 8 * (kB + 1 + 4 * j + half); };
-  auto ofull = [&](int j) { return bar0 + 8 * (kB + 3 + 4 * j); };
+  auto sfull = [&](int j) { return bar0 + 8 * (kB + 5 * j); };
+  auto pready = [&](int j, int half) { return bar0 + 8 * (kB + 1 + 5 * j + half); };
+  // O with the first half of a block's keys; with the last block of a segment
+  auto ohalf = [&](int j) { return bar0 + 8 * (kB + 3 + 5 * j); };
+  auto ofull = [&](int j) { return bar0 + 8 * (kB + 4 + 5 * j); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffAbort);
   Segment* const segments = reinterpret_cast<Segment*>(smem + L::kOffSeg);
   const int warp = threadIdx.x >> 5;
@@ -566,6 +562,7 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
     for (int j = 0; j < QT; ++j) {
       mbar_init(sfull(j), 1);
       for (int h = 0; h < 2; ++h) mbar_init(pready(j, h), 4);  // the tile's softmax warps
+      mbar_init(ohalf(j), 1);
       mbar_init(ofull(j), 1);
     }
     *abort_flag = 0;
@@ -597,7 +594,12 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
       // ---------------------------------------------- loads
       Cursor c = {};
       Share share = {0, 0, 0, 0};
-      bool more = first_segment(p, c, share);
+      long long want = blockIdx.x;  // an item, or a key block
+      if (p.split) {
+        share = my_share(p);
+        want = share.begin;
+      }
+      bool more = !p.split || share.begin < share.end, placed = false;
       if (p.split && lane == 0) p.meta[blockIdx.x].x = -1;
       const int boxes = kKeys / p.box;
       const uint32_t box_bytes = static_cast<uint32_t>(p.box) * 128u;  // of one panel
@@ -618,6 +620,10 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
       for (int seg = 0;; ++seg) {
         if (seg > 0) ok = __all_sync(kFull, wait_soon(qempty, (seg & 1) ^ 1, abort_flag));
         if (!ok) break;
+        if (more && !placed) {
+          more = seek(p, c, want, p.split ? share.end - share.begin : 1LL << 40);
+          placed = p.split;
+        }
         const Tile& tile = c.tile;
         if (lane == 0) {
           Segment& g = segments[seg % kSegments];
@@ -633,10 +639,8 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
           g.token0 = tile.token0;
           g.h = c.h;
           g.last_cta = -1;
-          if (more && p.split && c.begin == 0 && c.end < tile.blocks) {
-            const long long last = share.end - 1 + (tile.blocks - c.end);  // its last key block
-            g.last_cta = static_cast<int>(((last + 1) * share.ctas - 1) / share.total);
-          }
+          if (more && p.split && c.begin == 0 && c.end < tile.blocks)
+            g.last_cta = cta_of(share, share.end - 1 + (tile.blocks - c.end));
           mbar_arrive(segment_ready(seg));
           if (more) {
             mbar_arrive_expect_tx(qfull, QT * kP * p.G * p.q_tokens * 128);
@@ -706,7 +710,10 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
           page = next;
         }
         if (!ok) break;
-        more = next_segment(p, c, share);
+        if (p.split)
+          more = next_segment(p, c);
+        else
+          want += gridDim.x;
       }
       if (!ok && lane == 0) give_up();
       volatile int never = 0;  // stay until every load issued has landed
@@ -779,6 +786,7 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
                          make_desc(b + ks * (2048 >> 4)), idesc_o,
                          (k > begin || half + ks > 0) ? 1u : 0u);
                 if (j + 1 == QT && (kP == 2 || half == 1)) mma_commit(empty(s));
+                if (half == 0) mma_commit(ohalf(j));
               }
             }
             if (k + 1 < end)
@@ -828,17 +836,19 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
       const int lo_all = __reduce_max_sync(kFull, mine ? lo : 0);
       float m = -INFINITY, l = 0.0f;  // m is the maximum that P and O are scaled by
       const int begin = g.begin, end = g.end;
+      const int sink_blocks = g.sink_blocks, skip = g.main_block - sink_blocks;
+      const int seen_hi = g.hi, seen_lo = g.lo;  // by some row of the item
       for (int k = begin; k < end; ++k) {
-        const int key0 = (k < g.sink_blocks ? k : g.main_block + k - g.sink_blocks) * kKeys;
+        const int key0 = (k < sink_blocks ? k : k + skip) * kKeys;
         ok = __all_sync(kFull, wait_soon(sfull(j), parity, abort_flag));
         if (!ok) break;
         tc_fence_after();
         // V rows of a loaded page that no row of the item sees (behind the
         // context, before the window): whatever they hold, 0 * it must be 0.
         // Tile 0's P V comes first, and waits for this.
-        if (j == 0 && !(key0 + kKeys <= g.hi && (key0 >= g.lo || key0 + kKeys <= p.sinks))) {
+        if (j == 0 && !(key0 + kKeys <= seen_hi && (key0 >= seen_lo || key0 + kKeys <= p.sinks))) {
           const int key = key0 + row;
-          if (!(key < g.hi && (key >= g.lo || key < p.sinks))) {
+          if (!(key < seen_hi && (key >= seen_lo || key < p.sinks))) {
             int s = slot + row / L::kVKeys;
             uint32_t ph = phase;
             if (s >= S) s -= S, ph ^= 1;
@@ -855,80 +865,82 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
           ok = __all_sync(kFull, ok);
           if (!ok) break;
         }
-        // The row's 128 scores stay in registers from the maximum to P.
-        const bool all = key0 + kKeys <= hi_all && (key0 >= lo_all || key0 + kKeys <= p.sinks);
-        float s[2][kKeys / 2];
-        float mc = 0.0f;
-        if (busy) {
-          float m_new = m;
-          tmem_ld32(t_s, s[0]);
-          tmem_ld32(t_s + 32, s[0] + 32);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            tmem_wait_ld(s[half]);
-            if (half == 0) {
-              tmem_ld32(t_s + 64, s[1]);
-              tmem_ld32(t_s + 96, s[1] + 32);
-            }
-            if (!all) {
-              const int at = key0 + half * 64;
-              const uint64_t seen = below(hi - at) & (~below(lo - at) | below(p.sinks - at));
-              const uint32_t bits[2] = {static_cast<uint32_t>(seen),
-                                        static_cast<uint32_t>(seen >> 32)};
-#pragma unroll
-              for (int i = 0; i < kKeys / 2; ++i)
-                s[half][i] = bits[i / 32] & (1u << (i % 32)) ? s[half][i] : -INFINITY;
-            }
-            float mx[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mx[i] = s[half][i];
-#pragma unroll
-            for (int i = 4; i < kKeys / 2; i += 8)
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                mx[q] = i + 4 < kKeys / 2 ? max3f(mx[q], s[half][i + q], s[half][i + 4 + q])
-                                          : fmaxf(mx[q], s[half][i + q]);
-            m_new = max3f(m_new, fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          }
-          // -inf - -inf is NaN and compares false: nothing was summed yet
-          const bool grown = (m_new - m) * p.c > kRescaleLog2;
-          if (k == begin) {
-            m = m_new;
-          } else if (__any_sync(kFull, grown)) {
-            const float f = grown ? exp2_approx((m - m_new) * p.c) : 1.0f;
-            m = grown ? m_new : m;
-            l *= f;
+        // Each half of the block's keys by itself, P against the reference that
+        // the row has: no maximum is taken while that serves.  A sum above
+        // kSumLimit says that it no longer does, and a row that has none yet
+        // takes one; only then (every segment's first half, few others) is
+        // the maximum formed, O and l rescaled and P computed again.
+        const bool edge = !(key0 + kKeys <= hi_all && (key0 >= lo_all || key0 + kKeys <= p.sinks));
 #pragma unroll 1
-            for (int i = 0; i < D / 16; ++i) {
-              float o[16];
-              tmem_ld16(t_o + 16 * i, o);
-              tmem_wait_ld(o);
-#pragma unroll
-              for (int q = 0; q < 16; ++q) o[q] *= f;
-              tmem_st16(t_o + 16 * i, reinterpret_cast<uint32_t*>(o));
-            }
-          }
-          mc = reference(m);
-        }
-#pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (busy) {
-            const float2 c2 = make_float2(p.c, p.c), mc2 = make_float2(-mc, -mc);
-            float2 sum[2] = {};
+            float s[kKeys / 2];
+            tmem_ld32(t_s + 64 * half, s);
+            tmem_ld32(t_s + 64 * half + 32, s + 32);
+            tmem_wait_ld(s);
+            if (edge) {
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              uint32_t w[16];
+              for (int part = 0; part < 2; ++part) {  // masks only at an edge
+                const int at = key0 + 64 * half + part * 32;
+                if (at + 32 <= hi_all && (at >= lo_all || at + 32 <= p.sinks)) continue;
+                const uint32_t seen = below(hi - at) & (~below(lo - at) | below(p.sinks - at));
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float2 e = __ffma2_rn(make_float2(s[half][32 * part + 2 * i],
-                                                        s[half][32 * part + 2 * i + 1]), c2, mc2);
+                for (int i = 0; i < 32; ++i)
+                  s[32 * part + i] = seen & (1u << i) ? s[32 * part + i] : -INFINITY;
+              }
+            }
+            float sum;
+            uint32_t w[kKeys / 4];
+            auto exponentials = [&](float mc) {
+              const float2 c2 = make_float2(p.c, p.c), mc2 = make_float2(-mc, -mc);
+              float2 add[2] = {};
+#pragma unroll
+              for (int i = 0; i < kKeys / 4; ++i) {
+                const float2 e = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), c2, mc2);
                 const float2 f = make_float2(exp2_approx(e.x), exp2_approx(e.y));
-                sum[i % 2] = __fadd2_rn(sum[i % 2], f);
+                add[i % 2] = __fadd2_rn(add[i % 2], f);
                 w[i] = pack2<BF16>(f.x, f.y);
               }
-              tmem_st16(t_s + 32 * half + 16 * part, w);  // over S of the keys read before
+              sum = (add[0].x + add[0].y) + (add[1].x + add[1].y);
+            };
+#pragma unroll 1
+            for (int pass = 0;; ++pass) {  // once, or again with another reference
+              exponentials(reference(m));
+              const bool renew = mine && (m == -INFINITY || !(sum <= kSumLimit<BF16>));
+              if (pass == 1 || !__any_sync(kFull, renew)) break;
+              float mx[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mx[i] = s[i];
+#pragma unroll
+              for (int i = 4; i < kKeys / 2; i += 8)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  mx[q] = i + 4 < kKeys / 2 ? max3f(mx[q], s[i + q], s[i + 4 + q])
+                                            : fmaxf(mx[q], s[i + q]);
+              const float m_new = max3f(m, fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+              if (k > begin || half == 1) {  // O exists
+                // it is complete up to the half before: sfull followed the
+                // products of the block before
+                if (half == 1) ok = __all_sync(kFull, wait_soon(ohalf(j), parity, abort_flag));
+                tc_fence_after();
+                // a first maximum meets O and l that are still 0
+                const float f = renew && m != -INFINITY ? exp2_approx((m - m_new) * p.c) : 1.0f;
+                l *= f;
+#pragma unroll 1
+                for (int i = 0; i < D / 16; ++i) {
+                  float o[16];
+                  tmem_ld16(t_o + 16 * i, o);
+                  tmem_wait_ld(o);
+#pragma unroll
+                  for (int q = 0; q < 16; ++q) o[q] *= f;
+                  tmem_st16(t_o + 16 * i, reinterpret_cast<uint32_t*>(o));
+                }
+              }
+              m = renew ? m_new : m;
             }
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            l += sum;
+            tmem_st16(t_s + 32 * half, w);  // over S of the keys read before
+            tmem_st16(t_s + 32 * half + 16, w + 16);
             tmem_wait_st();
           }
           tc_fence_before();
@@ -949,32 +961,57 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
         const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
         const long long token = g.token0 + tok;
         const int h = g.h * p.G + head;
-        uint16_t* out = static_cast<uint16_t*>(p.out) + token * p.out_stride_t + h * p.out_stride_h;
         const long long at = static_cast<long long>(slot_of) * (QT * kRows) + tok * p.G + head;
-        float* part = p.part + at * D;
+        // this row in out or in the workspace; both are whole 16-byte pieces
+        char* const to = whole ? static_cast<char*>(p.out) +
+                                     2 * (token * p.out_stride_t + h * p.out_stride_h)
+                               : reinterpret_cast<char*>(p.part + at * D);
+        const unsigned rows = __ballot_sync(kFull, mine);
+        // 64 bytes of every row of the warp: v holds this lane's.  A lane's
+        // own row would go out 16 bytes at a time to 32 places; turned through
+        // shared memory (pieces swizzled against bank conflicts) four lanes
+        // write 64 bytes of one row.
+        auto store64 = [&](const uint4(&v)[4], int offset) {
+          if (true) {
 #pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (mine) *reinterpret_cast<uint4*>(to + offset + 16 * q) = v[q];
+            return;
+          }
+          uint4* turn = reinterpret_cast<uint4*>(smem + L::kOffTurn) + (warp - 4) * 128;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) turn[lane * 4 + (q ^ (lane >> 1 & 3))] = v[q];
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int r = 8 * q + (lane >> 2), piece = lane & 3;
+            char* row_to = reinterpret_cast<char*>(
+                __shfl_sync(kFull, reinterpret_cast<unsigned long long>(to), r));
+            const uint4 u = turn[r * 4 + (piece ^ (r >> 1 & 3))];
+            if (rows >> r & 1) *reinterpret_cast<uint4*>(row_to + offset + 16 * piece) = u;
+          }
+          __syncwarp();
+        };
+#pragma unroll 1
         for (int i = 0; i < D / 32; ++i) {
           float o[32];
           tmem_ld32(t_o + 32 * i, o);
           tmem_wait_ld(o);
-          if (mine && whole) {
+          if (whole) {
+            uint4 v[4];
 #pragma unroll
-            for (int q = 0; q < 32; q += 8) {
-              uint4 v;
-              v.x = pack2<BF16>(o[q] * inv, o[q + 1] * inv);
-              v.y = pack2<BF16>(o[q + 2] * inv, o[q + 3] * inv);
-              v.z = pack2<BF16>(o[q + 4] * inv, o[q + 5] * inv);
-              v.w = pack2<BF16>(o[q + 6] * inv, o[q + 7] * inv);
-              if (l == 0.0f) v = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4*>(out + 32 * i + q) = v;
+            for (int q = 0; q < 4; ++q) {
+              v[q].x = pack2<BF16>(o[8 * q] * inv, o[8 * q + 1] * inv);
+              v[q].y = pack2<BF16>(o[8 * q + 2] * inv, o[8 * q + 3] * inv);
+              v[q].z = pack2<BF16>(o[8 * q + 4] * inv, o[8 * q + 5] * inv);
+              v[q].w = pack2<BF16>(o[8 * q + 6] * inv, o[8 * q + 7] * inv);
+              if (l == 0.0f) v[q] = make_uint4(0, 0, 0, 0);
             }
-          } else if (mine) {
-#pragma unroll
-            for (int q = 0; q < 32; q += 4)
-              *reinterpret_cast<float4*>(part + 32 * i + q) =
-                  make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
+            store64(v, 64 * i);
+          } else {
+            store64(*reinterpret_cast<const uint4(*)[4]>(o), 128 * i);
+            store64(*reinterpret_cast<const uint4(*)[4]>(o + 16), 128 * i + 64);
           }
-          __syncwarp();
         }
         if (mine) {
           if (!whole)
