@@ -475,7 +475,7 @@ struct Segment {
   int begin, end;  // key blocks of the tile; end -1: there is no more work
   int sink_blocks, main_block, blocks;
   int hi, lo;
-  int pos0, tokens, token0, h;
+  int pos0, tokens, token0, h, b;
   int last_cta;    // of an item that starts here and goes on, else -1
 };
 // The load warp is at most two segments ahead of the slowest reader: it
@@ -489,7 +489,7 @@ struct ASmem {
   static constexpr int kTileBytes = kRows * D * 2;          // a query tile
   static constexpr int kQBytes = QT * kTileBytes;
   // two tiles: 2 KB per softmax warp through which rows are turned for stores
-  static constexpr int kTurnBytes = 0;
+  static constexpr int kTurnBytes = QT == 1 ? 0 : 16384;
   // units of the ring: 5 or 6 with two CTAs per SM, 9 or 11 with one
   static constexpr int kStages = ((QT == 1 ? 114688 : 229376) - kQBytes - kTurnBytes) / kUnitBytes;
   static constexpr int kVKeys = kKeys / kPanels;            // keys of a V unit
@@ -498,7 +498,7 @@ struct ASmem {
   static constexpr int kOffSeg = kOffTurn + kTurnBytes;
   static constexpr int kOffBar = kOffSeg + kSegments * static_cast<int>(sizeof(Segment));
   // barriers: full[S], empty[S], qfull, qempty, drain, segment[4], then per
-  // query tile sfull, pready[2], odone[2]
+  // query tile sfull, pready[2], ohalf, ofull
   static constexpr int kBars = 2 * kStages + 3 + kSegments + 5 * QT;
   static constexpr int kOffTmem = kOffBar + 8 * kBars;
   static constexpr int kOffAbort = kOffTmem + 4;
@@ -508,6 +508,7 @@ struct ASmem {
 
 // `rows` shared-memory rows of 128 bytes from `at` set to `word` by a warp.
 __device__ __forceinline__ void fill_rows(uint32_t at, int rows, uint32_t word) {
+#pragma unroll 1
   for (int i = threadIdx.x & 31; i < rows * 8; i += 32)
     asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + 16 * i), "r"(word)
                  : "memory");
@@ -590,136 +591,149 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape<QT>::kRegsFew));
-    if (warp == 0) {
+    if (warp == 0 || warp == 2) {
       // ---------------------------------------------- loads
+      // Warp 0 divides the work and loads Q and K, warp 2 loads V: with pages
+      // of 16 keys a block takes 32 copies, which one warp issues too slowly.
+      const bool keys = warp == 0;
       Cursor c = {};
       Share share = {0, 0, 0, 0};
       long long want = blockIdx.x;  // an item, or a key block
-      if (p.split) {
+      bool more = true, placed = false;
+      if (keys && p.split) {
         share = my_share(p);
         want = share.begin;
+        more = share.begin < share.end;
+        if (lane == 0) p.meta[blockIdx.x].x = -1;
       }
-      bool more = !p.split || share.begin < share.end, placed = false;
-      if (p.split && lane == 0) p.meta[blockIdx.x].x = -1;
       const int boxes = kKeys / p.box;
       const uint32_t box_bytes = static_cast<uint32_t>(p.box) * 128u;  // of one panel
-      int slot = 0, units = 0, queries = 0;  // the ring's next place; what was loaded
+      const int per = L::kVKeys / p.box;     // boxes of a V unit
+      int unit = keys ? 0 : kP;              // the ring's units alternate: kP of K, kP of V
+      int slot = unit, loads = 0, queries = 0;
       uint32_t phase = 1;                    // parity of the place's last release
       bool ok = true;
-      // waits until the ring's next unit may be written, and passes on
-      auto acquire = [&]() {
-        const int s = slot;
-        ok = ok && (units < S || wait_soon(empty(s), phase, abort_flag));
-        ok = __all_sync(kFull, ok);
-        if (ok) {
-          ++units;
-          if (++slot == S) slot = 0, phase ^= 1;
-        }
-        return s;
-      };
-      for (int seg = 0;; ++seg) {
-        if (seg > 0) ok = __all_sync(kFull, wait_soon(qempty, (seg & 1) ^ 1, abort_flag));
-        if (!ok) break;
-        if (more && !placed) {
-          more = seek(p, c, want, p.split ? share.end - share.begin : 1LL << 40);
-          placed = p.split;
-        }
-        const Tile& tile = c.tile;
-        if (lane == 0) {
-          Segment& g = segments[seg % kSegments];
-          g.begin = c.begin;
-          g.end = more ? c.end : -1;
-          g.sink_blocks = tile.sink_blocks;
-          g.main_block = tile.main_block;
-          g.blocks = tile.blocks;
-          g.hi = tile.hi;
-          g.lo = tile.lo;
-          g.pos0 = tile.pos0;
-          g.tokens = tile.tokens;
-          g.token0 = tile.token0;
-          g.h = c.h;
-          g.last_cta = -1;
-          if (more && p.split && c.begin == 0 && c.end < tile.blocks)
-            g.last_cta = cta_of(share, share.end - 1 + (tile.blocks - c.end));
-          mbar_arrive(segment_ready(seg));
-          if (more) {
-            mbar_arrive_expect_tx(qfull, QT * kP * p.G * p.q_tokens * 128);
-            for (int j = 0; j < QT; ++j)
-              for (int pn = 0; pn < kP; ++pn)
-                tma_load_3d(sbase + j * L::kTileBytes + pn * kRows * 128, &tq, pn * 64, c.h * p.G,
-                            tile.token0 + j * p.q_tokens, qfull);
+      for (int seg = 0; ok; ++seg) {
+        if (keys) {
+          if (seg > 0) ok = __all_sync(kFull, wait_soon(qempty, (seg & 1) ^ 1, abort_flag));
+          if (!ok) break;
+          if (more && !placed) {
+            more = seek(p, c, want, p.split ? share.end - share.begin : 1LL << 40);
+            placed = p.split;
           }
+          if (lane == 0) {
+            const Tile& tile = c.tile;
+            Segment& g = segments[seg % kSegments];
+            g.begin = c.begin;
+            g.end = more ? c.end : -1;
+            g.sink_blocks = tile.sink_blocks;
+            g.main_block = tile.main_block;
+            g.blocks = tile.blocks;
+            g.hi = tile.hi;
+            g.lo = tile.lo;
+            g.pos0 = tile.pos0;
+            g.tokens = tile.tokens;
+            g.token0 = tile.token0;
+            g.h = c.h;
+            g.b = c.b;
+            g.last_cta = -1;
+            if (more && p.split && c.begin == 0 && c.end < tile.blocks)
+              g.last_cta = cta_of(share, share.end - 1 + (tile.blocks - c.end));
+            mbar_arrive(segment_ready(seg));
+            if (more) {
+              mbar_arrive_expect_tx(qfull, QT * kP * p.G * p.q_tokens * 128);
+              for (int j = 0; j < QT; ++j)
+                for (int pn = 0; pn < kP; ++pn)
+                  tma_load_3d(sbase + j * L::kTileBytes + pn * kRows * 128, &tq, pn * 64,
+                              c.h * p.G, tile.token0 + j * p.q_tokens, qfull);
+            }
+          }
+          __syncwarp();
+          queries += more ? 1 : 0;
+        } else {
+          ok = __all_sync(kFull, wait_soon(segment_ready(seg), (seg / kSegments) & 1, abort_flag));
+          if (!ok) break;
         }
-        __syncwarp();
-        if (!more) break;
-        ++queries;
+        const Segment& g = segments[seg % kSegments];
+        const int begin = g.begin, end = g.end, hi = g.hi, lo = g.lo, h = g.h;
+        const int sink_blocks = g.sink_blocks, skip = g.main_block - sink_blocks;
+        if (end < 0) break;
+        const int* table = p.block_table + g.b * p.bt_stride;
         // box l of a block: its page, -1 if no row sees any of its keys, -2 if
         // the table names no page of the pool for it
-        const int* table = p.block_table + c.b * p.bt_stride;
-        auto lookup = [&](int k) {
-          const int key = tile.block(k) * kKeys + lane * p.box;
-          if (lane >= boxes || key >= tile.hi || (key + p.box <= tile.lo && key >= p.sinks))
-            return -1;
+        auto lookup = [&](int key0) {
+          const int key = key0 + lane * p.box;
+          if (lane >= boxes || key >= hi || (key + p.box <= lo && key >= p.sinks)) return -1;
           const int page = __ldg(table + key / p.page);
           return page >= 0 && page < p.num_pages ? page : -2;
         };
-        int page = lookup(c.begin);
-        for (int k = c.begin; k < c.end && ok; ++k) {
-          const int in_page = (tile.block(k) * kKeys + lane * p.box) % p.page;
-          const int next = k + 1 < c.end ? lookup(k + 1) : -1;
+        auto first_key = [&](int k) { return (k < sink_blocks ? k : k + skip) * kKeys; };
+        int page = lookup(first_key(begin));
+        for (int k = begin; k < end; ++k) {
+          const int in_page = (first_key(k) + lane * p.box) % p.page;
+          const int next = k + 1 < end ? lookup(first_key(k + 1)) : -1;
           const unsigned loaded = __ballot_sync(kFull, page >= 0);
           const unsigned bad = __ballot_sync(kFull, page == -2);
           const unsigned gone = ~loaded & ((1u << boxes) - 1u);
-          if (bad && lane == 0 && p.err) atomicOr(p.err, DSA_DEVERR_SLOT);
-          for (int pn = 0; pn < kP; ++pn) {  // K: 64 dims of all 128 keys
-            const int s = acquire();
+          if (keys && bad && lane == 0 && p.err) atomicOr(p.err, DSA_DEVERR_SLOT);
+          for (int i = 0; i < kP; ++i) {
+            // the ring's next unit, once it may be written
+            ok = unit < S || wait_soon(empty(slot), phase, abort_flag);
+            ok = __all_sync(kFull, ok);
             if (!ok) break;
-            const uint32_t at = sbase + L::kOffRing + s * kUnitBytes;
-            if (bad && pn == 0) {  // NaN keys, so the rows that see them become NaN
-              for (unsigned m = bad; m; m &= m - 1)
-                fill_rows(at + (__ffs(m) - 1) * box_bytes, p.box, 0x7fff7fffu);
-              fence_async_shared();
+            const uint32_t at = sbase + L::kOffRing + slot * kUnitBytes, bar = full(slot);
+            if (keys) {  // 64 dims of all 128 keys
+              if (bad && i == 0) {  // NaN keys, so the rows that see them become NaN
+                for (unsigned m = bad; m; m &= m - 1)
+                  fill_rows(at + (__ffs(m) - 1) * box_bytes, p.box, 0x7fff7fffu);
+                fence_async_shared();
+                __syncwarp();
+              }
+              if (lane == 0) mbar_arrive_expect_tx(bar, __popc(loaded) * box_bytes);
               __syncwarp();
-            }
-            if (lane == 0) mbar_arrive_expect_tx(full(s), __popc(loaded) * box_bytes);
-            __syncwarp();
-            if (page >= 0)
-              tma_load_4d(at + lane * box_bytes, &tk, pn * 64, in_page, c.h, page, full(s));
-          }
-          for (int u = 0; u < kP && ok; ++u) {  // V: all dims of kVKeys keys
-            const int s = acquire();
-            if (!ok) break;
-            const uint32_t at = sbase + L::kOffRing + s * kUnitBytes;
-            const int per = L::kVKeys / p.box;  // boxes of the unit
-            const unsigned here = ((1u << per) - 1u) << (u * per);
-            if (gone & here) {  // P is 0 there, and 0 * V must not be NaN
-              for (unsigned m = gone & here; m; m &= m - 1)
+              if (page >= 0) tma_load_4d(at + lane * box_bytes, &tk, i * 64, in_page, h, page, bar);
+            } else {  // all dims of kVKeys keys
+              const unsigned here = ((1u << per) - 1u) << (i * per);
+              if (gone & here) {  // P is 0 there, and 0 * V must not be NaN
+                for (unsigned m = gone & here; m; m &= m - 1)
+                  for (int pn = 0; pn < kP; ++pn)
+                    fill_rows(at + pn * L::kVKeys * 128 + (__ffs(m) - 1 - i * per) * box_bytes,
+                              p.box, 0u);
+                fence_async_shared();
+                __syncwarp();
+              }
+              if (lane == 0) mbar_arrive_expect_tx(bar, kP * __popc(loaded & here) * box_bytes);
+              __syncwarp();
+              if (page >= 0 && lane / per == i)
                 for (int pn = 0; pn < kP; ++pn)
-                  fill_rows(at + pn * L::kVKeys * 128 + (__ffs(m) - 1 - u * per) * box_bytes, p.box,
-                            0u);
-              fence_async_shared();
-              __syncwarp();
+                  tma_load_4d(at + pn * L::kVKeys * 128 + (lane - i * per) * box_bytes, &tv,
+                              pn * 64, in_page, h, page, bar);
             }
-            if (lane == 0) mbar_arrive_expect_tx(full(s), kP * __popc(loaded & here) * box_bytes);
-            __syncwarp();
-            if (page >= 0 && lane / per == u)
-              for (int pn = 0; pn < kP; ++pn)
-                tma_load_4d(at + pn * L::kVKeys * 128 + (lane - u * per) * box_bytes, &tv, pn * 64,
-                            in_page, c.h, page, full(s));
+            ++unit, ++loads;
+            if (++slot == S) slot = 0, phase ^= 1;
           }
+          if (!ok) break;
+          unit += kP, slot += kP;  // the other warp's
+          if (slot >= S) slot -= S, phase ^= 1;
           page = next;
         }
-        if (!ok) break;
+        if (!ok || !keys) continue;
         if (p.split)
           more = next_segment(p, c);
         else
           want += gridDim.x;
       }
-      if (!ok && lane == 0) give_up();
-      volatile int never = 0;  // stay until every load issued has landed
-      for (int d = units > S ? units - S : 0; d < units; ++d)
-        wait_soon(full(d % S), (d / S) & 1, &never);
-      if (queries > 0) wait_soon(qfull, (queries - 1) & 1, &never);
+      if (!ok) {
+        if (lane == 0) give_up();
+        // Stay until the loads issued have landed (else the MMA warp has waited
+        // for each of them).
+        volatile int never = 0;
+        for (int n = 0, d = unit; n < loads && n < S / 2; ++n) {
+          d -= d % (2 * kP) == (keys ? 0 : kP) ? kP + 1 : 1;
+          wait_soon(full(d % S), (d / S) & 1, &never);
+        }
+        if (queries > 0) wait_soon(qfull, (queries - 1) & 1, &never);
+      }
     } else if (warp == 1) {
       // ---------------------------------------------- MMA issuer
       // Query tile j's scores of block k + 1 follow its P V of block k at once:
@@ -736,29 +750,29 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
       int slot = 0;                        // ring place of the block's first K unit
       uint32_t phase = 0, parity = 0;      // its parity; the blocks' parity
       bool ok = true;
-      auto arrived = [&](int unit) {       // the unit-th one from the block's first
-        int s = slot + unit;
-        uint32_t ph = phase;
-        if (s >= S) s -= S, ph ^= 1;
-        ok = wait_soon(full(s), ph, abort_flag) && ok;
-        return s;
+      auto place = [&](int unit) {         // of the unit-th one from the block's first
+        const int s = slot + unit;
+        return s >= S ? s - S : s;
+      };
+      auto arrived = [&](int unit) {
+        const int s = slot + unit;
+        ok = wait_soon(full(s >= S ? s - S : s), s >= S ? phase ^ 1 : phase, abort_flag) && ok;
       };
       auto scores = [&](int j, int unit) {  // S_j = Q_j K^T
+        if (leader && ok) {
 #pragma unroll
-        for (int pn = 0; pn < kP; ++pn) {
-          const int s = arrived(unit + pn);
-          tc_fence_after();
-          if (leader && ok) {
+          for (int pn = 0; pn < kP; ++pn) {
+            const int s = place(unit + pn);
             const uint32_t a = q_lo + ((j * L::kTileBytes + pn * kRows * 128) >> 4);
             const uint32_t b = k_lo + s * (kUnitBytes >> 4);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_ss(tmem_s(j), make_desc(a + 2 * ks), make_desc(b + 2 * ks), idesc_s,
-                     pn + ks > 0 ? 1u : 0u);
+              mma_ss(tmem_s(j), make_desc(a + 2 * ks), make_desc(b + 2 * ks),
+                     idesc_s, pn + ks > 0 ? 1u : 0u);
             if (j + 1 == QT) mma_commit(empty(s));
           }
+          mma_commit(sfull(j));
         }
-        if (leader && ok) mma_commit(sfull(j));
       };
       for (int seg = 0; ok; ++seg) {
         ok = __all_sync(kFull, wait_soon(segment_ready(seg), (seg / kSegments) & 1, abort_flag));
@@ -766,34 +780,43 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
         if (!ok || end < 0) break;
         ok = wait_soon(qfull, seg & 1, abort_flag);
 #pragma unroll
+        for (int pn = 0; pn < kP; ++pn) arrived(pn);
+        tc_fence_after();
+#pragma unroll
         for (int j = 0; j < QT; ++j) scores(j, 0);
         if (leader && ok && begin + 1 == end) mma_commit(qempty);
         for (int k = begin; k < end; ++k) {
+          // O += P V of half a block, then the next scores where S is free
+          auto values = [&](int j, int half) {
+            const int u = half * kP / 2;           // its V unit of the block
+            const bool more = half == 1 && k + 1 < end;
+            // the loads first, at their first use: they are there before P is
+            if (j == 0) {
+              if (half == 0 || kP == 2) arrived(kP + u);
+              if (more) {
 #pragma unroll
-          for (int j = 0; j < QT; ++j) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {   // of the block's keys
-              const int u = half * kP / 2;           // its V unit of the block
-              ok = wait_soon(pready(j, half), parity, abort_flag) && ok;
-              const int s = arrived(kP + u);
-              tc_fence_after();
-              if (leader && ok) {
-                const int row = half * (kKeys / 2) - u * L::kVKeys;  // its first key in the unit
-                const uint32_t b = v_lo + s * (kUnitBytes >> 4) + (row * 128 >> 4);
-#pragma unroll
-                for (int ks = 0; ks < kKeys / 32; ++ks)
-                  mma_ts(tmem_o(j), tmem_s(j) + half * (kKeys / 4) + ks * 8,
-                         make_desc(b + ks * (2048 >> 4)), idesc_o,
-                         (k > begin || half + ks > 0) ? 1u : 0u);
-                if (j + 1 == QT && (kP == 2 || half == 1)) mma_commit(empty(s));
-                if (half == 0) mma_commit(ohalf(j));
+                for (int pn = 0; pn < kP; ++pn) arrived(2 * kP + pn);
               }
             }
-            if (k + 1 < end)
-              scores(j, 2 * kP);
-            else if (leader && ok)
-              mma_commit(ofull(j));
-          }
+            ok = wait_soon(pready(j, half), parity, abort_flag) && ok;
+            const int s = place(kP + u);
+            tc_fence_after();
+            if (leader && ok) {
+              const int row = half * (kKeys / 2) - u * L::kVKeys;  // its first key in the unit
+              const uint32_t b = v_lo + s * (kUnitBytes >> 4) + (row * 128 >> 4);
+#pragma unroll
+              for (int ks = 0; ks < kKeys / 32; ++ks)
+                mma_ts(tmem_o(j), tmem_s(j) + half * (kKeys / 4) + ks * 8,
+                       make_desc(b + ks * (2048 >> 4)), idesc_o,
+                       (k > begin || half + ks > 0) ? 1u : 0u);
+              if (j + 1 == QT && (kP == 2 || half == 1)) mma_commit(empty(s));
+              if (half == 0) mma_commit(ohalf(j));
+              if (half == 1 && k + 1 == end) mma_commit(ofull(j));
+            }
+            if (more) scores(j, 2 * kP);
+          };
+#pragma unroll
+          for (int i = 0; i < 2 * QT; ++i) values(i / 2, i % 2);
           if (leader && ok && k + 2 == end) mma_commit(qempty);
           parity ^= 1;
           slot += 2 * kP;
@@ -919,8 +942,8 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
                                             : fmaxf(mx[q], s[i + q]);
               const float m_new = max3f(m, fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
               if (k > begin || half == 1) {  // O exists
-                // it is complete up to the half before: sfull followed the
-                // products of the block before
+                // and has to be complete up to the half before; sfull followed
+                // the products of the block before
                 if (half == 1) ok = __all_sync(kFull, wait_soon(ohalf(j), parity, abort_flag));
                 tc_fence_after();
                 // a first maximum meets O and l that are still 0
@@ -972,7 +995,7 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
         // shared memory (pieces swizzled against bank conflicts) four lanes
         // write 64 bytes of one row.
         auto store64 = [&](const uint4(&v)[4], int offset) {
-          if (true) {
+          if (QT == 1) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               if (mine) *reinterpret_cast<uint4*>(to + offset + 16 * q) = v[q];
