@@ -15,6 +15,7 @@ fold, and the paged index-K cache write.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import os
@@ -31,7 +32,7 @@ __all__ = [
     "dsa_indexer_qk_prepare_store", "dsa_indexer_k_prepare_store", "dsa_status_string",
     "dsa_indexer_qk_prepare_store_unfused", "dsa_unfused_workspace_bytes",
     "dsa_indexer_qk_prepare_store_unfused_noalloc", "dsa_indexer_mqa_logits",
-    "dsa_paged_attention", "dsa_paged_attention_workspace_bytes",
+    "dsa_paged_attention", "dsa_paged_attention_workspace_bytes", "prepare_paged_attention",
     "dsa_cache_copy_pages", "dsa_cache_fork", "dsa_cache_free", "dsa_cache_compact",
     "dsa_cache_fork_workspace_bytes", "dsa_cache_compact_workspace_bytes",
     "library", "cache_bytes", "cache_views",
@@ -214,8 +215,10 @@ def _on(device):
 
 
 def _stream(stream, device=None) -> int:
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+    if stream is None:  # torch.cuda.current_stream(device).cuda_stream without the object
+        index = torch.cuda.current_device() if device is None or device.index is None \
+            else device.index
+        return torch._C._cuda_getCurrentRawStream(index)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -547,6 +550,61 @@ def dsa_paged_attention_workspace_bytes(T: int, B: int, H: int, Hkv: int, head_d
         int(T), int(B), int(H), int(Hkv), int(head_dim), int(max_context)))
 
 
+def _attention_args(q, k_cache, v_cache, block_table, query_start, context_lens, max_context,
+                    scale, window, sinks, out, lse, workspace, err_flags, pdl, stream):
+    """Checks and the C argument list; also returns the outputs and the workspace."""
+    _need(q, "q", (torch.bfloat16, torch.float16), 3)
+    dev, dtype = q.device, q.dtype
+    _need(k_cache, "k_cache", dtype, 4, dev)
+    _need(v_cache, "v_cache", dtype, 4, dev)
+    _need(block_table, "block_table", torch.int32, 2, dev)
+    _need(query_start, "query_start", torch.int32, 1, dev)
+    _need(context_lens, "context_lens", torch.int32, 1, dev)
+    T, H, D = q.shape
+    num_pages, page_size, Hkv, k_dim = shape = k_cache.shape
+    if v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache differ in shape")
+    if k_dim != D:
+        raise ValueError(f"q has head_dim {D}, the caches {k_dim}")
+    if Hkv < 1 or H % Hkv:
+        raise ValueError("H must be a multiple of the caches' heads")
+    B = query_start.shape[0] - 1
+    max_context = int(max_context)
+    if B < 0:
+        raise ValueError("query_start must hold B + 1 entries")
+    rows, cols = block_table.shape
+    if rows < B or cols * page_size < max_context:
+        raise ValueError("block_table must be [B, >= ceil(max_context / page_size)]")
+    if context_lens.shape[0] < B:
+        raise ValueError(f"context_lens has fewer than {B} entries")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=dtype, device=dev)
+    else:
+        _need(out, "out", dtype, 3, dev)
+        if out.shape[0] < T or out.shape[1:] != q.shape[1:]:
+            raise ValueError("out must be [T, H, D]")
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    else:
+        _need(lse, "lse", torch.float32, 2, dev)
+        if not lse.is_contiguous() or lse.shape[0] < T or lse.shape[1] != H:
+            raise ValueError("lse must be contiguous [T, H]")
+    need = library().dsa_paged_attention_workspace_bytes(T, B, H, Hkv, D, max_context)
+    ws = ws_bytes = 0
+    if need or workspace is not None:
+        workspace, ws, ws_bytes = _scratch(workspace, need, dev)
+    qs, ks, vs, os_, ts = (q.stride(), k_cache.stride(), v_cache.stride(), out.stride(),
+                           block_table.stride(0))
+    args = (q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2],
+            vs[0], vs[1], vs[2], num_pages, page_size, block_table.data_ptr(),
+            ts if ts > cols or rows > 1 else cols, query_start.data_ptr(), context_lens.data_ptr(),
+            max_context, D ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
+            os_[0], os_[1], lse.data_ptr(), T, B, H, Hkv, D, _ATTENTION_DTYPES[dtype],
+            FLAG_PDL if pdl else 0, ws or None, ws_bytes, _err_ptr(err_flags, dev),
+            _stream(stream, dev))
+    return args, out, lse, workspace
+
+
 def dsa_paged_attention(q, k_cache, v_cache, block_table, query_start, context_lens, max_context, *,
                         scale=None, window=0, sinks=0, out=None, lse=None, workspace=None,
                         err_flags=None, pdl=False, stream=None):
@@ -563,72 +621,44 @@ def dsa_paged_attention(q, k_cache, v_cache, block_table, query_start, context_l
     least dsa_paged_attention_workspace_bytes(...) bytes, allocated here when
     not given.  Returns (out [T, H, D], lse [T, H] fp32); rows that belong to
     no sequence are left as they are."""
-    _need(q, "q", (torch.bfloat16, torch.float16), 3)
-    dev = q.device
-    _need(k_cache, "k_cache", q.dtype, 4, dev)
-    _need(v_cache, "v_cache", q.dtype, 4, dev)
-    _need(block_table, "block_table", torch.int32, 2, dev)
-    _need(query_start, "query_start", torch.int32, 1, dev)
-    _need(context_lens, "context_lens", torch.int32, 1, dev)
-    T, H, D = q.shape
-    num_pages, page_size, Hkv, k_dim = k_cache.shape
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache differ in shape")
-    if k_dim != D:
-        raise ValueError(f"q has head_dim {D}, the caches {k_dim}")
-    if Hkv < 1 or H % Hkv:
-        raise ValueError("H must be a multiple of the caches' heads")
-    B = query_start.shape[0] - 1
-    max_context = int(max_context)
-    if B < 0:
-        raise ValueError("query_start must hold B + 1 entries")
-    if block_table.shape[0] < B or block_table.shape[1] * page_size < max_context:
-        raise ValueError("block_table must be [B, >= ceil(max_context / page_size)]")
-    if context_lens.shape[0] < B:
-        raise ValueError(f"context_lens has fewer than {B} entries")
-    if out is None:
-        out = torch.empty((T, H, D), dtype=q.dtype, device=dev)
-    _need(out, "out", q.dtype, 3, dev)
-    if out.shape[0] < T or out.shape[1:] != q.shape[1:]:
-        raise ValueError("out must be [T, H, D]")
-    if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-    _need(lse, "lse", torch.float32, 2, dev)
-    if not lse.is_contiguous() or lse.shape[0] < T or lse.shape[1] != H:
-        raise ValueError("lse must be contiguous [T, H]")
-    lib = library()
-    need = lib.dsa_paged_attention_workspace_bytes(T, B, H, Hkv, D, max_context)
-    keep, ws, ws_bytes = _scratch(workspace, need, dev) if need or workspace is not None \
-        else (None, None, 0)
-    with _on(dev):
-        st = lib.dsa_paged_attention(
-            q.data_ptr(), q.stride(0), q.stride(1), k_cache.data_ptr(), v_cache.data_ptr(),
-            k_cache.stride(0), k_cache.stride(1), k_cache.stride(2), v_cache.stride(0),
-            v_cache.stride(1), v_cache.stride(2), num_pages, page_size, block_table.data_ptr(),
-            max(block_table.stride(0), block_table.shape[1]), query_start.data_ptr(),
-            context_lens.data_ptr(), max_context, D ** -0.5 if scale is None else float(scale),
-            int(window), int(sinks), out.data_ptr(), out.stride(0), out.stride(1), lse.data_ptr(),
-            T, B, H, Hkv, D, _ATTENTION_DTYPES[q.dtype], FLAG_PDL if pdl else 0, ws, ws_bytes,
-            _err_ptr(err_flags, dev), _stream(stream, dev))
+    args, out, lse, workspace = _attention_args(
+        q, k_cache, v_cache, block_table, query_start, context_lens, max_context, scale, window,
+        sinks, out, lse, workspace, err_flags, pdl, stream)
+    with _on(q.device):
+        st = library().dsa_paged_attention(*args)
     if st != 0:
         raise DsaError(st, "dsa_paged_attention")
     return out, lse
 
 
+def prepare_paged_attention(q, k_cache, v_cache, block_table, query_start, context_lens,
+                            max_context, *, scale=None, window=0, sinks=0, out=None, lse=None,
+                            workspace=None, err_flags=None, pdl=False, stream=None):
+    """dsa_paged_attention checked and bound once: returns a PreparedCall that
+    launches it on these buffers, the workspace among them (see PreparedCall)."""
+    args, out, lse, workspace = _attention_args(
+        q, k_cache, v_cache, block_table, query_start, context_lens, max_context, scale, window,
+        sinks, out, lse, workspace, err_flags, pdl, stream)
+    keep = (q, k_cache, v_cache, block_table, query_start, context_lens, out, lse, workspace,
+            err_flags)
+    return PreparedCall(library().dsa_paged_attention, "dsa_paged_attention", args, q.device,
+                        (out, lse), keep)
+
+
 # ------------------------------------------------------- pages of a paged cache
 
 def _cache_arrays(caches, num_pages: int, device):
-    """The host arrays of base pointers and page sizes of the caches of a pool."""
-    n = len(caches)
-    bases, sizes = [0] * n, [0] * n
+    """The host arrays of base pointers and page sizes of the caches of a pool:
+    (keep, pointer to the bases, pointer to the sizes, count)."""
+    sizes = [t.nbytes for t in caches]
     for i, t in enumerate(caches):
-        if t.device != device or not t.is_contiguous():
+        if not t.is_contiguous() or t.device != device:
             raise ValueError(f"caches[{i}] must be a contiguous tensor on {device}")
-        nbytes = t.nbytes
-        if nbytes % num_pages or not nbytes:
+        if sizes[i] % num_pages or not sizes[i]:
             raise ValueError(f"caches[{i}] is not {num_pages} pages of equal size")
-        bases[i], sizes[i] = t.data_ptr(), nbytes // num_pages
-    return (ctypes.c_void_p * n)(*bases), (ctypes.c_int64 * n)(*sizes), n
+    keep = (array.array("Q", [t.data_ptr() for t in caches]),
+            array.array("q", [n // num_pages for n in sizes]))
+    return keep, keep[0].buffer_info()[0], keep[1].buffer_info()[0], len(sizes)
 
 
 def _pool(page_refs, block_table, context_lens):
@@ -678,7 +708,7 @@ def dsa_cache_copy_pages(caches, num_pages, src_pages, dst_pages, *, err_flags=N
         raise ValueError("src_pages and dst_pages differ in length")
     if int(num_pages) < 1:
         raise ValueError("num_pages must be at least 1")
-    bases, sizes, n = _cache_arrays(caches, int(num_pages), dev)
+    hold, bases, sizes, n = _cache_arrays(caches, int(num_pages), dev)
     with _on(dev):
         st = library().dsa_cache_copy_pages(
             bases, sizes, n, int(num_pages), src_pages.data_ptr(), dst, src_pages.shape[0], 0,
@@ -705,7 +735,7 @@ def dsa_cache_fork(caches, page_refs, block_table, context_lens, page_size, pare
     n = parents.shape[0]
     if children.shape[0] != n:
         raise ValueError("parents and children differ in length")
-    bases, sizes, n_caches = _cache_arrays(caches, num_pages, dev)
+    hold, bases, sizes, n_caches = _cache_arrays(caches, num_pages, dev)
     keep, ws, ws_bytes = _scratch(workspace, 8 * n, dev)
     with _on(dev):
         st = library().dsa_cache_fork(
@@ -743,7 +773,7 @@ def dsa_cache_compact(caches, page_refs, block_table, context_lens, page_size, *
     Returns live_pages, an int32 [1] CUDA tensor with the number of pages in
     use; the pages from there on are free."""
     dev, num_pages, pool = _pool(page_refs, block_table, context_lens)
-    bases, sizes, n_caches = _cache_arrays(caches, num_pages, dev)
+    hold, bases, sizes, n_caches = _cache_arrays(caches, num_pages, dev)
     if live_pages is None:
         live_pages = torch.empty(1, dtype=torch.int32, device=dev)
     _list(live_pages, "live_pages", dev)
