@@ -488,6 +488,10 @@ struct ASmem {
   static constexpr int kPanels = D / 64;                    // 128-byte panels of a row
   static constexpr int kTileBytes = kRows * D * 2;          // a query tile
   static constexpr int kQBytes = QT * kTileBytes;
+  // Places for S in TMEM.  With three for two tiles (where O leaves the room)
+  // a tile's next scores are formed while its softmax is still at this block;
+  // with one per tile they follow the block's P V.
+  static constexpr int kLook = QT == 1 ? 1 : D == 64 ? 3 : 2;
   // two tiles: 2 KB per softmax warp through which rows are turned for stores
   static constexpr int kTurnBytes = QT == 1 ? 0 : 16384;
   // units of the ring: 5 or 6 with two CTAs per SM, 9 or 11 with one
@@ -498,8 +502,8 @@ struct ASmem {
   static constexpr int kOffSeg = kOffTurn + kTurnBytes;
   static constexpr int kOffBar = kOffSeg + kSegments * static_cast<int>(sizeof(Segment));
   // barriers: full[S], empty[S], qfull, qempty, drain, segment[4], then per
-  // query tile sfull, pready[2], ohalf, ofull
-  static constexpr int kBars = 2 * kStages + 3 + kSegments + 5 * QT;
+  // query tile sfull[2], pready[2][2], ohalf, oblock, ofull
+  static constexpr int kBars = 2 * kStages + 3 + kSegments + 9 * QT;
   static constexpr int kOffTmem = kOffBar + 8 * kBars;
   static constexpr int kOffAbort = kOffTmem + 4;
   static constexpr int kBytes = kOffAbort + 4;
@@ -536,11 +540,19 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
   const uint32_t drain = bar0 + 8 * (2 * S + 2);
   auto segment_ready = [&](int i) { return bar0 + 8 * (2 * S + 3 + i % kSegments); };
   constexpr int kB = 2 * S + 3 + kSegments;
-  auto sfull = [&](int j) { return bar0 + 8 * (kB + 5 * j); };
-  auto pready = [&](int j, int half) { return bar0 + 8 * (kB + 1 + 5 * j + half); };
-  // O with the first half of a block's keys; with the last block of a segment
-  auto ohalf = [&](int j) { return bar0 + 8 * (kB + 3 + 5 * j); };
-  auto ofull = [&](int j) { return bar0 + 8 * (kB + 4 + 5 * j); };
+  // Of the n-th block.  With three places for S the scores of a tile's next
+  // block may be there while some warp of it is still at this one: the others
+  // go on, so two blocks take turns at these barriers.
+  constexpr int kLook = L::kLook, kTurns = kLook == 3 ? 2 : 1;
+  auto turn = [](int n) { return static_cast<uint32_t>(n / kTurns) & 1u; };  // its parity
+  auto sfull = [&](int j, int n) { return bar0 + 8 * (kB + 9 * j + n % kTurns); };
+  auto pready = [&](int j, int half, int n) {
+    return bar0 + 8 * (kB + 2 + 9 * j + 2 * half + n % kTurns);
+  };
+  // O with the first half of a block's keys; with all; with a segment's last
+  auto ohalf = [&](int j) { return bar0 + 8 * (kB + 6 + 9 * j); };
+  auto oblock = [&](int j) { return bar0 + 8 * (kB + 7 + 9 * j); };
+  auto ofull = [&](int j) { return bar0 + 8 * (kB + 8 + 9 * j); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffAbort);
   Segment* const segments = reinterpret_cast<Segment*>(smem + L::kOffSeg);
   const int warp = threadIdx.x >> 5;
@@ -561,8 +573,11 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
     mbar_init(drain, 1);
     for (int i = 0; i < kSegments; ++i) mbar_init(segment_ready(i), 1);
     for (int j = 0; j < QT; ++j) {
-      mbar_init(sfull(j), 1);
-      for (int h = 0; h < 2; ++h) mbar_init(pready(j, h), 4);  // the tile's softmax warps
+      for (int n = 0; n < kTurns; ++n) {
+        mbar_init(sfull(j, n), 1);
+        for (int h = 0; h < 2; ++h) mbar_init(pready(j, h, n), 4);  // the tile's softmax warps
+      }
+      mbar_init(oblock(j), 1);
       mbar_init(ohalf(j), 1);
       mbar_init(ofull(j), 1);
     }
@@ -578,8 +593,8 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kOffTmem);
-  auto tmem_s = [&](int j) { return tmem + j * kKeys; };
-  auto tmem_o = [&](int j) { return tmem + QT * kKeys + j * D; };
+  auto tmem_s = [&](int i) { return tmem + i * kKeys; };  // the i-th place for S
+  auto tmem_o = [&](int j) { return tmem + kLook * kKeys + j * D; };
 
   grid_dependency_wait();
   grid_launch_dependents();
@@ -736,11 +751,11 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
       }
     } else if (warp == 1) {
       // ---------------------------------------------- MMA issuer
-      // Query tile j's scores of block k + 1 follow its P V of block k at once:
-      // the other tile's softmax runs meanwhile.  Products issued by one thread
-      // are carried out in their order, so S may be overwritten behind P V.  The
-      // warp stays together, one lane issues, and the ring's places are counted,
-      // not divided: at three hand-overs a block this code's own time counts.
+      // The steps go from block to block and tile to tile.  Behind the P V of
+      // step n come the scores of step n + kLook, into the same place of TMEM:
+      // products issued by one thread are carried out in their order.  The warp
+      // stays together, one lane issues, and the ring's places are counted, not
+      // divided: at three hand-overs a step this code's own time counts.
       constexpr uint32_t idesc_s = mma_idesc(BF16, false, kKeys);
       constexpr uint32_t idesc_o = mma_idesc(BF16, true, D);
       const bool leader = elect_one();
@@ -748,7 +763,8 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
       const uint32_t k_lo = desc_lo(sbase + L::kOffRing, 0);
       const uint32_t v_lo = desc_lo(sbase + L::kOffRing, L::kVKeys * 128);
       int slot = 0;                        // ring place of the block's first K unit
-      uint32_t phase = 0, parity = 0;      // its parity; the blocks' parity
+      uint32_t phase = 0;                  // its parity
+      int block = 0, first = 0;            // blocks done; place for S of tile 0's block
       bool ok = true;
       auto place = [&](int unit) {         // of the unit-th one from the block's first
         const int s = slot + unit;
@@ -758,67 +774,74 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
         const int s = slot + unit;
         ok = wait_soon(full(s >= S ? s - S : s), s >= S ? phase ^ 1 : phase, abort_flag) && ok;
       };
-      auto scores = [&](int j, int unit) {  // S_j = Q_j K^T
+      // S = Q_j K^T of the block `ahead` of this one
+      auto scores = [&](int j, int ahead, int at) {
         if (leader && ok) {
 #pragma unroll
           for (int pn = 0; pn < kP; ++pn) {
-            const int s = place(unit + pn);
+            const int s = place(2 * kP * ahead + pn);
             const uint32_t a = q_lo + ((j * L::kTileBytes + pn * kRows * 128) >> 4);
             const uint32_t b = k_lo + s * (kUnitBytes >> 4);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_ss(tmem_s(j), make_desc(a + 2 * ks), make_desc(b + 2 * ks),
-                     idesc_s, pn + ks > 0 ? 1u : 0u);
+              mma_ss(tmem_s(at), make_desc(a + 2 * ks), make_desc(b + 2 * ks), idesc_s,
+                     pn + ks > 0 ? 1u : 0u);
             if (j + 1 == QT) mma_commit(empty(s));
           }
-          mma_commit(sfull(j));
+          mma_commit(sfull(j, block + ahead));
         }
+      };
+      auto keys_arrived = [&](int ahead) {
+#pragma unroll
+        for (int pn = 0; pn < kP; ++pn) arrived(2 * kP * ahead + pn);
+      };
+      auto place_of = [&](int j) {  // for S of tile j's block
+        return kLook < 3 ? j : first + j < 3 ? first + j : first + j - 3;
       };
       for (int seg = 0; ok; ++seg) {
         ok = __all_sync(kFull, wait_soon(segment_ready(seg), (seg / kSegments) & 1, abort_flag));
         const int begin = segments[seg % kSegments].begin, end = segments[seg % kSegments].end;
         if (!ok || end < 0) break;
         ok = wait_soon(qfull, seg & 1, abort_flag);
-#pragma unroll
-        for (int pn = 0; pn < kP; ++pn) arrived(pn);
+        keys_arrived(0);
+        if (kLook == 3 && begin + 1 < end) keys_arrived(1);
         tc_fence_after();
 #pragma unroll
-        for (int j = 0; j < QT; ++j) scores(j, 0);
+        for (int j = 0; j < QT; ++j) scores(j, 0, place_of(j));
+        if (kLook == 3 && begin + 1 < end) scores(0, 1, place_of(2));
         if (leader && ok && begin + 1 == end) mma_commit(qempty);
         for (int k = begin; k < end; ++k) {
-          // O += P V of half a block, then the next scores where S is free
+          // O += P V of half a block, then the scores of kLook steps on
           auto values = [&](int j, int half) {
             const int u = half * kP / 2;           // its V unit of the block
-            const bool more = half == 1 && k + 1 < end;
+            const int ahead = (j + kLook) / QT, then = (j + kLook) % QT;
+            const bool more = half == 1 && k + ahead < end;
             // the loads first, at their first use: they are there before P is
-            if (j == 0) {
-              if (half == 0 || kP == 2) arrived(kP + u);
-              if (more) {
-#pragma unroll
-                for (int pn = 0; pn < kP; ++pn) arrived(2 * kP + pn);
-              }
-            }
-            ok = wait_soon(pready(j, half), parity, abort_flag) && ok;
-            const int s = place(kP + u);
+            if (j == 0 && (half == 0 || kP == 2)) arrived(kP + u);
+            if (more && then == 0) keys_arrived(ahead);
+            ok = wait_soon(pready(j, half, block), turn(block), abort_flag) && ok;
+            const int s = place(kP + u), at = place_of(j);
             tc_fence_after();
             if (leader && ok) {
               const int row = half * (kKeys / 2) - u * L::kVKeys;  // its first key in the unit
               const uint32_t b = v_lo + s * (kUnitBytes >> 4) + (row * 128 >> 4);
 #pragma unroll
               for (int ks = 0; ks < kKeys / 32; ++ks)
-                mma_ts(tmem_o(j), tmem_s(j) + half * (kKeys / 4) + ks * 8,
+                mma_ts(tmem_o(j), tmem_s(at) + half * (kKeys / 4) + ks * 8,
                        make_desc(b + ks * (2048 >> 4)), idesc_o,
                        (k > begin || half + ks > 0) ? 1u : 0u);
               if (j + 1 == QT && (kP == 2 || half == 1)) mma_commit(empty(s));
               if (half == 0) mma_commit(ohalf(j));
+              if (half == 1 && kLook == 3) mma_commit(oblock(j));
               if (half == 1 && k + 1 == end) mma_commit(ofull(j));
             }
-            if (more) scores(j, 2 * kP);
+            if (more) scores(then, ahead, at);
           };
 #pragma unroll
           for (int i = 0; i < 2 * QT; ++i) values(i / 2, i % 2);
           if (leader && ok && k + 2 == end) mma_commit(qempty);
-          parity ^= 1;
+          ++block;
+          if (kLook == 3) first = first == 0 ? 2 : first - 1;  // two steps on
           slot += 2 * kP;
           if (slot >= S) slot -= S, phase ^= 1;
           ok = __all_sync(kFull, ok);
@@ -836,13 +859,14 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
     const int j = QT == 1 ? 0 : (warp - 4) >> 2;  // the query tile
     const int sub = warp & 3;           // the TMEM lanes this warp may touch
     const int row = 32 * sub + lane;    // of the query tile
-    const uint32_t t_s = tmem_s(j) + (static_cast<uint32_t>(32 * sub) << 16);
-    const uint32_t t_o = tmem_o(j) + (static_cast<uint32_t>(32 * sub) << 16);
+    const uint32_t lanes = static_cast<uint32_t>(32 * sub) << 16;
+    const uint32_t t_o = tmem_o(j) + lanes;
     // what the exponents are taken against, in powers of two
     auto reference = [&](float m) { return (m == -INFINITY ? 0.0f : m * p.c) - (BF16 ? 0.0f : 7.0f); };
     const int tok = j * p.q_tokens + row / p.G;   // of the item
     int slot = kP;                      // ring place of the block's first V unit
-    uint32_t phase = 0, parity = 0;     // its parity; the blocks' parity
+    uint32_t phase = 0;                 // its parity
+    int block = 0, at_s = j;            // blocks done; place of S
     bool ok = true;
     for (int seg = 0; ok; ++seg) {
       ok = __all_sync(kFull, wait_soon(segment_ready(seg), (seg / kSegments) & 1, abort_flag));
@@ -863,7 +887,7 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
       const int seen_hi = g.hi, seen_lo = g.lo;  // by some row of the item
       for (int k = begin; k < end; ++k) {
         const int key0 = (k < sink_blocks ? k : k + skip) * kKeys;
-        ok = __all_sync(kFull, wait_soon(sfull(j), parity, abort_flag));
+        ok = __all_sync(kFull, wait_soon(sfull(j, block), turn(block), abort_flag));
         if (!ok) break;
         tc_fence_after();
         // V rows of a loaded page that no row of the item sees (behind the
@@ -893,6 +917,7 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
         // kSumLimit says that it no longer does, and a row that has none yet
         // takes one; only then (every segment's first half, few others) is
         // the maximum formed, O and l rescaled and P computed again.
+        const uint32_t t_s = tmem_s(at_s) + lanes;
         const bool edge = !(key0 + kKeys <= hi_all && (key0 >= lo_all || key0 + kKeys <= p.sinks));
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
@@ -942,9 +967,11 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
                                             : fmaxf(mx[q], s[i + q]);
               const float m_new = max3f(m, fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
               if (k > begin || half == 1) {  // O exists
-                // and has to be complete up to the half before; sfull followed
-                // the products of the block before
-                if (half == 1) ok = __all_sync(kFull, wait_soon(ohalf(j), parity, abort_flag));
+                // and has to be complete up to the half before; with one place
+                // for S sfull followed the products of the block before
+                if (half == 1 || kLook == 3)
+                  ok = __all_sync(kFull, wait_soon(half == 1 ? ohalf(j) : oblock(j),
+                                                   (block + 1 - half) & 1, abort_flag));
                 tc_fence_after();
                 // a first maximum meets O and l that are still 0
                 const float f = renew && m != -INFINITY ? exp2_approx((m - m_new) * p.c) : 1.0f;
@@ -968,9 +995,10 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(pready(j, half));
+          if (lane == 0) mbar_arrive(pready(j, half, block));
         }
-        parity ^= 1;
+        ++block;
+        if (kLook == 3) at_s = at_s == 0 ? 2 : at_s - 1;
         slot += 2 * kP;
         if (slot >= S) slot -= S, phase ^= 1;
       }
