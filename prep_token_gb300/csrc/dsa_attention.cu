@@ -951,42 +951,48 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
               }
               sum = (add[0].x + add[0].y) + (add[1].x + add[1].y);
             };
+            // a segment's first half takes its maximum at once
+            bool renew = mine, again = k == begin && half == 0;
 #pragma unroll 1
-            for (int pass = 0;; ++pass) {  // once, or again with another reference
-              exponentials(reference(m));
-              const bool renew = mine && (m == -INFINITY || !(sum <= kSumLimit<BF16>));
-              if (pass == 1 || !__any_sync(kFull, renew)) break;
-              float mx[4];
+            for (;;) {
+              if (again) {
+                float mx[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) mx[i] = s[i];
+                for (int i = 0; i < 4; ++i) mx[i] = s[i];
 #pragma unroll
-              for (int i = 4; i < kKeys / 2; i += 8)
+                for (int i = 4; i < kKeys / 2; i += 8)
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  mx[q] = i + 4 < kKeys / 2 ? max3f(mx[q], s[i + q], s[i + 4 + q])
-                                            : fmaxf(mx[q], s[i + q]);
-              const float m_new = max3f(m, fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-              if (k > begin || half == 1) {  // O exists
-                // and has to be complete up to the half before; with one place
-                // for S sfull followed the products of the block before
-                if (half == 1 || kLook == 3)
-                  ok = __all_sync(kFull, wait_soon(half == 1 ? ohalf(j) : oblock(j),
-                                                   (block + 1 - half) & 1, abort_flag));
-                tc_fence_after();
-                // a first maximum meets O and l that are still 0
-                const float f = renew && m != -INFINITY ? exp2_approx((m - m_new) * p.c) : 1.0f;
-                l *= f;
+                  for (int q = 0; q < 4; ++q)
+                    mx[q] = i + 4 < kKeys / 2 ? max3f(mx[q], s[i + q], s[i + 4 + q])
+                                              : fmaxf(mx[q], s[i + q]);
+                const float m_new = max3f(m, fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (k > begin || half == 1) {  // O exists
+                  // and has to be complete up to the half before; with one place
+                  // for S sfull followed the products of the block before
+                  if (half == 1 || kLook == 3)
+                    ok = __all_sync(kFull, wait_soon(half == 1 ? ohalf(j) : oblock(j),
+                                                     (block + 1 - half) & 1, abort_flag));
+                  tc_fence_after();
+                  // a first maximum meets O and l that are still 0
+                  const float f = renew && m != -INFINITY ? exp2_approx((m - m_new) * p.c) : 1.0f;
+                  l *= f;
 #pragma unroll 1
-                for (int i = 0; i < D / 16; ++i) {
-                  float o[16];
-                  tmem_ld16(t_o + 16 * i, o);
-                  tmem_wait_ld(o);
+                  for (int i = 0; i < D / 16; ++i) {
+                    float o[16];
+                    tmem_ld16(t_o + 16 * i, o);
+                    tmem_wait_ld(o);
 #pragma unroll
-                  for (int q = 0; q < 16; ++q) o[q] *= f;
-                  tmem_st16(t_o + 16 * i, reinterpret_cast<uint32_t*>(o));
+                    for (int q = 0; q < 16; ++q) o[q] *= f;
+                    tmem_st16(t_o + 16 * i, reinterpret_cast<uint32_t*>(o));
+                  }
                 }
+                m = renew ? m_new : m;
               }
-              m = renew ? m_new : m;
+              exponentials(reference(m));
+              if (again) break;
+              renew = mine && (m == -INFINITY || !(sum <= kSumLimit<BF16>));
+              if (!__any_sync(kFull, renew)) break;
+              again = true;
             }
             l += sum;
             tmem_st16(t_s + 32 * half, w);  // over S of the keys read before
@@ -1018,6 +1024,14 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
                                      2 * (token * p.out_stride_t + h * p.out_stride_h)
                                : reinterpret_cast<char*>(p.part + at * D);
         const unsigned rows = __ballot_sync(kFull, mine);
+        char* row_to[4];  // QT 2: where this lane writes a quarter of 64 bytes
+        if (QT == 2) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            row_to[q] = reinterpret_cast<char*>(__shfl_sync(
+                            kFull, reinterpret_cast<unsigned long long>(to), 8 * q + (lane >> 2))) +
+                        16 * (lane & 3);
+        }
         // 64 bytes of every row of the warp: v holds this lane's.  A lane's
         // own row would go out 16 bytes at a time to 32 places; turned through
         // shared memory (pieces swizzled against bank conflicts) four lanes
@@ -1035,11 +1049,9 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
           __syncwarp();
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int r = 8 * q + (lane >> 2), piece = lane & 3;
-            char* row_to = reinterpret_cast<char*>(
-                __shfl_sync(kFull, reinterpret_cast<unsigned long long>(to), r));
-            const uint4 u = turn[r * 4 + (piece ^ (r >> 1 & 3))];
-            if (rows >> r & 1) *reinterpret_cast<uint4*>(row_to + offset + 16 * piece) = u;
+            const int r = 8 * q + (lane >> 2);
+            const uint4 u = turn[r * 4 + ((lane & 3) ^ (r >> 1 & 3))];
+            if (rows >> r & 1) *reinterpret_cast<uint4*>(row_to[q] + offset) = u;
           }
           __syncwarp();
         };
