@@ -375,8 +375,8 @@ dsa_status dsa_indexer_mqa_logits(
  * A visible key whose block-table entry is outside [0, num_pages) sets
  * DSA_DEVERR_SLOT and makes the rows that see it NaN.  Cache contents that no
  * query sees (behind a context, before a window) may be anything, NaN
- * included; a non-finite value or key that some query sees makes out
- * unspecified for the queries of its sequence.
+ * included.  A key or value that is not finite changes only the rows that see
+ * it, whose out (some or all elements) and lse are then not finite.
  */
 size_t dsa_paged_attention_workspace_bytes(int32_t T, int32_t B, int32_t H,
                                            int32_t Hkv, int32_t head_dim,

@@ -251,6 +251,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
+// c + 0 * v for two values of the 16-bit type: NaN where v is not finite.
+template <bool BF16>
+__device__ __forceinline__ uint32_t fma0(uint32_t v, uint32_t c) {
+  uint32_t r;
+  if (BF16)
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0), "r"(c));
+  else
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0), "r"(c));
+  return r;
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -500,10 +511,11 @@ struct ASmem {
   static constexpr int kOffRing = kQBytes;
   static constexpr int kOffTurn = kOffRing + kStages * kUnitBytes;
   static constexpr int kOffSeg = kOffTurn + kTurnBytes;
-  static constexpr int kOffBar = kOffSeg + kSegments * static_cast<int>(sizeof(Segment));
+  static constexpr int kOffOdd = kOffSeg + kSegments * static_cast<int>(sizeof(Segment));
+  static constexpr int kOffBar = kOffOdd + 4 * 4 * 4;
   // barriers: full[S], empty[S], qfull, qempty, drain, segment[4], then per
-  // query tile sfull[2], pready[2][2], ohalf, oblock, ofull
-  static constexpr int kBars = 2 * kStages + 3 + kSegments + 9 * QT;
+  // query tile sfull[2], pready[2][2], ohalf, oblock, ofull; checked[4]
+  static constexpr int kBars = 2 * kStages + 3 + kSegments + 9 * QT + 4;
   static constexpr int kOffTmem = kOffBar + 8 * kBars;
   static constexpr int kOffAbort = kOffTmem + 4;
   static constexpr int kBytes = kOffAbort + 4;
@@ -553,6 +565,10 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
   auto ohalf = [&](int j) { return bar0 + 8 * (kB + 6 + 9 * j); };
   auto oblock = [&](int j) { return bar0 + 8 * (kB + 7 + 9 * j); };
   auto ofull = [&](int j) { return bar0 + 8 * (kB + 8 + 9 * j); };
+  // V of the n-th block at an edge has been looked at; its keys that are odd.
+  // The tiles are never four such blocks apart.
+  auto checked = [&](int n) { return bar0 + 8 * (kB + 9 * QT + (n & 3)); };
+  volatile uint32_t* const odd_keys = reinterpret_cast<volatile uint32_t*>(smem + L::kOffOdd);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffAbort);
   Segment* const segments = reinterpret_cast<Segment*>(smem + L::kOffSeg);
   const int warp = threadIdx.x >> 5;
@@ -572,6 +588,7 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
     mbar_init(qempty, 1);
     mbar_init(drain, 1);
     for (int i = 0; i < kSegments; ++i) mbar_init(segment_ready(i), 1);
+    for (int i = 0; i < 4; ++i) mbar_init(checked(i), 4);  // tile 0's warps
     for (int j = 0; j < QT; ++j) {
       for (int n = 0; n < kTurns; ++n) {
         mbar_init(sfull(j, n), 1);
@@ -867,6 +884,7 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
     int slot = kP;                      // ring place of the block's first V unit
     uint32_t phase = 0;                 // its parity
     int block = 0, at_s = j;            // blocks done; place of S
+    int edges = 0;                      // blocks that not every row saw whole
     bool ok = true;
     for (int seg = 0; ok; ++seg) {
       ok = __all_sync(kFull, wait_soon(segment_ready(seg), (seg / kSegments) & 1, abort_flag));
@@ -885,38 +903,71 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
       const int begin = g.begin, end = g.end;
       const int sink_blocks = g.sink_blocks, skip = g.main_block - sink_blocks;
       const int seen_hi = g.hi, seen_lo = g.lo;  // by some row of the item
+      const int every_hi = g.pos0 + 1;           // by every row
+      const int every_lo = p.window ? g.pos0 + g.tokens - p.window : 0;
       for (int k = begin; k < end; ++k) {
         const int key0 = (k < sink_blocks ? k : k + skip) * kKeys;
+        // Where some row of the item does not see some key of the block, 0 *
+        // its V must be 0 whatever V holds.  Tile 0's thread r looks at key
+        // r's row: it zeroes what no row sees (behind the context, before the
+        // window) and what is not finite.  In the latter case the rows that do
+        // see the key become NaN.  Tile 0's P V comes first, and waits.  All of it
+        // before S is waited for: V comes sooner.
+        if (!(key0 + kKeys <= every_hi && (key0 >= every_lo || key0 + kKeys <= p.sinks))) {
+          if (j == 0) {
+            const int key = key0 + row;
+            bool odd = false;
+            if (!(key < every_hi && (key >= every_lo || key < p.sinks))) {
+              int s = slot + row / L::kVKeys;
+              uint32_t ph = phase;
+              if (s >= S) s -= S, ph ^= 1;
+              ok = wait_soon(full(s), ph, abort_flag);
+              const uint32_t at = sbase + L::kOffRing + s * kUnitBytes + (row % L::kVKeys) * 128;
+              auto piece = [&](int i) {  // 16 bytes; lanes apart, for the banks
+                return at + (i >> 3) * (L::kVKeys * 128) + 16 * ((i + lane) & 7);
+              };
+              const bool some = key < seen_hi && (key >= seen_lo || key < p.sinks);
+              if (some) {
+                uint32_t zero = 0;  // += 0 * V: stays 0 if all of V is finite
+#pragma unroll 4
+                for (int i = 0; i < 8 * kP; ++i) {
+                  uint32_t v[4];
+                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                               : "r"(piece(i)) : "memory");
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) zero = fma0<BF16>(v[q], zero);
+                }
+                odd = (zero & 0x7fff7fffu) != 0;
+              }
+              if (!some || odd) {
+#pragma unroll 1
+                for (int i = 0; i < 8 * kP; ++i)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};"
+                               ::"r"(piece(i)), "r"(0) : "memory");
+                fence_async_shared();
+              }
+            }
+            const unsigned mask = __ballot_sync(kFull, odd);
+            if (lane == 0) {
+              odd_keys[4 * (edges & 3) + sub] = mask;
+              mbar_arrive(checked(edges));
+            }
+          }
+          ok = __all_sync(kFull, ok && wait_soon(checked(edges), (edges >> 2) & 1, abort_flag));
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = key0 + 32 * i;
+            const uint32_t mask = odd_keys[4 * (edges & 3) + i];
+            if (mask & below(hi - at) & (~below(lo - at) | below(p.sinks - at)))
+              l = __int_as_float(0x7fc00000);
+          }
+          ++edges;
+        }
         ok = __all_sync(kFull, wait_soon(sfull(j, block), turn(block), abort_flag));
         if (!ok) break;
         tc_fence_after();
-        // V rows of a loaded page that no row of the item sees (behind the
-        // context, before the window): whatever they hold, 0 * it must be 0.
-        // Tile 0's P V comes first, and waits for this.
-        if (j == 0 && !(key0 + kKeys <= seen_hi && (key0 >= seen_lo || key0 + kKeys <= p.sinks))) {
-          const int key = key0 + row;
-          if (!(key < seen_hi && (key >= seen_lo || key < p.sinks))) {
-            int s = slot + row / L::kVKeys;
-            uint32_t ph = phase;
-            if (s >= S) s -= S, ph ^= 1;
-            ok = wait_soon(full(s), ph, abort_flag);
-            const uint32_t at = sbase + L::kOffRing + s * kUnitBytes + (row % L::kVKeys) * 128;
-#pragma unroll
-            for (int pn = 0; pn < kP; ++pn)
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};"
-                             ::"r"(at + pn * L::kVKeys * 128 + 16 * i), "r"(0) : "memory");
-            fence_async_shared();
-          }
-          ok = __all_sync(kFull, ok);
-          if (!ok) break;
-        }
-        // Each half of the block's keys by itself, P against the reference that
-        // the row has: no maximum is taken while that serves.  A sum above
-        // kSumLimit says that it no longer does, and a row that has none yet
-        // takes one; only then (every segment's first half, few others) is
-        // the maximum formed, O and l rescaled and P computed again.
         const uint32_t t_s = tmem_s(at_s) + lanes;
         const bool edge = !(key0 + kKeys <= hi_all && (key0 >= lo_all || key0 + kKeys <= p.sinks));
 #pragma unroll 1

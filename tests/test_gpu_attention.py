@@ -282,3 +282,34 @@ def test_binding_refusals():
                 1, 3), ctx=300), "SHAPE")]:
         with pytest.raises(dp.DsaError, match=what):
             call(**over)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("dim,window", [(128, 0), (64, 0), (128, 100), (64, 100)])
+def test_values_that_are_not_finite_touch_only_the_rows_that_see_them(dim, window, dtype):
+    """A NaN key, and values that are NaN or infinite, among the new tokens:
+    the rows before them (and those whose window has passed them) are as if
+    they were not there, the rows that see them are not finite."""
+    new, ctx = [300, 1, 40], [420, 300, 700]
+    b = Batch(new, ctx, 8, 2, dim, page=32, dtype=dtype, seed=22, window=window,
+              sinks=3 if window else 0)
+    clean = Batch(new, ctx, 8, 2, dim, page=32, dtype=dtype, seed=22, window=window,
+                  sinks=3 if window else 0)
+    odd = {200: ("v", float("nan")), 260: ("v", float("inf")), 261: ("v", -float("inf")),
+           333: ("k", float("nan")), 419: ("v", float("nan"))}
+    for key, (what, x) in odd.items():  # of sequence 0, which has positions 120 .. 419
+        page = int(b.table[0, key // 32])
+        (b.v if what == "v" else b.k)[page, key % 32, 1, 5] = x
+    out, lse = b.run()
+    want, z, tol, tol_l = clean.reference()
+    heads = torch.arange(8, device="cuda") >= 4  # those of kv head 1
+    pos = torch.arange(120, 420, device="cuda")
+    hit = torch.zeros(341, dtype=torch.bool, device="cuda")
+    for key in odd:
+        hit[:300] |= (pos >= key) & (pos < key + window if window else pos >= key)
+    hit = hit[:, None] & heads
+    assert not torch.isfinite(out).all(-1)[hit].any()
+    ok = ~hit
+    assert torch.isfinite(out).all(-1)[ok].all() and torch.isfinite(lse)[ok].all()
+    assert ((out.double() - want).abs() <= tol)[ok].all()
+    assert ((lse.double() - z).abs() <= tol_l)[ok].all()
