@@ -1049,6 +1049,31 @@ def run_probe(which, local_rank):
         torch.cuda.synchronize(dev)
         print(f"probe k_only: 6 calls (T={inp.T}, four input sets)")
         return
+    if which.startswith("attention"):
+        # a chunk of 512 tokens behind a prefix; 16 single tokens, 537 MB of keys and values
+        new, B = (512, 1) if which == "attention" else (1, 16)
+        ctx, H, kv, D, page = 8192, 64, 8, 128, 64
+        gen = torch.Generator(device=dev).manual_seed(0)
+        k, v = (torch.randn((B * ctx // page, page, kv, D), generator=gen, device=dev,
+                            dtype=torch.bfloat16) for _ in range(2))
+        q = torch.randn((B * new, H, D), generator=gen, device=dev, dtype=torch.bfloat16)
+        table = torch.randperm(B * ctx // page, generator=gen, device=dev)
+        table = table.to(torch.int32).view(B, ctx // page)
+        start = torch.arange(0, B * new + 1, new, dtype=torch.int32, device=dev)
+        lens = torch.full((B,), ctx, dtype=torch.int32, device=dev)
+        for _ in range(6):
+            dp.dsa_paged_attention(q, k, v, table, start, lens, ctx)
+        torch.cuda.synchronize(dev)
+        print(f"probe {which}: 6 calls (B={B}, new={new}, context={ctx}, H={H}, Hkv={kv})")
+        return
+    if which == "copy_pages":  # 256 K/V pages of 128 KB in four caches, to other pages
+        caches = [torch.zeros((600, 131072), dtype=torch.uint8, device=dev) for _ in range(4)]
+        pages = torch.randperm(600, device=dev).to(torch.int32)
+        for _ in range(6):
+            dp.dsa_cache_copy_pages(caches, 600, pages[:256], pages[256:512])
+        torch.cuda.synchronize(dev)
+        print("probe copy_pages: 6 calls (256 pages of 128 KB, 4 caches)")
+        return
     inp, had = probe_workload(which)
     d = _dev_inputs(inp, dev)
     stream = torch.cuda.current_stream()
@@ -1073,7 +1098,8 @@ def main():
     ap.add_argument("--cpu-seconds", type=float, default=10.0)
     ap.add_argument("--probe", choices=("prefill", "decode", "logits", "prefill_hadamard",
                                         "decode_hadamard", "k_only", "prefill_h32",
-                                        "prefill_h16"),
+                                        "prefill_h16", "attention", "attention_decode",
+                                        "copy_pages"),
                     help="make 6 eager calls on that workload and exit (for profilers)")
     ap.add_argument("--traffic-from", nargs=2, metavar=("CSV", "WHICH"),
                     help="write the traffic summary of WHICH (prefill | decode | k_only) "

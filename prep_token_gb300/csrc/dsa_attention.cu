@@ -1151,11 +1151,14 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
                  ::"r"(tmem), "n"(Shape<QT>::kTmemCols) : "memory");
 }
 
-// Joins the parts of the item that starts in CTA blockIdx.x of the first
-// kernel: with M the largest m, out = sum 2^(m - M) O / sum 2^(m - M) l.  The
-// eight warps take a row each where the parts are few, else all one row, an
-// eighth of its parts each; every sum is in the order of the parts or warps.
-constexpr int kJoinWarps = 8, kJoinGroups = 8;
+// Joins the parts of the items that a cut divides: with M the largest m of a
+// row's parts, out = sum 2^(m - M) O / sum 2^(m - M) l.  Which items those are
+// stands in meta; every CTA counts their rows and the rows are dealt out
+// evenly, one to a warp at a time, or where they are fewer than the CTAs and
+// have many parts one to a CTA, whose warps take an eighth of the parts each.  Bound: the waits
+// for meta, (m, l) and O, one behind the other.  Every sum has a fixed order.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinCtas = 8 * kSms;
 
 template <int N>
 struct Vec;
@@ -1169,52 +1172,91 @@ struct Vec<4> {
 };
 
 template <int D, bool BF16, int QT>
-__global__ void __launch_bounds__(32 * kJoinWarps) dsa_attention_join_kernel(const __grid_constant__ AParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    dsa_attention_join_kernel(const __grid_constant__ AParams p) {
+  constexpr int kMost = Shape<QT>::kCtas;  // entries of meta, two to a thread
+  static_assert(kMost <= 64 * kJoinWarps && kMost % 2 == 0, "entries");
+  __shared__ int4 metas[kMost];
+  __shared__ int before[kMost];  // rows of the items before
+  __shared__ int warp_rows[kJoinWarps];
   __shared__ float sums[kJoinWarps][D + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int4 meta = p.meta[blockIdx.x];
-  if (meta.x < 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int first = blockIdx.x, parts = meta.x - first + 1;
-  const bool few = parts <= kJoinWarps;
-  const int step = few ? 1 : kJoinWarps, from = few ? 0 : warp;
-  auto slot = [&](int i) { return i == 0 ? 2LL * first + 1 : 2LL * (first + i); };
-  using V = typename Vec<D / 32>::type;
-  for (int r0 = blockIdx.y * (few ? kJoinWarps : 1); r0 < meta.w * p.G;
-       r0 += kJoinGroups * (few ? kJoinWarps : 1)) {
-    const int row = r0 + (few ? warp : 0);
-    if (few && row >= meta.w * p.G) return;
+  int rows[2] = {0, 0}, most = 0;
+  const int e = 2 * threadIdx.x;
+  if (e < kMost) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      metas[e + i] = p.meta[e + i];
+      rows[i] = metas[e + i].x < 0 ? 0 : metas[e + i].w * p.G;
+      most = max(most, metas[e + i].x - (e + i) + 1);  // parts
+    }
+  }
+  int upto = rows[0] + rows[1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) warp_rows[warp] = upto;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    if (w < warp) upto += warp_rows[w];
+    total += warp_rows[w];
+  }
+  if (e < kMost) {
+    before[e] = upto - rows[0] - rows[1];
+    before[e + 1] = upto - rows[1];
+  }
+  const bool long_rows = __syncthreads_or(most > kJoinWarps);
+
+  constexpr int kV = D / 32;  // values of a row per lane
+  using V = typename Vec<kV>::type;
+  const bool alone = !long_rows || total > static_cast<int>(gridDim.x);  // a row to a warp
+  const int step = gridDim.x * (alone ? kJoinWarps : 1);
+  for (int n = alone ? blockIdx.x * kJoinWarps + warp : blockIdx.x; n < total; n += step) {
+    int first = 0;  // the last entry with before <= n: the CTA in which the item starts
+#pragma unroll
+    for (int o = 256; o; o >>= 1)
+      if (first + o < kMost && before[first + o] <= n) first += o;
+    const int4 meta = metas[first];
+    const int row = n - before[first], parts = meta.x - first + 1;
+    auto at = [&](int i) {  // the row's part i in ml and part
+      return (i == 0 ? 2LL * first + 1 : 2LL * (first + i)) * (QT * kRows) + row;
+    };
     float top = -INFINITY;
-    for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.ml[slot(i) * (QT * kRows) + row].x);
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.ml[at(i)].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
     const float ref = top == -INFINITY ? 0.0f : top;
-    float acc[D / 32] = {};
+    float acc[kV] = {};
     float l = 0.0f;
 #pragma unroll 8
-    for (int i = from; i < parts; i += step) {
-      const float2 ml = p.ml[slot(i) * (QT * kRows) + row];
-      const V o = *reinterpret_cast<const V*>(p.part + (slot(i) * (QT * kRows) + row) * D + lane * (D / 32));
+    for (int i = alone ? 0 : warp; i < parts; i += alone ? 1 : kJoinWarps) {
+      const float2 ml = p.ml[at(i)];
+      const V o = *reinterpret_cast<const V*>(p.part + at(i) * D + lane * kV);
       const float f = exp2_approx(ml.x - ref);
       l = fmaf(f, ml.y, l);
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) acc[j] = fmaf(f, reinterpret_cast<const float*>(&o)[j], acc[j]);
+      for (int j = 0; j < kV; ++j) acc[j] = fmaf(f, reinterpret_cast<const float*>(&o)[j], acc[j]);
     }
-    if (!few) {
+    if (!alone) {
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) sums[warp][lane * (D / 32) + j] = acc[j];
+      for (int j = 0; j < kV; ++j) sums[warp][lane * kV + j] = acc[j];
       if (lane == 0) sums[warp][D] = l;
       __syncthreads();
       if (warp != 0) continue;
       l = 0.0f;
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) acc[j] = 0.0f;
+      for (int j = 0; j < kV; ++j) acc[j] = 0.0f;
       for (int w = 0; w < kJoinWarps; ++w) {
         l += sums[w][D];
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) acc[j] += sums[w][lane * (D / 32) + j];
+        for (int j = 0; j < kV; ++j) acc[j] += sums[w][lane * kV + j];
       }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -1222,9 +1264,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) dsa_attention_join_kernel(con
     const int h = meta.z * p.G + row % p.G;
     uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
                                                 token * p.out_stride_t + h * p.out_stride_h) +
-                    lane * (D / 64);
+                    lane * (kV / 2);
 #pragma unroll
-    for (int j = 0; j < D / 32; j += 2)
+    for (int j = 0; j < kV; j += 2)
       out[j / 2] = l == 0.0f ? 0u : pack2<BF16>(acc[j] * inv, acc[j + 1] * inv);
     if (lane == 0 && p.lse)
       p.lse[token * (p.Hkv * p.G) + h] = l == 0.0f ? -INFINITY : ref * kLn2 + logf(l);
@@ -1287,9 +1329,14 @@ cudaError_t prepare_device() {
   return e;
 }
 
-// Query tiles of a CTA.  Two where sequences fill them: keys are then loaded
-// once for 256 rows.
-int query_tiles(int T, int B, int q_tokens) { return T / q_tokens >= 2LL * B ? 2 : 1; }
+// Query tiles of a CTA.  Two where the sequences have half a tile of new tokens
+// or more on average: keys are then loaded once for up to 256 rows.  Measured
+// with one and two, 64 heads of 128 on 8 kv heads, context 4000, 16 sequences
+// of 8, 12, 24 new tokens (16 fill a tile): 62.5 and 60.1, 67 and 63, 106 and
+// 74 us; 64 single tokens over 8192: 325 and 339 us.
+int query_tiles(int T, int B, int q_tokens) {
+  return 2LL * T >= static_cast<long long>(q_tokens) * B ? 2 : 1;
+}
 
 long long max_items(int T, int B, int Hkv, int tile_tokens) {
   return (static_cast<long long>(T) / tile_tokens + B) * Hkv;
@@ -1335,7 +1382,7 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   cfg.numAttrs = pdl ? 1 : 0;
   cudaError_t e = cudaLaunchKernelEx(&cfg, dsa_paged_attention_kernel<D, BF16, QT>, tq, tk, tv, p);
   if (e != cudaSuccess || !p.split) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), kJoinGroups);
+  cfg.gridDim = dim3(kJoinCtas);
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
