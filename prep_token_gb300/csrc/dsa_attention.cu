@@ -11,11 +11,13 @@
 // and sum l of a softmax, so S never leaves the chip:
 //   p_j = 2^(c s_j - c m) with c = scale * log2(e);  O += P V;  l += sum p.
 //
-// A work item is 128 rows (floor(128 / G) tokens, their G heads of one kv
-// head packed token by token) of one sequence; a single token fills G of them.
-//   * warp 0 loads: the query tile, then per key block the 16 KB units of K
-//     (128 keys x 64 dims) and V (128 * 64 / D keys x D dims) into one ring,
-//     by 4-D TMA boxes of min(page, 64) keys with the 128-byte swizzle; lane l
+// A query tile is 128 rows: floor(128 / G) tokens, their G heads of one kv head
+// packed token by token; a single token fills G of them.  A work item is one or
+// two query tiles of one sequence, which share the loaded keys (query_tiles says
+// when two).
+//   * warps 0 and 2 load: the query tiles, then per key block the 16 KB units of
+//     K (128 keys x 64 dims) and V (8192 / D keys x D dims) into one ring, by
+//     4-D TMA boxes of min(page, 64) keys with the 128-byte swizzle; lane l
 //     looks up and issues box l of the block.
 //   * warp 1 (one lane) issues S = Q K^T (M = N = 128, both operands in shared
 //     memory) and O += P V (A = P in TMEM over the columns of S, B = V in
@@ -28,13 +30,26 @@
 //     the values' type for the matrix product (at most 2^-8 of it in bf16,
 //     2^-11 in fp16); the sum l takes it unrounded.  In fp16 P, O and l carry a
 //     factor of 2^7: a p down to 2^-21 of the largest keeps all its bits.
-// Two CTAs share an SM, so one's softmax runs beside the other's products.
+// An SM holds two query tiles, in one CTA or two: one's softmax runs beside the
+// other's products.
 //
-// Bound: a chunk by the tensor cores (4 D flops per row and visible key),
-// single tokens by the cache's bytes.  The key blocks of all items are laid end
-// to end and cut into equal shares, one per CTA; an item that a cut divides
-// leaves partial (O, m, l) in the workspace, which a second kernel joins in a
-// fixed order.  (use_split says when CTAs take whole items instead.)
+// Bound, and what was measured (152 SMs, 6.78 TB/s, 1892 TFLOP/s of bf16):
+//   * a chunk by the tensor cores, 4 D flops per row and visible key.  A
+//     128 x 128 x 16 product with both operands in shared memory takes 105
+//     cycles (64 at the nominal rate), with A in TMEM 75: a block of a tile 1445
+//     for D = 128, where the nominal rate has 1024.  2048 tokens over 16384, 64
+//     heads: 665 us, 1550 TFLOP/s.  For D = 64 the softmax is as long as the
+//     products, and the hand-overs between them count: 520 us.
+//   * single tokens by the cache's bytes: 64 over 8192, 8 kv heads: 325 us, 6.6
+//     TB/s.  About 12 us of a call are its start, its first loads and the second
+//     kernel: 1 token over 1000 takes 13 us, 2 over 65536 55 us (40 at 6.78 TB/s).
+//   * short items (a window) by what each begins and ends with, about 5 us of
+//     code that the instruction cache does not keep: so code is small before it
+//     is unrolled here.
+// The key blocks of all items are laid end to end and cut into equal shares, one
+// per CTA; an item that a cut divides leaves partial (O, m, l) in the workspace,
+// which a second kernel joins in a fixed order.  (use_split says when CTAs take
+// whole items instead.)
 //
 // Every wait is bounded in time; TMEM is always released before exit.
 #include <cuda.h>
@@ -73,7 +88,7 @@ struct Shape {
 // A half block's sum of P above which a row's reference is renewed.  P in
 // bf16 has fp32's range; in fp16 no p may pass 65504.
 template <bool BF16>
-constexpr float kSumLimit = BF16 ? 0x1p40f : 0x1p15f;
+constexpr float kSumLimit = BF16 ? 0x1p20f : 0x1p15f;
 constexpr float kLn2 = 0.693147180559945309f;
 
 struct AParams {
@@ -1342,15 +1357,31 @@ long long max_items(int T, int B, int Hkv, int tile_tokens) {
   return (static_cast<long long>(T) / tile_tokens + B) * Hkv;
 }
 
-// The key blocks are cut into equal shares unless items of one sequence share
-// keys that L2 cannot hold: a share's place in the keys differs from CTA to
-// CTA, so all keys of the call are in use at once, while whole items taken in
-// order keep the CTAs on one kv head.  That needs items enough for a balance.
-bool use_split(int T, int B, int Hkv, int D, int q_tokens, int max_context) {
-  const int tiles = query_tiles(T, B, q_tokens);
+// Whether the key blocks are cut into equal shares, or CTAs take whole items.
+// Cutting balances any lengths, but costs about 15 us: the second kernel, and
+// one more item begun per CTA.  So whole items are taken, given two query tiles
+// (one: single tokens, whose lengths differ) and two rounds of them, where
+//   * the last round leaves few block times (1.6 us) idle: a prompt of 8192
+//     with a window of 1024, 32 heads, 7 rounds of 11 blocks, takes 162 us
+//     whole and 187 cut; without the window, 64 blocks, 472 and 460;
+//   * or items of one sequence share keys that L2 cannot hold: a cut's place in
+//     the keys differs from CTA to CTA, so all keys are in use at once, while
+//     items in order keep the CTAs on one kv head: 4096 tokens over 65536 with
+//     8 kv heads (268 MB) take 5.35 ms whole and 5.59 cut, over 32768 2.61 and
+//     2.57.
+bool use_split(int T, int B, int Hkv, int D, int q_tokens, int max_context, int window, int sinks) {
+  if (max_context <= kKeys) return false;
+  const int tile_tokens = 2 * q_tokens;
+  if (query_tiles(T, B, q_tokens) != 2) return true;
+  // about: how the sequences' ends fall is not known here
+  const long long items = (static_cast<long long>(T) / tile_tokens + (B + 1) / 2) * Hkv;
+  const long long rounds = (items + kSms - 1) / kSms;
+  long long keys = max_context;
+  if (window && static_cast<long long>(window) + sinks + tile_tokens < keys)
+    keys = static_cast<long long>(window) + sinks + tile_tokens;
+  const long long idle = (rounds * kSms - items) * ((keys + kKeys - 1) / kKeys);
   const double bytes = 4.0 * D * Hkv * max_context * B;
-  return max_context > kKeys &&
-         !(tiles == 2 && bytes > 9.6e7 && max_items(T, B, Hkv, tiles * q_tokens) >= 4 * kSms);
+  return !(rounds >= 2 && idle <= 8LL * kSms) && !(rounds >= 4 && bytes > 2e8);
 }
 
 bool encode_map(CUtensorMap* map, bool bf16, const void* base, int rank, const cuuint64_t* dims,
@@ -1408,7 +1439,7 @@ extern "C" {
 size_t dsa_paged_attention_workspace_bytes(int32_t T, int32_t B, int32_t H, int32_t Hkv,
                                            int32_t head_dim, int32_t max_context) {
   if (T < 1 || B < 1 || Hkv < 1 || H < Hkv || H % Hkv || H / Hkv > kRows || head_dim < 1) return 0;
-  if (!use_split(T, B, Hkv, head_dim, kRows / (H / Hkv), max_context)) return 0;
+  if (!use_split(T, B, Hkv, head_dim, kRows / (H / Hkv), max_context, 0, 0)) return 0;
   return kMetaBytes + kMlBytes + kPartRows * static_cast<size_t>(head_dim) * sizeof(float);
 }
 
@@ -1522,7 +1553,8 @@ dsa_status dsa_paged_attention(
   p.window = window < max_context ? window : 0;  // such a window hides nothing
   p.sinks = p.window ? (sinks < max_context ? sinks : max_context) : 0;
   p.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
-  p.split = need ? 1 : 0;
+  // a window makes whole items likelier, never the other way
+  p.split = need && use_split(T, B, Hkv, head_dim, q_tokens, max_context, p.window, p.sinks) ? 1 : 0;
   p.meta = static_cast<int4*>(workspace);
   p.ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + kMetaBytes);
   p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kMetaBytes + kMlBytes);
