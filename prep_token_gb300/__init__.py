@@ -579,12 +579,14 @@ def _attention_args(q, k_cache, v_cache, block_table, query_start, context_lens,
         raise ValueError(f"context_lens has fewer than {B} entries")
     if out is None:
         out = torch.empty((T, H, D), dtype=dtype, device=dev)
+        _lend(stream, dev, out)
     else:
         _need(out, "out", dtype, 3, dev)
         if out.shape[0] < T or out.shape[1:] != q.shape[1:]:
             raise ValueError("out must be [T, H, D]")
     if lse is None:
         lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+        _lend(stream, dev, lse)
     else:
         _need(lse, "lse", torch.float32, 2, dev)
         if not lse.is_contiguous() or lse.shape[0] < T or lse.shape[1] != H:
@@ -592,7 +594,7 @@ def _attention_args(q, k_cache, v_cache, block_table, query_start, context_lens,
     need = library().dsa_paged_attention_workspace_bytes(T, B, H, Hkv, D, max_context)
     ws = ws_bytes = 0
     if need or workspace is not None:
-        workspace, ws, ws_bytes = _scratch(workspace, need, dev)
+        workspace, ws, ws_bytes = _scratch(workspace, need, dev, stream)
     qs, ks, vs, os_, ts = (q.stride(), k_cache.stride(), v_cache.stride(), out.stride(),
                            block_table.stride(0))
     args = (q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2],
@@ -685,10 +687,22 @@ def _list(t, name, dev):
     return t.data_ptr()
 
 
-def _scratch(workspace, need, dev):
+def _lend(stream, dev, *tensors):
+    """Tensors allocated for a call on a stream that is not the current one:
+    their memory is not given out again before that stream has passed them."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), dev) if int(stream) \
+                else torch.cuda.default_stream(dev)
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _scratch(workspace, need, dev, stream=None):
     """A given workspace checked, or one allocated: (keep, pointer, bytes)."""
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        _lend(stream, dev, workspace)
     if not isinstance(workspace, torch.Tensor) or workspace.device != dev \
             or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
@@ -736,7 +750,7 @@ def dsa_cache_fork(caches, page_refs, block_table, context_lens, page_size, pare
     if children.shape[0] != n:
         raise ValueError("parents and children differ in length")
     hold, bases, sizes, n_caches = _cache_arrays(caches, num_pages, dev)
-    keep, ws, ws_bytes = _scratch(workspace, 8 * n, dev)
+    keep, ws, ws_bytes = _scratch(workspace, 8 * n, dev, stream)
     with _on(dev):
         st = library().dsa_cache_fork(
             bases, sizes, n_caches, num_pages, *pool, int(page_size), parents_ptr, children_ptr, n,
@@ -776,12 +790,13 @@ def dsa_cache_compact(caches, page_refs, block_table, context_lens, page_size, *
     hold, bases, sizes, n_caches = _cache_arrays(caches, num_pages, dev)
     if live_pages is None:
         live_pages = torch.empty(1, dtype=torch.int32, device=dev)
+        _lend(stream, dev, live_pages)
     _list(live_pages, "live_pages", dev)
     if live_pages.numel() < 1:
         raise ValueError("live_pages must hold one int32")
     lib = library()
     keep, ws, ws_bytes = _scratch(
-        workspace, lib.dsa_cache_compact_workspace_bytes(num_pages), dev)
+        workspace, lib.dsa_cache_compact_workspace_bytes(num_pages), dev, stream)
     with _on(dev):
         st = lib.dsa_cache_compact(
             bases, sizes, n_caches, num_pages, *pool, int(page_size), live_pages.data_ptr(), 0, ws,

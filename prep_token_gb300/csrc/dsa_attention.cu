@@ -922,12 +922,21 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
       const int every_lo = p.window ? g.pos0 + g.tokens - p.window : 0;
       for (int k = begin; k < end; ++k) {
         const int key0 = (k < sink_blocks ? k : k + skip) * kKeys;
+        auto scores_done = [&]() {
+          ok = __all_sync(kFull, wait_soon(sfull(j, block), turn(block), abort_flag));
+          tc_fence_after();
+          return ok;
+        };
+        if (QT == 1 && !scores_done()) break;
         // Where some row of the item does not see some key of the block, 0 *
         // its V must be 0 whatever V holds.  Tile 0's thread r looks at key
         // r's row: it zeroes what no row sees (behind the context, before the
         // window) and what is not finite.  In the latter case the rows that do
-        // see the key become NaN.  Tile 0's P V comes first, and waits.  All of it
-        // before S is waited for: V comes sooner.
+        // see the key become NaN.  Tile 0's P V comes first, and waits.  With two
+        // tiles all of it is done before S is waited for, as V comes sooner.
+        // That takes a ring so long that the unit before V's in its place has
+        // landed by now: a barrier's parity tells only its last two phases apart.
+        static_assert(QT == 1 || S >= 4 * kP, "a place of V is looked at too early");
         if (!(key0 + kKeys <= every_hi && (key0 >= every_lo || key0 + kKeys <= p.sinks))) {
           if (j == 0) {
             const int key = key0 + row;
@@ -980,9 +989,7 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
           }
           ++edges;
         }
-        ok = __all_sync(kFull, wait_soon(sfull(j, block), turn(block), abort_flag));
-        if (!ok) break;
-        tc_fence_after();
+        if (QT == 2 && !scores_done()) break;
         const uint32_t t_s = tmem_s(at_s) + lanes;
         const bool edge = !(key0 + kKeys <= hi_all && (key0 >= lo_all || key0 + kKeys <= p.sinks));
 #pragma unroll 1
@@ -1033,11 +1040,14 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
                                               : fmaxf(mx[q], s[i + q]);
                 const float m_new = max3f(m, fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 if (k > begin || half == 1) {  // O exists
-                  // and has to be complete up to the half before; with one place
-                  // for S sfull followed the products of the block before
-                  if (half == 1 || kLook == 3)
-                    ok = __all_sync(kFull, wait_soon(half == 1 ? ohalf(j) : oblock(j),
-                                                     (block + 1 - half) & 1, abort_flag));
+                  // and has to be complete up to the half before.  With one place
+                  // for S per tile sfull followed the products of the block
+                  // before; else they are waited for, before ohalf, whose
+                  // parity would else not tell this block from the last but one.
+                  if (kLook == 3)
+                    ok = __all_sync(kFull, wait_soon(oblock(j), (block + 1) & 1, abort_flag));
+                  if (half == 1)
+                    ok = __all_sync(kFull, wait_soon(ohalf(j), block & 1, abort_flag) && ok);
                   tc_fence_after();
                   // a first maximum meets O and l that are still 0
                   const float f = renew && m != -INFINITY ? exp2_approx((m - m_new) * p.c) : 1.0f;
@@ -1479,6 +1489,9 @@ dsa_status dsa_paged_attention(
   auto bad_stride = [](int64_t stride, int64_t extent) {
     return extent > 1 && (stride % 8 != 0);
   };
+  // rows of out may not overlap
+  if ((T > 1 && out_stride_t < head_dim) || (H > 1 && out_stride_h < head_dim))
+    return DSA_ERR_SHAPE;
   auto bad_size = [](int64_t stride, int64_t extent) {
     return extent > 1 && (stride < 1 || stride >= (1LL << 39));
   };

@@ -133,7 +133,7 @@ def _att(lib, **over):
     (dict(q=A + 8), 2), (dict(k=A + 8), 2), (dict(v=A + 8), 2), (dict(out=A + 8), 2),
     (dict(qst=1028), 2), (dict(ksp=16388), 2), (dict(vsh=124), 2), (dict(osh=132), 2),
     (dict(lse=A + 2), 2), (dict(ws=A + 8), 2), (dict(wsb=1 << 20), 3), (dict(kst=0), 3),
-    (dict(ksp=-16384), 3), (dict(T=1 << 29, H=8), 3),
+    (dict(ksp=-16384), 3), (dict(T=1 << 29, H=8), 3), (dict(osh=64), 3), (dict(ost=0), 3),
     (dict(T=0, q=None, out=None), 0), (dict(B=0, start=None), 0)])
 def test_attention_validation(lib, over, status):
     assert _att(lib, **over) == status

@@ -117,16 +117,20 @@ def test_long_chunk():
     go([700], [9000], 16, 2, seed=5)
 
 
-def test_peaked_scores_rescale():
-    """Scores far above one another, growing along the keys, so that the running
-    maximum moves often, in rows of one warp at different blocks."""
-    b = Batch([40], [2000], 8, 1, seed=6, poison=False, q_scale=8.0)
-    ramp = torch.linspace(0.1, 3.0, b.k.shape[0] * 64, device="cuda").view(-1, 64, 1, 1)
-    order = torch.argsort(b.table[0, :32].long())
-    b.k[b.table[0, :32].long()] *= ramp[:32].to(b.k.dtype)
-    assert len(order) == 32
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("dim,new,kv", [(128, 40, 1), (64, 40, 1), (128, 1, 1), (64, 500, 2)])
+def test_peaked_scores_rescale(dim, new, kv, dtype):
+    """Scores far above one another, growing along the keys, so that the row's
+    reference moves often, in rows of one warp at different blocks and halves.
+    Every pass gives the bits of the first, which is checked."""
+    b = Batch([new], [4000], 8, kv, dim, dtype=dtype, seed=6, poison=False, q_scale=8.0)
+    pages = b.table[0, :63].long()
+    b.k[pages] *= torch.linspace(0.05, 4.0, 63 * 64, device="cuda").view(63, 64, 1, 1).to(dtype)
     out, lse = b.run()
     b.check(out, lse)
+    for _ in range(10):
+        again = b.run()
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
 
 
 def test_equal_scores_average_the_values():
@@ -218,6 +222,22 @@ def test_same_call_same_bits():
         assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
 
 
+@pytest.mark.parametrize("window", [0, 700])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_keys_from_far_memory_same_bits(dim, window):
+    """More keys than L2 holds, each block waited for: every pass gives the bits
+    of the first, which is checked."""
+    ctx = [3000 + 37 * i for i in range(40)]
+    b = Batch([1] * 40, ctx, 32, 8, dim, seed=31, window=window, sinks=5)
+    out, lse = b.run()
+    b.check(out, lse)
+    flush = torch.empty(200_000_000, dtype=torch.uint8, device="cuda")
+    for i in range(30):
+        flush.fill_(i)
+        again = b.run()
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1]), f"pass {i}"
+
+
 def test_graph_and_streams():
     """Captured and replayed on new inputs; two calls at once with a workspace each."""
     import prep_token_gb300 as dp
@@ -242,6 +262,25 @@ def test_graph_and_streams():
     torch.cuda.synchronize()
     b.check(out, lse)
     c.check(oc, lc)
+
+
+def test_explicit_stream_keeps_what_was_allocated_for_it():
+    """The call runs late on a stream of its own; what it allocated is not given
+    out again to the current stream meanwhile."""
+    b = Batch([1, 40], [3000, 700], 16, 2, seed=19)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+    out, lse = b.run(stream=side)
+    for _ in range(8):  # of the workspace's size, the outputs' size
+        torch.full((42_000_000,), 255, dtype=torch.uint8, device="cuda")
+        torch.full_like(b.q, 3.0)
+    side.synchronize()
+    b.check(out, lse)
+    again, _ = b.run(stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(out, again)
 
 
 def test_pdl_reads_what_the_call_before_it_wrote():
