@@ -13,7 +13,7 @@
 //
 // A query tile is 128 rows: floor(128 / G) tokens, their G heads of one kv head
 // packed token by token; a single token fills G of them.  A work item is one or
-// two query tiles of one sequence, which share the loaded keys (query_tiles says
+// two query tiles of one sequence, which share the loaded keys (make_plan says
 // when two).
 //   * warps 0 and 2 load: the query tiles, then per key block the 16 KB units of
 //     K (128 keys x 64 dims) and V (8192 / D keys x D dims) into one ring, by
@@ -48,7 +48,7 @@
 //     is unrolled here.
 // The key blocks of all items are laid end to end and cut into equal shares, one
 // per CTA; an item that a cut divides leaves partial (O, m, l) in the workspace,
-// which a second kernel joins in a fixed order.  (use_split says when CTAs take
+// which a second kernel joins in a fixed order.  (make_plan says when CTAs take
 // whole items instead.)
 //
 // Every wait is bounded in time; TMEM is always released before exit.
@@ -1354,44 +1354,85 @@ cudaError_t prepare_device() {
   return e;
 }
 
-// Query tiles of a CTA.  Two where the sequences have half a tile of new tokens
-// or more on average: keys are then loaded once for up to 256 rows.  Measured
-// with one and two, 64 heads of 128 on 8 kv heads, context 4000, 16 sequences
-// of 8, 12, 24 new tokens (16 fill a tile): 62.5 and 60.1, 67 and 63, 106 and
-// 74 us; 64 single tokens over 8192: 325 and 339 us.
-int query_tiles(int T, int B, int q_tokens) {
-  return 2LL * T >= static_cast<long long>(q_tokens) * B ? 2 : 1;
-}
-
 long long max_items(int T, int B, int Hkv, int tile_tokens) {
   return (static_cast<long long>(T) / tile_tokens + B) * Hkv;
 }
 
-// Whether the key blocks are cut into equal shares, or CTAs take whole items.
-// Cutting balances any lengths, but costs about 15 us: the second kernel, and
-// one more item begun per CTA.  So whole items are taken, given two query tiles
-// (one: single tokens, whose lengths differ) and two rounds of them, where
-//   * the last round leaves few block times (1.6 us) idle: a prompt of 8192
-//     with a window of 1024, 32 heads, 7 rounds of 11 blocks, takes 162 us
-//     whole and 187 cut; without the window, 64 blocks, 472 and 460;
-//   * or items of one sequence share keys that L2 cannot hold: a cut's place in
-//     the keys differs from CTA to CTA, so all keys are in use at once, while
-//     items in order keep the CTAs on one kv head: 4096 tokens over 65536 with
-//     8 kv heads (268 MB) take 5.35 ms whole and 5.59 cut, over 32768 2.61 and
-//     2.57.
-bool use_split(int T, int B, int Hkv, int D, int q_tokens, int max_context, int window, int sinks) {
+// Items of about equal lengths.
+long long mean_items(int T, int B, int Hkv, int tile_tokens) {
+  const long long per_head = static_cast<long long>(T) / tile_tokens + (B + 1) / 2;
+  return (per_head > B ? per_head : B) * Hkv;
+}
+
+// Calls that may be cut and need a workspace for it.  Not those of one key
+// block, nor four rounds of items of two tiles over keys that L2 cannot hold: a
+// cut's place in the keys differs from CTA to CTA, so all keys are in use at
+// once, while items in order keep the CTAs on one kv head (4096 tokens over
+// 65536 with 8 kv heads, 268 MB: 5.35 ms whole, 5.59 cut).  Any other call needs
+// it, cut or not, so that a caller may size it for the largest.
+bool may_split(int T, int B, int Hkv, int D, int q_tokens, int max_context) {
   if (max_context <= kKeys) return false;
-  const int tile_tokens = 2 * q_tokens;
-  if (query_tiles(T, B, q_tokens) != 2) return true;
-  // about: how the sequences' ends fall is not known here
-  const long long items = (static_cast<long long>(T) / tile_tokens + (B + 1) / 2) * Hkv;
-  const long long rounds = (items + kSms - 1) / kSms;
-  long long keys = max_context;
-  if (window && static_cast<long long>(window) + sinks + tile_tokens < keys)
-    keys = static_cast<long long>(window) + sinks + tile_tokens;
-  const long long idle = (rounds * kSms - items) * ((keys + kKeys - 1) / kKeys);
-  const double bytes = 4.0 * D * Hkv * max_context * B;
-  return !(rounds >= 2 && idle <= 8LL * kSms) && !(rounds >= 4 && bytes > 2e8);
+  return mean_items(T, B, Hkv, 2 * q_tokens) <= 3 * kSms || 4.0 * D * Hkv * max_context * B <= 2e8 ||
+         2LL * T < static_cast<long long>(q_tokens) * B;
+}
+
+// How a call is carried out: 1 or 2 query tiles per CTA, and whether the key
+// blocks are cut into equal shares or CTAs take whole items.  Two tiles load
+// the keys once for 256 rows, but leave more rows empty where sequences end.
+// Cutting balances any lengths, but its parts are written, joined by a second
+// kernel and read, and one more item is begun per CTA.  The times of both are
+// estimated in us for sequences of equal lengths at max_context (the lengths
+// are on the device), with
+//   block   a key block of a CTA at D = 128 / 64: 2.6 / 1.6 us with one tile
+//           (two CTAs share the SM), 1.7 / 1.1 with two;
+//   item    what an item begins and ends with: 3.5 us, with two tiles 5;
+//   cut     parts and join: 12 us, with two tiles 15;
+//   ragged  a twentieth of an item, by which whole items of unequal lengths
+//           end later.
+// What is cut has two tiles where sequences have half a tile of new tokens.
+// Over 880 random calls (1 to 4096 new tokens, contexts to 40000, 1 to 128
+// sequences, of equal lengths, ragged, or one long context among short ones)
+// the choice takes 2.2% more than the best of the four on average; the rule
+// that it replaces, which cut nearly everything, 11%.  In us:
+//                                        whole, 1 and 2 tiles; cut, 1 and 2
+//   12 x 350 over 2000, 16 on 16, D 64        61    78    88    88
+//   32 x 64 over 1000, 32 on 8, D 128         48    42    97    66
+//   2048 over 2048, 32 on 8                   59    56    87    79
+//   64 x 8 over 500, 32 on 32                 99   133   102   146
+//   8 x 64 over 30000, 32 on 8               352   365   319   196
+//   256 over 8192, 64 on 8                   101   106    81    70
+struct Plan {
+  int tiles;
+  bool split;
+};
+
+Plan make_plan(int T, int B, int Hkv, int D, int q_tokens, int max_context, int window, int sinks,
+               bool may) {
+  constexpr double kItem[2] = {3.5, 5.0}, kCut[2] = {12.0, 15.0}, kRagged = 0.05;
+  const double block[2] = {D == 64 ? 1.6 : 2.6, D == 64 ? 1.1 : 1.7};
+  const int most_tiles = 2LL * T < static_cast<long long>(q_tokens) * B ? 1 : 2;
+  Plan best = {1, false};
+  double best_us = 0;
+  for (int tiles = 1; tiles <= most_tiles; ++tiles) {
+    const int tile_tokens = tiles * q_tokens;
+    const double items = static_cast<double>(mean_items(T, B, Hkv, tile_tokens));
+    double keys = max_context;  // of an item on average
+    if (window) {
+      const double most = static_cast<double>(window) + sinks + tile_tokens;
+      keys = most < keys ? most : keys;
+    } else {
+      const double new_tokens = static_cast<double>(T) / B;
+      keys -= (new_tokens < keys ? new_tokens : keys) / 2;
+      keys = keys < kKeys ? kKeys : keys;
+    }
+    const double ctas = 2 / tiles * kSms, one = keys / kKeys * block[tiles - 1];
+    const double whole = std::ceil(items / ctas) * (one + kItem[tiles - 1]) + kRagged * one;
+    if (tiles == 1 || whole < best_us) best = {tiles, false}, best_us = whole;
+    if (!may || tiles < most_tiles) continue;
+    const double cut = items / ctas * one + (items / ctas + 1) * kItem[tiles - 1] + kCut[tiles - 1];
+    if (cut < best_us) best = {tiles, true}, best_us = cut;
+  }
+  return best;
 }
 
 bool encode_map(CUtensorMap* map, bool bf16, const void* base, int rank, const cuuint64_t* dims,
@@ -1449,7 +1490,7 @@ extern "C" {
 size_t dsa_paged_attention_workspace_bytes(int32_t T, int32_t B, int32_t H, int32_t Hkv,
                                            int32_t head_dim, int32_t max_context) {
   if (T < 1 || B < 1 || Hkv < 1 || H < Hkv || H % Hkv || H / Hkv > kRows || head_dim < 1) return 0;
-  if (!use_split(T, B, Hkv, head_dim, kRows / (H / Hkv), max_context, 0, 0)) return 0;
+  if (!may_split(T, B, Hkv, head_dim, kRows / (H / Hkv), max_context)) return 0;
   return kMetaBytes + kMlBytes + kPartRows * static_cast<size_t>(head_dim) * sizeof(float);
 }
 
@@ -1559,15 +1600,15 @@ dsa_status dsa_paged_attention(
   p.B = B;
   p.Hkv = Hkv;
   p.G = G;
-  const int tiles = query_tiles(T, B, q_tokens);
+  p.window = window < max_context ? window : 0;  // such a window hides nothing
+  p.sinks = p.window ? (sinks < max_context ? sinks : max_context) : 0;
+  const Plan plan = make_plan(T, B, Hkv, head_dim, q_tokens, max_context, p.window, p.sinks, need > 0);
+  const int tiles = plan.tiles;
   p.q_tokens = q_tokens;
   p.tile_tokens = tiles * q_tokens;
   p.max_context = max_context;
-  p.window = window < max_context ? window : 0;  // such a window hides nothing
-  p.sinks = p.window ? (sinks < max_context ? sinks : max_context) : 0;
   p.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
-  // a window makes whole items likelier, never the other way
-  p.split = need && use_split(T, B, Hkv, head_dim, q_tokens, max_context, p.window, p.sinks) ? 1 : 0;
+  p.split = plan.split ? 1 : 0;
   p.meta = static_cast<int4*>(workspace);
   p.ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + kMetaBytes);
   p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kMetaBytes + kMlBytes);

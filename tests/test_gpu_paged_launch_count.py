@@ -30,6 +30,26 @@ def test_attention(rt, new, ctx, count):  # noqa: F811
     assert _nodes(rt, call) == count
 
 
+@pytest.mark.parametrize("tokens,heads", [(8, 32), (64, 8)])  # a tile of 128 rows, or two
+def test_whole_items_of_short_contexts(rt, tokens, heads):  # noqa: F811
+    """Items enough for the SMs and short: not cut, with a workspace or not used."""
+    import prep_token_gb300 as dp
+    r = torch.Generator().manual_seed(tokens)
+    new = torch.randint(tokens // 2, tokens + 1, (40,), generator=r).tolist()
+    ctx = [n + int(torch.randint(0, 400, (1,), generator=r)) for n in new]
+    b = Batch(new, ctx, 32, heads, 128, seed=tokens)
+    need = dp.dsa_paged_attention_workspace_bytes(sum(new), 40, 32, heads, 128, b.max_context)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(b.q), torch.empty((sum(new), 32), device="cuda")
+
+    def call(s):
+        b.run(out=out, lse=lse, workspace=ws, stream=s)
+
+    call(torch.cuda.current_stream().cuda_stream)
+    b.check(out, lse)
+    assert _nodes(rt, call) == 1
+
+
 def test_pages(rt):  # noqa: F811
     import prep_token_gb300 as dp
     ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
