@@ -375,8 +375,11 @@ dsa_status dsa_indexer_mqa_logits(
  * A visible key whose block-table entry is outside [0, num_pages) sets
  * DSA_DEVERR_SLOT and makes the rows that see it NaN.  Cache contents that no
  * query sees (behind a context, before a window) may be anything, NaN
- * included.  A key or value that is not finite changes only the rows that see
- * it, whose out (some or all elements) and lse are then not finite.
+ * included.  What is not finite changes only the rows that see it.  A score of
+ * NaN or +inf makes their out and lse NaN; a score of -inf is a weight of 0 (a
+ * row that has no other score gets out 0 and lse -inf, as if it saw no key).  A
+ * value never changes lse: out is not finite in the elements in which a value
+ * that the row sees is not, and in such a row the others may be NaN too.
  */
 size_t dsa_paged_attention_workspace_bytes(int32_t T, int32_t B, int32_t H,
                                            int32_t Hkv, int32_t head_dim,

@@ -915,6 +915,7 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
       const int hi_all = __reduce_min_sync(kFull, mine ? hi : 0x7fffffff);
       const int lo_all = __reduce_max_sync(kFull, mine ? lo : 0);
       float m = -INFINITY, l = 0.0f;  // m is the maximum that P and O are scaled by
+      bool spoiled = false;  // this row sees a value, zeroed below, that was not finite
       const int begin = g.begin, end = g.end;
       const int sink_blocks = g.sink_blocks, skip = g.main_block - sink_blocks;
       const int seen_hi = g.hi, seen_lo = g.lo;  // by some row of the item
@@ -931,8 +932,9 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
         // Where some row of the item does not see some key of the block, 0 *
         // its V must be 0 whatever V holds.  Tile 0's thread r looks at key
         // r's row: it zeroes what no row sees (behind the context, before the
-        // window) and what is not finite.  In the latter case the rows that do
-        // see the key become NaN.  Tile 0's P V comes first, and waits.  With two
+        // window) and what is not finite.  In the latter case out of the rows that
+        // do see the key becomes NaN; their lse, which no value enters, does not.
+        // Tile 0's P V comes first, and waits.  With two
         // tiles all of it is done before S is waited for, as V comes sooner.
         // That takes a ring so long that the unit before V's in its place has
         // landed by now: a barrier's parity tells only its last two phases apart.
@@ -984,8 +986,7 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
           for (int i = 0; i < 4; ++i) {
             const int at = key0 + 32 * i;
             const uint32_t mask = odd_keys[4 * (edges & 3) + i];
-            if (mask & below(hi - at) & (~below(lo - at) | below(p.sinks - at)))
-              l = __int_as_float(0x7fc00000);
+            if (mask & below(hi - at) & (~below(lo - at) | below(p.sinks - at))) spoiled = true;
           }
           ++edges;
         }
@@ -1091,7 +1092,8 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
       if (busy) {
         const int head = row % p.G;
         const int slot_of = 2 * blockIdx.x + (begin == 0 ? 1 : 0);
-        const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+        float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;  // of O
+        if (spoiled) inv = __int_as_float(0x7fc00000);
         const long long token = g.token0 + tok;
         const int h = g.h * p.G + head;
         const long long at = static_cast<long long>(slot_of) * (QT * kRows) + tok * p.G + head;
@@ -1136,14 +1138,16 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
           float o[32];
           tmem_ld32(t_o + 32 * i, o);
           tmem_wait_ld(o);
+#pragma unroll
+          for (int q = 0; q < 32; ++q) o[q] *= inv;
           if (whole) {
             uint4 v[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              v[q].x = pack2<BF16>(o[8 * q] * inv, o[8 * q + 1] * inv);
-              v[q].y = pack2<BF16>(o[8 * q + 2] * inv, o[8 * q + 3] * inv);
-              v[q].z = pack2<BF16>(o[8 * q + 4] * inv, o[8 * q + 5] * inv);
-              v[q].w = pack2<BF16>(o[8 * q + 6] * inv, o[8 * q + 7] * inv);
+              v[q].x = pack2<BF16>(o[8 * q], o[8 * q + 1]);
+              v[q].y = pack2<BF16>(o[8 * q + 2], o[8 * q + 3]);
+              v[q].z = pack2<BF16>(o[8 * q + 4], o[8 * q + 5]);
+              v[q].w = pack2<BF16>(o[8 * q + 6], o[8 * q + 7]);
               if (l == 0.0f) v[q] = make_uint4(0, 0, 0, 0);
             }
             store64(v, 64 * i);
