@@ -364,7 +364,10 @@ dsa_status dsa_indexer_mqa_logits(
  *   workspace      dsa_paged_attention_workspace_bytes(T, B, H, Hkv, head_dim,
  *                  max_context) bytes, 16-byte aligned (0 bytes: may be
  *                  NULL), contents scratch; calls that may run at the same
- *                  time need one each.
+ *                  time need one each.  The size may fall to 0 as a call
+ *                  grows: one workspace for calls of many sizes has
+ *                  dsa_paged_attention_max_workspace_bytes(head_dim) bytes,
+ *                  enough for every call with that head_dim.
  *   head_dim 64 or 128; G <= 128; page_size 8, 16, 32 or a multiple of 64;
  *   scale finite and > 0; flags may hold DSA_FLAG_PDL.  q, k_cache, v_cache
  *   and out are 16-byte aligned and their strides multiples of 8; the
@@ -384,6 +387,7 @@ dsa_status dsa_indexer_mqa_logits(
 size_t dsa_paged_attention_workspace_bytes(int32_t T, int32_t B, int32_t H,
                                            int32_t Hkv, int32_t head_dim,
                                            int32_t max_context);
+size_t dsa_paged_attention_max_workspace_bytes(int32_t head_dim);
 
 dsa_status dsa_paged_attention(
     const void* q, int64_t q_stride_t, int64_t q_stride_h,

@@ -32,7 +32,8 @@ __all__ = [
     "dsa_indexer_qk_prepare_store", "dsa_indexer_k_prepare_store", "dsa_status_string",
     "dsa_indexer_qk_prepare_store_unfused", "dsa_unfused_workspace_bytes",
     "dsa_indexer_qk_prepare_store_unfused_noalloc", "dsa_indexer_mqa_logits",
-    "dsa_paged_attention", "dsa_paged_attention_workspace_bytes", "prepare_paged_attention",
+    "dsa_paged_attention", "dsa_paged_attention_workspace_bytes",
+    "dsa_paged_attention_max_workspace_bytes", "prepare_paged_attention",
     "dsa_cache_copy_pages", "dsa_cache_fork", "dsa_cache_free", "dsa_cache_compact",
     "dsa_cache_fork_workspace_bytes", "dsa_cache_compact_workspace_bytes",
     "library", "cache_bytes", "cache_views",
@@ -99,6 +100,8 @@ def library() -> ctypes.CDLL:
         lib.dsa_indexer_mqa_logits.restype = ctypes.c_int
         lib.dsa_paged_attention_workspace_bytes.argtypes = [I32] * 6
         lib.dsa_paged_attention_workspace_bytes.restype = SZ
+        lib.dsa_paged_attention_max_workspace_bytes.argtypes = [I32]
+        lib.dsa_paged_attention_max_workspace_bytes.restype = SZ
         lib.dsa_paged_attention.argtypes = [
             P, I64, I64, P, P, I64, I64, I64, I64, I64, I64, I64, I32, P, I64, P, P, I32, F32, I32,
             I32, P, I64, I64, P, I32, I32, I32, I32, I32, I32, U32, P, SZ, P, P]
@@ -550,6 +553,12 @@ def dsa_paged_attention_workspace_bytes(T: int, B: int, H: int, Hkv: int, head_d
         int(T), int(B), int(H), int(Hkv), int(head_dim), int(max_context)))
 
 
+def dsa_paged_attention_max_workspace_bytes(head_dim: int) -> int:
+    """Workspace that serves every dsa_paged_attention call with this head_dim
+    (the size for one call may be smaller for a larger call)."""
+    return int(library().dsa_paged_attention_max_workspace_bytes(int(head_dim)))
+
+
 def _attention_args(q, k_cache, v_cache, block_table, query_start, context_lens, max_context,
                     scale, window, sinks, out, lse, workspace, err_flags, pdl, stream):
     """Checks and the C argument list; also returns the outputs and the workspace."""
@@ -620,8 +629,9 @@ def dsa_paged_attention(q, k_cache, v_cache, block_table, query_start, context_l
     included.  Each sees the keys up to itself or, with a ``window``, the last
     ``window`` of them (itself counted) and the first ``sinks`` ones.
     ``scale`` defaults to D ** -0.5.  ``workspace``: a CUDA uint8 tensor of at
-    least dsa_paged_attention_workspace_bytes(...) bytes, allocated here when
-    not given.  Returns (out [T, H, D], lse [T, H] fp32); rows that belong to
+    least dsa_paged_attention_workspace_bytes(...) bytes (for calls of many
+    sizes dsa_paged_attention_max_workspace_bytes(D)), allocated here when not
+    given.  Returns (out [T, H, D], lse [T, H] fp32); rows that belong to
     no sequence are left as they are."""
     args, out, lse, workspace = _attention_args(
         q, k_cache, v_cache, block_table, query_start, context_lens, max_context, scale, window,

@@ -1373,7 +1373,7 @@ long long mean_items(int T, int B, int Hkv, int tile_tokens) {
 // cut's place in the keys differs from CTA to CTA, so all keys are in use at
 // once, while items in order keep the CTAs on one kv head (4096 tokens over
 // 65536 with 8 kv heads, 268 MB: 5.35 ms whole, 5.59 cut).  Any other call needs
-// it, cut or not, so that a caller may size it for the largest.
+// it, cut or not; its size is that of the CTAs, whatever the call's.
 bool may_split(int T, int B, int Hkv, int D, int q_tokens, int max_context) {
   if (max_context <= kKeys) return false;
   return mean_items(T, B, Hkv, 2 * q_tokens) <= 3 * kSms || 4.0 * D * Hkv * max_context * B <= 2e8 ||
@@ -1487,6 +1487,10 @@ constexpr size_t kMetaBytes = 2 * kSms * sizeof(int4);
 constexpr size_t kPartRows = 2 * 2 * kSms * kRows;
 constexpr size_t kMlBytes = kPartRows * sizeof(float2);
 
+size_t workspace_bytes_of(int32_t head_dim) {
+  return kMetaBytes + kMlBytes + kPartRows * static_cast<size_t>(head_dim) * sizeof(float);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1495,7 +1499,11 @@ size_t dsa_paged_attention_workspace_bytes(int32_t T, int32_t B, int32_t H, int3
                                            int32_t head_dim, int32_t max_context) {
   if (T < 1 || B < 1 || Hkv < 1 || H < Hkv || H % Hkv || H / Hkv > kRows || head_dim < 1) return 0;
   if (!may_split(T, B, Hkv, head_dim, kRows / (H / Hkv), max_context)) return 0;
-  return kMetaBytes + kMlBytes + kPartRows * static_cast<size_t>(head_dim) * sizeof(float);
+  return workspace_bytes_of(head_dim);
+}
+
+size_t dsa_paged_attention_max_workspace_bytes(int32_t head_dim) {
+  return head_dim < 1 ? 0 : workspace_bytes_of(head_dim);
 }
 
 dsa_status dsa_paged_attention(
