@@ -450,14 +450,17 @@ dsa_status dsa_cache_copy_pages(
  * parents[i].  They share the parent's whole pages (page_refs + 1 each; an
  * absent entry stays absent); where the parent ends inside a page the child
  * gets a free page of its own, into which that page is copied in every cache,
- * so that both may go on writing.  A parent may have any number of children.
+ * so that both may go on writing.  A parent may have any number of children;
+ * the child of an unused row stays unused.  Parents are read as they were
+ * before the call.
  *   parents, children  int32 [n], n <= DSA_MAX_FORKS.  A child must be an
  *                  unused row (context_lens 0), named once.
  *   workspace      dsa_cache_fork_workspace_bytes(n) bytes, 8-byte aligned,
  *                  contents scratch.
  * A fork whose rows are out of range, whose child is in use or was named
- * before, or whose parent has more blocks than bt_cols sets DSA_DEVERR_ROW and
- * does not happen.  Free pages are given in the order of the list; a fork
+ * before, whose parent has more blocks than bt_cols, or whose parent is unused
+ * and named as a child in the same list sets DSA_DEVERR_ROW and does not
+ * happen.  Free pages are given in the order of the list; a fork
  * that finds none sets DSA_DEVERR_POOL and does not happen.
  */
 size_t dsa_cache_fork_workspace_bytes(int32_t n);

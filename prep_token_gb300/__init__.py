@@ -753,7 +753,8 @@ def dsa_cache_fork(caches, page_refs, block_table, context_lens, page_size, pare
     launches).  caches: contiguous CUDA tensors of page_refs.numel() equal
     pages each; page_refs [pages], block_table [rows, blocks], context_lens
     [rows], parents and children [n] int32.  Children are unused rows
-    (context_lens 0), each named once."""
+    (context_lens 0), each named once; parents are read as they were before
+    the call, so a child of the list is no parent of it."""
     dev, num_pages, pool = _pool(page_refs, block_table, context_lens)
     parents_ptr, children_ptr = _list(parents, "parents", dev), _list(children, "children", dev)
     n = parents.shape[0]

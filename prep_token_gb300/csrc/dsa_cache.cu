@@ -165,8 +165,11 @@ __global__ void __launch_bounds__(kPlanThreads) dsa_fork_plan_kernel(const ForkP
     }
   }
   __syncthreads();
-  if (i < p.n)  // a child named before belongs to the earlier fork
+  if (i < p.n) {  // a child named before belongs to the earlier fork
     for (int j = 0; j < i; ++j) ok = ok && child_of[j] != child;
+    if (ok && len == 0)  // parents are read as they were: one that this call makes is not there yet
+      for (int j = 0; j < p.n; ++j) ok = ok && child_of[j] != parent;
+  }
   if (i < p.n && !ok) report(p.err, DSA_DEVERR_ROW);
   const bool need = ok && len % p.page_size != 0;
   int total = 0;
