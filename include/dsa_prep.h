@@ -497,8 +497,8 @@ dsa_status dsa_cache_free(
  * Pages L and above are free afterwards (their bytes stay).  num_pages <= 2^20.
  *   workspace      dsa_cache_compact_workspace_bytes(num_pages) bytes, 4-byte
  *                  aligned, contents scratch.
- * A table entry whose page has no reference and lies above the border becomes
- * -1 and sets DSA_DEVERR_REFS.
+ * A table entry whose page has no reference becomes -1 and sets
+ * DSA_DEVERR_REFS.
  */
 size_t dsa_cache_compact_workspace_bytes(int64_t num_pages);
 

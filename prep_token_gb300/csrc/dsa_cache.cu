@@ -297,7 +297,8 @@ struct CompactParams {
   long long bt_stride;
   int bt_cols, rows, num_pages, page_size;
   int* live;
-  int* moves;  // workspace: count, then src[num_pages / 2 + 1], dst[the same], to[num_pages]
+  int* moves;  // workspace: count, then src[num_pages / 2 + 1], dst[the same], and
+               // to[num_pages]: where a page's entries point afterwards, -1 if it was free
   int* err;
 };
 
@@ -359,8 +360,10 @@ __global__ void __launch_bounds__(kPlanThreads) dsa_compact_plan_kernel(const Co
     for (unsigned b = used[w] & ~below(w); b; b &= b - 1) src[mover_at++] = 32 * w + __ffs(b) - 1;
   }
   __syncthreads();
-  for (int page = live + threadIdx.x; page < p.num_pages; page += kPlanThreads)
-    if (!(used[page >> 5] >> (page & 31) & 1)) to[page] = -1;
+  for (int page = threadIdx.x; page < p.num_pages; page += kPlanThreads) {
+    const bool in_use = used[page >> 5] >> (page & 31) & 1;
+    if (!in_use || page < live) to[page] = in_use ? page : -1;
+  }
   for (int k = threadIdx.x; k < count; k += kPlanThreads) {
     const int s = src[k], d = dst[k];
     to[s] = d;
@@ -388,7 +391,6 @@ __global__ void __launch_bounds__(kCopyThreads)
     return;
   }
   if (blockIdx.z != 0) return;
-  const int live = *p.live;
   for (int row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const int len = p.lens[row];
     long long blocks = len > 0 ? (static_cast<long long>(len) + p.page_size - 1) / p.page_size : 0;
@@ -399,14 +401,15 @@ __global__ void __launch_bounds__(kCopyThreads)
     int* entry = p.table + row * p.bt_stride;
     for (int j = threadIdx.x; j < blocks; j += kCopyThreads) {
       const int e = entry[j];
-      if (e < live) continue;  // absent, or a page that stays
+      if (e < 0) continue;
       if (e >= p.num_pages) {
         report(p.err, DSA_DEVERR_SLOT);
         continue;
       }
       const int moved = to[e];
-      if (moved < 0) report(p.err, DSA_DEVERR_REFS);  // an entry that held a free page
-      entry[j] = moved;
+      // an entry that held a free page: another row's page may be there by now
+      if (moved < 0) report(p.err, DSA_DEVERR_REFS);
+      if (moved != e) entry[j] = moved;
     }
   }
 }

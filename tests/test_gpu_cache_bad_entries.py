@@ -1,7 +1,8 @@
-"""Lists that contradict themselves: a fork of a row that the same list makes."""
+"""Lists and tables that contradict themselves: a fork of a row that the same
+list makes, an entry that holds a page without references."""
 import pytest
 
-from _pool import ROW, Pool
+from _pool import REFS, ROW, Pool
 from test_gpu_cache import Device, _cuda  # noqa: F401  (a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -43,4 +44,18 @@ def test_fork_of_a_used_row_that_the_list_names_as_a_child():
     for q in (p, d):
         q.fork([0, 1], [1, 2])
     assert p.err == ROW and p.lens[:3].tolist() == [6, 9, 9]
+    d.check(p)
+
+def test_compact_leaves_no_entry_on_a_page_that_another_row_gets():
+    """An entry below the border whose page nobody counts: the page is a hole, and
+    another row's page moves there."""
+    p = Pool(12, 3, 4, 4, [16, 8])
+    p.fill_row(0, 11, [5, 0, 9])
+    p.fill_row(1, 7, [2, 7])
+    p.refs[2] = 0
+    d = Device(p, extra_cols=1)
+    assert d.compact() == p.compact() == 4
+    assert p.table[0, :3].tolist() == [1, 0, 3] and p.table[1, :2].tolist() == [2, 2]
+    p.table[1, 0] = -1
+    p.err |= REFS
     d.check(p)
