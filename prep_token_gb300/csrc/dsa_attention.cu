@@ -1376,6 +1376,10 @@ long long mean_items(int T, int B, int Hkv, int tile_tokens) {
 // it, cut or not; its size is that of the CTAs, whatever the call's.
 bool may_split(int T, int B, int Hkv, int D, int q_tokens, int max_context) {
   if (max_context <= kKeys) return false;
+  // seek counts the key blocks of a sequence and kv head in 32 bits: 116,000 rows
+  // over 2^30 keys would pass them
+  const long long blocks = (max_context + kKeys - 1LL) / kKeys;
+  if ((static_cast<long long>(T) / q_tokens + 1) * blocks > 0x7fffffffLL) return false;
   return mean_items(T, B, Hkv, 2 * q_tokens) <= 3 * kSms || 4.0 * D * Hkv * max_context * B <= 2e8 ||
          2LL * T < static_cast<long long>(q_tokens) * B;
 }

@@ -36,6 +36,18 @@ def test_a_prompt_needs_none_and_its_decode_step_does(lib):
     assert _att(lib, wsb=need - 1, **big) == 3
 
 
+@pytest.mark.parametrize("T,B,H,kv,ctx", [(116000, 1, 1, 1, 1 << 30), (116000, 1, 1, 1, 400_000_000),
+                                          (900, 1, 128, 1, 400_000_000),
+                                          (4_000_000, 70_000, 1, 1, 10_000_000)])
+def test_no_cut_where_a_head_has_more_key_blocks_than_32_bits_count(lib, T, B, H, kv, ctx):
+    """The place of a cut in a sequence is a 32-bit number of key blocks."""
+    tiles, blocks = -(-T // (128 // (H // kv))), -(-ctx // 128)
+    assert tiles * blocks >= 1 << 31
+    assert dp.dsa_paged_attention_workspace_bytes(T, B, H, kv, 64, ctx) == 0
+    # half the rows, and few enough keys: cut as before
+    assert dp.dsa_paged_attention_workspace_bytes(T // 2, B, H, kv, 64, ctx // 16) > 0
+
+
 @pytest.mark.gpu
 def test_one_workspace_for_a_prompt_and_its_decode_steps():
     if not torch.cuda.is_available():
