@@ -359,7 +359,8 @@ dsa_status dsa_indexer_mqa_logits(
  *   context_lens   int32 [B], keys of each sequence, the new tokens included;
  *                  at most max_context (a longer one is clamped).
  *   window, sinks  0: the whole context.  sinks counts only with a window.
- *   out            dtype [T, H, head_dim], strides out_stride_t, out_stride_h.
+ *   out            dtype [T, H, head_dim], strides out_stride_t, out_stride_h;
+ *                  no two rows may overlap.
  *   lse            fp32 [T, H] contiguous, natural logarithm; may be NULL.
  *   workspace      dsa_paged_attention_workspace_bytes(T, B, H, Hkv, head_dim,
  *                  max_context) bytes, 16-byte aligned (0 bytes: may be

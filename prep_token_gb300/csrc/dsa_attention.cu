@@ -1486,6 +1486,24 @@ cudaError_t launch_tiles(int tiles, const CUtensorMap& tq, const CUtensorMap& tk
                     : launch<D, BF16, 1>(tq, tk, tv, p, pdl, s);
 }
 
+// Whether two of T x H rows of D elements, at t * stride_t + h * stride_h, share
+// an element: rows (t, h) and (t + a, h - b) with |a * stride_t - b * stride_h| < D.
+// Strides are at least D (so rows of one t or one h do not).
+bool rows_overlap(int64_t T, int64_t stride_t, int64_t H, int64_t stride_h, int64_t D) {
+  using Wide = __int128;
+  if (T < 2 || H < 2 || stride_t >= static_cast<Wide>(H - 1) * stride_h + D ||
+      stride_h >= static_cast<Wide>(T - 1) * stride_t + D)
+    return false;
+  if (T < H) return rows_overlap(H, stride_h, T, stride_t, D);
+  for (int64_t b = 1; b < H; ++b) {
+    const Wide x = static_cast<Wide>(b) * stride_h;
+    const Wide a = x / stride_t;  // the nearest multiples are a and a + 1
+    if (a >= 1 && a < T && x - a * stride_t < D) return true;
+    if (a + 1 < T && (a + 1) * stride_t - x < D) return true;
+  }
+  return false;
+}
+
 // the same for one and two query tiles
 constexpr size_t kMetaBytes = 2 * kSms * sizeof(int4);
 constexpr size_t kPartRows = 2 * 2 * kSms * kRows;
@@ -1546,7 +1564,6 @@ dsa_status dsa_paged_attention(
   auto bad_stride = [](int64_t stride, int64_t extent) {
     return extent > 1 && (stride % 8 != 0);
   };
-  // rows of out may not overlap
   if ((T > 1 && out_stride_t < head_dim) || (H > 1 && out_stride_h < head_dim))
     return DSA_ERR_SHAPE;
   auto bad_size = [](int64_t stride, int64_t extent) {
@@ -1563,6 +1580,7 @@ dsa_status dsa_paged_attention(
       bad_stride(v_stride_token, page_size) || bad_stride(v_stride_head, Hkv) ||
       bad_stride(out_stride_t, T) || bad_stride(out_stride_h, H))
     return DSA_ERR_ALIGN;
+  if (rows_overlap(T, out_stride_t, H, out_stride_h, head_dim)) return DSA_ERR_SHAPE;
   if (misaligned(q, 16) || misaligned(k_cache, 16) || misaligned(v_cache, 16) ||
       misaligned(out, 16) || misaligned(block_table, 4) || misaligned(query_start, 4) ||
       misaligned(context_lens, 4) || misaligned(lse, 4) || misaligned(err_flags, 4))
