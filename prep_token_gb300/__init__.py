@@ -662,6 +662,7 @@ def prepare_paged_attention(q, k_cache, v_cache, block_table, query_start, conte
 def _cache_arrays(caches, num_pages: int, device):
     """The host arrays of base pointers and page sizes of the caches of a pool:
     (keep, pointer to the bases, pointer to the sizes, count)."""
+    caches = list(caches)  # gone through more than once
     sizes = [t.nbytes for t in caches]
     for i, t in enumerate(caches):
         if not t.is_contiguous() or t.device != device:
