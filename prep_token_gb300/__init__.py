@@ -587,15 +587,13 @@ def _attention_args(q, k_cache, v_cache, block_table, query_start, context_lens,
     if context_lens.shape[0] < B:
         raise ValueError(f"context_lens has fewer than {B} entries")
     if out is None:
-        out = torch.empty((T, H, D), dtype=dtype, device=dev)
-        _lend(stream, dev, out)
+        out = _new((T, H, D), dtype, dev, stream)
     else:
         _need(out, "out", dtype, 3, dev)
         if out.shape[0] < T or out.shape[1:] != q.shape[1:]:
             raise ValueError("out must be [T, H, D]")
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-        _lend(stream, dev, lse)
+        lse = _new((T, H), torch.float32, dev, stream)
     else:
         _need(lse, "lse", torch.float32, 2, dev)
         if not lse.is_contiguous() or lse.shape[0] < T or lse.shape[1] != H:
@@ -698,22 +696,26 @@ def _list(t, name, dev):
     return t.data_ptr()
 
 
-def _lend(stream, dev, *tensors):
-    """Tensors allocated for a call on a stream that is not the current one:
-    their memory is not given out again before that stream has passed them."""
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), dev) if int(stream) \
-                else torch.cuda.default_stream(dev)
-        for t in tensors:
-            t.record_stream(stream)
+def _new(shape, dtype, dev, stream):
+    """A tensor for a call on `stream`.  Its memory is of that stream's own, so
+    that nothing still queued on the current one uses it, and is not given out
+    again before what is queued on the current one when it is freed has run."""
+    if stream is None or _stream(stream) == _stream(None, dev):
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), dev) if int(stream) \
+            else torch.cuda.default_stream(dev)
+    current = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(current)
+    return t
 
 
 def _scratch(workspace, need, dev, stream=None):
     """A given workspace checked, or one allocated: (keep, pointer, bytes)."""
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-        _lend(stream, dev, workspace)
+        workspace = _new(max(need, 1), torch.uint8, dev, stream)
     if not isinstance(workspace, torch.Tensor) or workspace.device != dev \
             or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
@@ -801,8 +803,7 @@ def dsa_cache_compact(caches, page_refs, block_table, context_lens, page_size, *
     dev, num_pages, pool = _pool(page_refs, block_table, context_lens)
     hold, bases, sizes, n_caches = _cache_arrays(caches, num_pages, dev)
     if live_pages is None:
-        live_pages = torch.empty(1, dtype=torch.int32, device=dev)
-        _lend(stream, dev, live_pages)
+        live_pages = _new(1, torch.int32, dev, stream)
     _list(live_pages, "live_pages", dev)
     if live_pages.numel() < 1:
         raise ValueError("live_pages must hold one int32")
