@@ -543,6 +543,12 @@ def dsa_indexer_mqa_logits(q_fp8, weights, index_k_cache, page_size, block_table
 
 # ------------------------------------------------------- attention over a paged cache
 
+def _span(n) -> int:
+    """A number of tokens as int32 (ctypes would take its low 32 bits): no context
+    is longer than the largest, and the library refuses any negative one."""
+    return max(-1, min(int(n), 0x7FFFFFFF))
+
+
 _ATTENTION_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 
@@ -607,10 +613,10 @@ def _attention_args(q, k_cache, v_cache, block_table, query_start, context_lens,
     args = (q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2],
             vs[0], vs[1], vs[2], num_pages, page_size, block_table.data_ptr(),
             ts if ts > cols or rows > 1 else cols, query_start.data_ptr(), context_lens.data_ptr(),
-            max_context, D ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
-            os_[0], os_[1], lse.data_ptr(), T, B, H, Hkv, D, _ATTENTION_DTYPES[dtype],
-            FLAG_PDL if pdl else 0, ws or None, ws_bytes, _err_ptr(err_flags, dev),
-            _stream(stream, dev))
+            max_context, D ** -0.5 if scale is None else scale, _span(window), _span(sinks),
+            out.data_ptr(), os_[0], os_[1], lse.data_ptr(), T, B, H, Hkv, D,
+            _ATTENTION_DTYPES[dtype], FLAG_PDL if pdl else 0, ws or None, ws_bytes,
+            _err_ptr(err_flags, dev), _stream(stream, dev))
     return args, out, lse, workspace
 
 
@@ -784,8 +790,8 @@ def dsa_cache_free(page_refs, block_table, context_lens, page_size, rows, *, win
     rows_ptr = _list(rows, "rows", dev)
     with _on(dev):
         st = library().dsa_cache_free(
-            num_pages, *pool, int(page_size), rows_ptr, rows.shape[0], int(window), int(sinks), 0,
-            _err_ptr(err_flags, dev), _stream(stream, dev))
+            num_pages, *pool, int(page_size), rows_ptr, rows.shape[0], _span(window), _span(sinks),
+            0, _err_ptr(err_flags, dev), _stream(stream, dev))
     if st != 0:
         raise DsaError(st, "dsa_cache_free")
 
