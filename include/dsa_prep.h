@@ -332,10 +332,13 @@ dsa_status dsa_indexer_mqa_logits(
     int32_t T, int32_t H, uint32_t flags, int32_t* err_flags, void* stream);
 
 /*
- * Attention of new tokens over a paged K/V cache: the dense attention of a
- * DSA model's layers while a context is short of the indexer's top-k, and of
- * sliding-window layers.  A batch of B sequences mixes chunks of prompts and
- * single tokens.  With G = H / Hkv, query i of sequence b (row query_start[b]
+ * Attention of new tokens over a paged K/V cache, kept by the same block tables
+ * and lengths as the index-K cache: the dense attention of layers while a
+ * context is short of the indexer's top-k, and of sliding-window layers, in
+ * models that cache K and V per kv head with one width for both (multi-head,
+ * grouped-query or multi-query attention; a latent cache whose scores and values
+ * differ in width is not read).  The K and V pages are the caller's to write.
+ * A batch of B sequences mixes chunks of prompts and single tokens.  With G = H / Hkv, query i of sequence b (row query_start[b]
  * + i of q, n_b of them) is the token at
  *   pos = context_lens[b] - n_b + i,
  * its keys and values already in the cache, and head h of it sees kv head
@@ -427,9 +430,13 @@ dsa_status dsa_paged_attention(
  * DSA_MAX_CACHES; with none only the tables are kept.
  *
  * A page given out is always the lowest free one, so results do not depend on
- * the order in which the GPU runs.  `flags` must be 0.  Calls on one pool must
- * be ordered (one stream, or events).  Bad entries of the lists and tables set
- * bits of *err_flags and are left out; they never leave the buffers.
+ * the order in which the GPU runs.  A page that a row grows into is the
+ * caller's to take (any free one) and to count.  `flags` must be 0.  Calls on one
+ * pool must be ordered (one stream, or events).  Bad entries of the lists and
+ * tables set bits of *err_flags and are left out; they never leave the buffers.
+ * The tables are held to page_refs as far as each call says: dsa_cache_fork does
+ * not look whether a parent's page has a reference, and one without may be given
+ * out by the same call.
  */
 #define DSA_MAX_CACHES 128
 #define DSA_MAX_FORKS 1024
@@ -462,7 +469,9 @@ dsa_status dsa_cache_copy_pages(
  * before, whose parent has more blocks than bt_cols, or whose parent is unused
  * and named as a child in the same list sets DSA_DEVERR_ROW and does not
  * happen.  Free pages are given in the order of the list; a fork
- * that finds none sets DSA_DEVERR_POOL and does not happen.
+ * that finds none sets DSA_DEVERR_POOL and does not happen.  Where the parent's
+ * last, partly filled page is absent or outside the pool, DSA_DEVERR_SLOT is set
+ * and the child's own page is given but not written.
  */
 size_t dsa_cache_fork_workspace_bytes(int32_t n);
 

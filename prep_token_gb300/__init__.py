@@ -546,7 +546,8 @@ def dsa_indexer_mqa_logits(q_fp8, weights, index_k_cache, page_size, block_table
 def _span(n) -> int:
     """A number of tokens as int32 (ctypes would take its low 32 bits): no context
     is longer than the largest, and the library refuses any negative one."""
-    return max(-1, min(int(n), 0x7FFFFFFF))
+    n = int(n)
+    return n if 0 <= n <= 0x7FFFFFFF else -1 if n < 0 else 0x7FFFFFFF
 
 
 _ATTENTION_DTYPES = {torch.bfloat16: 0, torch.float16: 1}

@@ -48,8 +48,9 @@
 //     is unrolled here.
 // The key blocks of all items are laid end to end and cut into equal shares, one
 // per CTA; an item that a cut divides leaves partial (O, m, l) in the workspace,
-// which a second kernel joins in a fixed order.  (make_plan says when CTAs take
-// whole items instead.)
+// which a second kernel joins in a fixed order.  (make_plan and may_split say when
+// CTAs take whole items instead: then in the order of the batch, so that unequal
+// ones leave CTAs idle at the end.)
 //
 // Every wait is bounded in time; TMEM is always released before exit.
 #include <cuda.h>
@@ -78,7 +79,9 @@ template <int QT>
 struct Shape {
   static constexpr int kThreads = (1 + QT) * 128;  // loads, MMA, 2 idle warps; softmax
   // Registers: the launch's share per thread is 128 (two CTAs of 256 threads)
-  // or 168 (one of 384); the first warpgroup gives some to the others.
+  // or 168 (one of 384); the first warpgroup gives some to the others.  ptxas
+  // allots by the launch's share: with one tile it spills 140 (D 128) and 88 (D
+  // 64) bytes of a thread, with two none.
   static constexpr int kRegsFew = QT == 1 ? 64 : 88;
   static constexpr int kRegsMany = QT == 1 ? 192 : 208;
   static_assert(kRegsFew + QT * kRegsMany <= (1 + QT) * (QT == 1 ? 128 : 168), "registers");
@@ -305,11 +308,7 @@ struct Tile {
   int token0, tokens;  // in q; tokens of the tile
   int pos0;            // position of its first token
   int hi, lo;          // keys seen by some row: [lo, hi) and [0, min(sinks, hi))
-  int sink_blocks, main_block, blocks;
-
-  __device__ __forceinline__ int block(int k) const {  // the k-th block's first key / 128
-    return k < sink_blocks ? k : main_block + k - sink_blocks;
-  }
+  int sink_blocks, main_block, blocks;  // blocks [0, sink_blocks), then from main_block on
 };
 
 __device__ __forceinline__ Tile make_tile(const AParams& p, int q0, int n, int ctx, int t) {
@@ -1373,7 +1372,11 @@ long long mean_items(int T, int B, int Hkv, int tile_tokens) {
 // cut's place in the keys differs from CTA to CTA, so all keys are in use at
 // once, while items in order keep the CTAs on one kv head (4096 tokens over
 // 65536 with 8 kv heads, 268 MB: 5.35 ms whole, 5.59 cut).  Any other call needs
-// it, cut or not; its size is that of the CTAs, whatever the call's.
+// it, cut or not; its size is that of the CTAs, whatever the call's.  The rule
+// goes by capacities, as the lengths are on the device: a batch of that kind with
+// one long context among short ones ends with the CTAs that have it (2048 tokens
+// over 4000 beside 31 single tokens over 3000 and one over 100,000, 64 heads on 8:
+// 1277 us; the chunk and the single tokens as calls of their own 181 + 136).
 bool may_split(int T, int B, int Hkv, int D, int q_tokens, int max_context) {
   if (max_context <= kKeys) return false;
   // seek counts the key blocks of a sequence and kv head in 32 bits: 116,000 rows

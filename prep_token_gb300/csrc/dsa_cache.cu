@@ -15,8 +15,9 @@
 // Bound: the page bytes (2 per byte moved) for large calls, launch and one or
 // two dependent memory round trips for small ones.  Measured (6.78 TB/s): 1024
 // pages of 128 KB in 4 caches, 1.07 GB, copied in 162 us (6.64 TB/s); 600 live of
-// 2048 such pages packed in 8 caches in 146 us, both calls' host time hidden; a
-// fork of 4 rows with 21 caches and the free of the children 9 us in a graph.
+// 2048 such pages packed in 8 caches in 135 us in a graph; a fork of 4 rows with 21
+// caches and the free of the children 9 us, the release of half of 64 rows of 512
+// blocks behind a window 3.3 us, both in a graph.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -449,8 +450,9 @@ dsa_status check_tables(const int32_t* page_refs, const int32_t* block_table, in
   return DSA_OK;
 }
 
-// A launch that may start while the call's first kernel drains; it waits for
-// that kernel's memory before it reads anything.
+// The launch of a call's second kernel, which waits for the first one's memory
+// before it reads anything.  The first does not announce it early, so what the
+// attribute may overlap is the first kernel's very end.
 template <class... P, class... A>
 cudaError_t launch_second(void (*k)(P...), dim3 grid, int threads, cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg = {};
