@@ -49,8 +49,9 @@
  *   - All work is enqueued on `stream` (a cudaStream_t; NULL = the legacy
  *     default stream).  No call synchronises the host, so every call can be
  *     captured into a CUDA graph.  One kernel launch per call (the unfused
- *     comparison chain: four; dsa_cache_fork and dsa_cache_compact: two;
- *     dsa_paged_attention: one or two).  The first call
+ *     comparison chain: four; dsa_cache_fork, dsa_cache_compact and
+ *     dsa_cache_keep: two; dsa_paged_attention and dsa_tree_attention: one or
+ *     two).  The first call
  *     on a device raises the kernel's dynamic shared-memory limit there (a
  *     per-device, once-only setting); make it before capturing a graph.
  *   - Host-side checks: a bad argument returns a status other than DSA_OK and
@@ -91,6 +92,9 @@ typedef enum {
 typedef enum { DSA_ROPE_NEOX = 0, DSA_ROPE_GPTJ = 1 } dsa_rope_style;
 
 typedef enum { DSA_DTYPE_BF16 = 0, DSA_DTYPE_FP16 = 1 } dsa_dtype;
+
+/* How dsa_rms_norm writes a scale 2^e: as fp32, or as the byte e + 127. */
+typedef enum { DSA_SCALE_FP32 = 0, DSA_SCALE_UE8M0 = 1 } dsa_scale_format;
 
 #define DSA_HEAD_DIM 128
 
@@ -332,12 +336,86 @@ dsa_status dsa_indexer_mqa_logits(
     int32_t T, int32_t H, uint32_t flags, int32_t* err_flags, void* stream);
 
 /*
+ * RMS norm of token rows, with the residual's addition in front of it: what a
+ * layer does before its projections, whose 8-bit inputs it can write at once.
+ *   z = x + residual,  y = z * gamma / sqrt(mean(z^2) + eps)
+ * in fp32 from the unrounded z; residual_out = z and out = y, rounded once.
+ * The e4m3 output has one scale per `group` values (the last group of a row may
+ * be shorter), by the rule of the prepare-and-store calls: e = the smallest
+ * integer with max(amax(y), 1e-4) <= 448 * 2^e, codes = e4m3_rne(y * 2^-e),
+ * scale 2^e.
+ *
+ *   x              bf16 or fp16 (dtype) [T, N], row stride x_stride.
+ *   residual       the same, or NULL (z = x).
+ *   residual_out   the same [T, N]; may be NULL, and is without a residual.  May
+ *                  be `residual` or x itself, row for row.
+ *   gamma          fp32 [N], 16-byte aligned; eps finite and > 0.
+ *   out            dtype [T, N], or NULL.  May be x itself, row for row.
+ *   codes, scales  e4m3 bytes [T, N], 8-byte aligned, and [T, ceil(N / group)]
+ *                  scales as scale_format says (fp32: 4-byte aligned), or both
+ *                  NULL.  At least one of out and codes is given.
+ *   N a multiple of 8, at most 32768; group 32 or 128; flags may hold
+ *   DSA_FLAG_PDL.  The 16-bit rows are 16-byte aligned; their strides and
+ *   codes_stride are multiples of 8.  Rows of an output may not overlap.
+ * The squares are summed in fp32, which holds rows with sqrt(sum z^2) < 1.8e19.
+ */
+dsa_status dsa_rms_norm(
+    const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+    void* residual_out, int64_t residual_out_stride, const float* gamma, float eps,
+    void* out, int64_t out_stride, void* codes, int64_t codes_stride,
+    void* scales, int64_t scales_stride, int32_t scale_format, int32_t group,
+    int32_t T, int32_t N, int32_t dtype, uint32_t flags, void* stream);
+
+/*
+ * Appends new tokens to the paged K/V cache that dsa_paged_attention and
+ * dsa_tree_attention read, and rotates q for them, in one launch.  For every
+ * head's row x of q and k, in fp32:
+ *   x *= gamma / sqrt(mean(x^2) + norm_eps)       (where q_gamma or k_gamma is given)
+ *   RoPE on x[0:rope_dim) as in dsa_indexer_qk_prepare_store
+ * rounded once.  k and v rows go to slot out_cache_loc[t] of their caches (slot
+ * s is token s % page_size of page s / page_size), q rows to q_out.
+ *
+ *   q              bf16 or fp16 (dtype) [T, H, head_dim]; H may be 0 (K and V
+ *                  only), then q and q_out may be NULL.
+ *   k, v           the same type [T, Hkv, head_dim].  All three with strides for
+ *                  tokens and heads, so they may be slices of one projection.
+ *   positions, out_cache_loc, cos_cache, sin_cache, cs_stride, max_position
+ *                  as in dsa_indexer_qk_prepare_store.
+ *   q_gamma,       fp32 [head_dim], 16-byte aligned, or NULL (no norm); with
+ *   k_gamma        either, norm_eps is finite and > 0.
+ *   q_out          dtype [T, H, head_dim]; may be q itself (the same strides).
+ *   k_cache,       dtype [num_pages, page_size, Hkv, head_dim], strides for
+ *   v_cache        pages, tokens and heads as in dsa_paged_attention.
+ *   head_dim 64 or 128; rope_dim a multiple of 16, at most head_dim; page_size
+ *   any; T * (H + 2 Hkv) <= 2^30; flags may hold DSA_FLAG_PDL.  Tensors of dtype
+ *   are 16-byte aligned, their strides multiples of 8; rows of q_out, k_cache
+ *   and v_cache may not overlap, nor their dimensions interleave: each stride
+ *   passes what the dimensions of smaller strides span.
+ * Bad positions and slots set their bits as in dsa_indexer_qk_prepare_store: a
+ * token with a bad position writes nothing, one with a bad slot only its q.
+ */
+dsa_status dsa_kv_append(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h,
+    const void* k, int64_t k_stride_t, int64_t k_stride_h,
+    const void* v, int64_t v_stride_t, int64_t v_stride_h,
+    const int64_t* positions, const int64_t* out_cache_loc,
+    const float* cos_cache, const float* sin_cache, int64_t cs_stride,
+    int64_t max_position, const float* q_gamma, const float* k_gamma, float norm_eps,
+    void* q_out, int64_t q_out_stride_t, int64_t q_out_stride_h,
+    void* k_cache, void* v_cache,
+    int64_t kc_stride_page, int64_t kc_stride_token, int64_t kc_stride_head,
+    int64_t vc_stride_page, int64_t vc_stride_token, int64_t vc_stride_head,
+    int64_t num_pages, int32_t page_size, int32_t T, int32_t H, int32_t Hkv,
+    int32_t head_dim, int32_t rope_dim, int32_t rope_style, int32_t dtype,
+    uint32_t flags, int32_t* err_flags, void* stream);
+
+/*
  * Attention of new tokens over a paged K/V cache, kept by the same block tables
  * and lengths as the index-K cache: the dense attention of layers while a
  * context is short of the indexer's top-k, and of sliding-window layers, in
  * models that cache K and V per kv head with one width for both (multi-head,
  * grouped-query or multi-query attention; a latent cache whose scores and values
- * differ in width is not read).  The K and V pages are the caller's to write.
+ * differ in width is not read).  dsa_kv_append writes the pages.
  * A batch of B sequences mixes chunks of prompts and single tokens.  With G = H / Hkv, query i of sequence b (row query_start[b]
  * + i of q, n_b of them) is the token at
  *   pos = context_lens[b] - n_b + i,
@@ -401,6 +479,38 @@ dsa_status dsa_paged_attention(
     int64_t num_pages, int32_t page_size,
     const int32_t* block_table, int64_t bt_stride, const int32_t* query_start,
     const int32_t* context_lens, int32_t max_context, float scale,
+    int32_t window, int32_t sinks,
+    void* out, int64_t out_stride_t, int64_t out_stride_h, float* lse,
+    int32_t T, int32_t B, int32_t H, int32_t Hkv, int32_t head_dim,
+    int32_t dtype, uint32_t flags, void* workspace, size_t workspace_bytes,
+    int32_t* err_flags, void* stream);
+
+/*
+ * Attention for trees of drafted tokens over a paged K/V cache: as
+ * dsa_paged_attention, with the last n_b keys of sequence b -- its drafts, whose
+ * keys and values are in the cache like any others -- visible by a mask.  Draft
+ * i (row query_start[b] + i of q) is key before + i, before = context_lens[b] -
+ * n_b, and sees
+ *   key before + j, j < n_b, where bit j % 32 of tree_mask[query_start[b] + i]
+ *     [j / 32] is set (for a tree: itself and the drafts above it), and
+ *   key j < before with (window == 0 or j > pos - window or j < sinks), where pos
+ *     = before - 1 + the number of drafts it sees, its position in the tree.
+ * The window hides no draft.  A row that sees no key gets out 0 and lse -inf.
+ *   tree_mask      uint32 words [T, mask_words], row stride mask_stride words,
+ *                  4-byte aligned.  Drafts past 32 * mask_words are seen by none;
+ *                  bits at n_b and behind are ignored.
+ *   block_table    entries of all drafts are read, named by a mask or not.
+ * Everything else, the workspace included, is as in dsa_paged_attention.
+ */
+dsa_status dsa_tree_attention(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h,
+    const void* k_cache, const void* v_cache,
+    int64_t k_stride_page, int64_t k_stride_token, int64_t k_stride_head,
+    int64_t v_stride_page, int64_t v_stride_token, int64_t v_stride_head,
+    int64_t num_pages, int32_t page_size,
+    const int32_t* block_table, int64_t bt_stride, const int32_t* query_start,
+    const int32_t* context_lens, int32_t max_context,
+    const uint32_t* tree_mask, int32_t mask_words, int64_t mask_stride, float scale,
     int32_t window, int32_t sinks,
     void* out, int64_t out_stride_t, int64_t out_stride_h, float* lse,
     int32_t T, int32_t B, int32_t H, int32_t Hkv, int32_t head_dim,
@@ -518,6 +628,40 @@ dsa_status dsa_cache_compact(
     int32_t bt_cols, int64_t bt_stride, const int32_t* context_lens,
     int32_t rows, int32_t page_size, int32_t* live_pages, uint32_t flags,
     void* workspace, size_t workspace_bytes, int32_t* err_flags, void* stream);
+
+/*
+ * Keeps the accepted ones of rows' drafted tokens (two launches).  The last
+ * drafted[i] tokens of row which[i] are drafts; kept[i * kept_stride + j], j <
+ * n_kept[i], are the accepted ones among them, ascending from 0.  In every cache
+ * entry before + kept[j] moves to token before + j, before = context_lens[row] -
+ * drafted[i]; context_lens[row] becomes before + n_kept[i]; entries of the table
+ * behind it become -1, their page_refs one less.
+ *
+ * A cache is given by where its tokens' entries are: `bases` and `shapes` are
+ * HOST arrays, read during the call; with s = shapes + 5 * v, token t of page p
+ * of view v is at bases[v] + p * s[0] + t * s[1] + h * s[2], s[4] bytes for each
+ * head h < s[3].  All are multiples of 4 (of 16: 16 bytes move at a time).  A
+ * page-blocked index-K cache is two views, its codes and its scales.  0 <=
+ * n_views <= DSA_MAX_VIEWS; with none only the tables are kept.
+ *
+ *   which, drafted, n_kept  int32 [n], n <= DSA_MAX_KEEPS; every row named once.
+ *   kept           int32 [n, kept_stride >= max_kept]; NULL if max_kept is 0.
+ * An entry of the list whose row is out of range or was named before, whose
+ * drafts pass the row's length, whose length passes the table, or whose kept
+ * are more than max_kept or drafted, not ascending or not among the drafts sets
+ * DSA_DEVERR_ROW and changes nothing.  An entry on a page outside the pool sets
+ * DSA_DEVERR_SLOT and is not moved.  The pages of entries that are written must be the
+ * row's own (after dsa_cache_fork they are).
+ */
+#define DSA_MAX_VIEWS 256
+#define DSA_MAX_KEEPS 1024
+
+dsa_status dsa_cache_keep(
+    void* const* bases, const int64_t* shapes, int32_t n_views, int64_t num_pages,
+    int32_t* page_refs, int32_t* block_table, int32_t bt_cols, int64_t bt_stride,
+    int32_t* context_lens, int32_t rows, int32_t page_size, const int32_t* which,
+    const int32_t* drafted, const int32_t* kept, int64_t kept_stride, int32_t max_kept,
+    const int32_t* n_kept, int32_t n, uint32_t flags, int32_t* err_flags, void* stream);
 
 /* A static, NUL-terminated description of a status code. */
 const char* dsa_status_string(dsa_status status);

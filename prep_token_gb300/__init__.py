@@ -36,6 +36,9 @@ __all__ = [
     "dsa_paged_attention_max_workspace_bytes", "prepare_paged_attention",
     "dsa_cache_copy_pages", "dsa_cache_fork", "dsa_cache_free", "dsa_cache_compact",
     "dsa_cache_fork_workspace_bytes", "dsa_cache_compact_workspace_bytes",
+    "dsa_rms_norm", "dsa_rms_norm_fp8", "dsa_kv_append", "prepare_kv_append",
+    "dsa_tree_attention", "prepare_tree_attention", "dsa_cache_keep", "TokenViews",
+    "index_k_token_views",
     "library", "cache_bytes", "cache_views",
     "PreparedCall", "prepare_qk_prepare_store", "prepare_k_prepare_store",
 ]
@@ -106,6 +109,10 @@ def library() -> ctypes.CDLL:
             P, I64, I64, P, P, I64, I64, I64, I64, I64, I64, I64, I32, P, I64, P, P, I32, F32, I32,
             I32, P, I64, I64, P, I32, I32, I32, I32, I32, I32, U32, P, SZ, P, P]
         lib.dsa_paged_attention.restype = ctypes.c_int
+        lib.dsa_tree_attention.argtypes = [
+            P, I64, I64, P, P, I64, I64, I64, I64, I64, I64, I64, I32, P, I64, P, P, I32, P, I32, I64,
+            F32, I32, I32, P, I64, I64, P, I32, I32, I32, I32, I32, I32, U32, P, SZ, P, P]
+        lib.dsa_tree_attention.restype = ctypes.c_int
         lib.dsa_cache_copy_pages.argtypes = [P, P, I32, I64, P, P, I32, U32, P, P]
         lib.dsa_cache_copy_pages.restype = ctypes.c_int
         lib.dsa_cache_fork_workspace_bytes.argtypes = [I32]
@@ -121,6 +128,16 @@ def library() -> ctypes.CDLL:
         lib.dsa_cache_compact.argtypes = [
             P, P, I32, I64, P, P, I32, I64, P, I32, I32, P, U32, P, SZ, P, P]
         lib.dsa_cache_compact.restype = ctypes.c_int
+        lib.dsa_rms_norm.argtypes = [
+            P, I64, P, I64, P, I64, P, F32, P, I64, P, I64, P, I64, I32, I32, I32, I32, I32, U32, P]
+        lib.dsa_rms_norm.restype = ctypes.c_int
+        lib.dsa_kv_append.argtypes = [
+            P, I64, I64, P, I64, I64, P, I64, I64, P, P, P, P, I64, I64, P, P, F32, P, I64, I64, P,
+            P, I64, I64, I64, I64, I64, I64, I64, I32, I32, I32, I32, I32, I32, I32, I32, U32, P, P]
+        lib.dsa_kv_append.restype = ctypes.c_int
+        lib.dsa_cache_keep.argtypes = [
+            P, P, I32, I64, P, P, I32, I64, P, I32, I32, P, P, P, I64, I32, P, I32, U32, P, P]
+        lib.dsa_cache_keep.restype = ctypes.c_int
         lib.dsa_status_string.argtypes = [ctypes.c_int]
         lib.dsa_status_string.restype = ctypes.c_char_p
         lib.dsa_prep_version.argtypes = []
@@ -541,6 +558,192 @@ def dsa_indexer_mqa_logits(q_fp8, weights, index_k_cache, page_size, block_table
     return logits[:, :max_context]
 
 
+# ------------------------------------------------------- norm and append
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+_16BIT = (torch.bfloat16, torch.float16)
+_SCALES = {torch.float32: 0, torch.float8_e8m0fnu: 1, torch.uint8: 1}
+
+
+def _row_output(t, name, T, N, dtype, dev, stream):
+    """An output [T, N] of rows checked, or a new one."""
+    if t is None:
+        return _new((T, N), dtype, dev, stream)
+    _need(t, name, dtype, 2, dev)
+    if t.shape[0] < T or t.shape[1] != N:
+        raise ValueError(f"{name} must be [{T}, {N}]")
+    return t
+
+
+def _rms_norm(x, gamma, eps, residual, residual_out, out, codes, scales, scale_format, group, pdl,
+              stream):
+    _need(x, "x", _16BIT, 2)
+    dev, dtype = x.device, x.dtype
+    _need(gamma, "gamma", torch.float32, 1, dev)
+    T, N = x.shape
+    if gamma.shape[0] != N:
+        raise ValueError(f"gamma must hold {N} values")
+    res = res_stride = to = to_stride = None
+    if residual is not None:
+        _need(residual, "residual", dtype, 2, dev)
+        if residual.shape != x.shape:
+            raise ValueError("residual and x differ in shape")
+        residual_out = _row_output(residual_out, "residual_out", T, N, dtype, dev, stream)
+        res, res_stride = residual.data_ptr(), residual.stride(0)
+        to, to_stride = residual_out.data_ptr(), residual_out.stride(0)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    with _on(dev):
+        st = library().dsa_rms_norm(
+            x.data_ptr(), x.stride(0), res, res_stride or 0, to, to_stride or 0, gamma.data_ptr(),
+            eps, _ptr(out), out.stride(0) if out is not None else 0, _ptr(codes),
+            codes.stride(0) if codes is not None else 0, _ptr(scales),
+            scales.stride(0) if scales is not None else 0, scale_format, group, T, N,
+            _DTYPES[dtype], FLAG_PDL if pdl else 0, _stream(stream, dev))
+    if st != 0:
+        raise DsaError(st, "dsa_rms_norm")
+    return residual_out
+
+
+def dsa_rms_norm(x, gamma, eps, *, residual=None, residual_out=None, out=None, pdl=False,
+                 stream=None):
+    """RMS norm of rows (one launch): out = z * gamma / sqrt(mean(z^2) + eps)
+    with z = x + residual, in fp32 and rounded once.  x, residual [T, N] bf16 or
+    fp16 (N a multiple of 8, rows of any stride), gamma [N] fp32.  Returns out,
+    or (out, residual_out) with residual_out = z rounded once if a residual is
+    given; residual_out may be the residual, out may be x."""
+    _need(x, "x", _16BIT, 2)
+    out = _row_output(out, "out", *x.shape, x.dtype, x.device, stream)
+    z = _rms_norm(x, gamma, eps, residual, residual_out, out, None, None, 0, 128, pdl, stream)
+    return out if residual is None else (out, z)
+
+
+def dsa_rms_norm_fp8(x, gamma, eps, *, residual=None, group=128, scale_dtype=torch.float32,
+                     residual_out=None, out=None, codes=None, scales=None, pdl=False, stream=None):
+    """dsa_rms_norm with its output in e4m3: codes [T, N] float8_e4m3fn and one
+    power-of-two scale per ``group`` (32 or 128) values, [T, ceil(N / group)]
+    as ``scale_dtype``: torch.float32, or torch.float8_e8m0fnu (torch.uint8:
+    the same bytes).  ``out`` takes the 16-bit output too.  Returns (codes,
+    scales), and residual_out behind them if a residual is given."""
+    _need(x, "x", _16BIT, 2)
+    if group not in (32, 128):
+        raise ValueError("group must be 32 or 128")
+    T, N = x.shape
+    dev = x.device
+    if scales is not None:
+        scale_dtype = scales.dtype
+    if scale_dtype not in _SCALES:
+        raise TypeError("scales are float32, float8_e8m0fnu or uint8")
+    codes = _row_output(codes, "codes", T, N, (torch.float8_e4m3fn, torch.uint8), dev, stream) \
+        if codes is not None else _new((T, N), torch.float8_e4m3fn, dev, stream)
+    scales = _row_output(scales, "scales", T, -(-N // group), scale_dtype, dev, stream)
+    if out is not None:
+        _row_output(out, "out", T, N, x.dtype, dev, stream)
+    z = _rms_norm(x, gamma, eps, residual, residual_out, out, codes, scales, _SCALES[scale_dtype],
+                  group, pdl, stream)
+    return (codes, scales) if residual is None else (codes, scales, z)
+
+
+def _append_args(q, k, v, positions, out_cache_loc, cos_cache, sin_cache, k_cache, v_cache, rope_dim,
+                 rope_style, q_gamma, k_gamma, eps, q_out, num_tokens, max_position, err_flags, pdl,
+                 stream):
+    """Checks and the C argument list; also returns q_out."""
+    _need(k, "k", _16BIT, 3)
+    dev, dtype = k.device, k.dtype
+    _need(v, "v", dtype, 3, dev)
+    _need(k_cache, "k_cache", dtype, 4, dev)
+    _need(v_cache, "v_cache", dtype, 4, dev)
+    _need(positions, "positions", torch.int64, 1, dev)
+    _need(out_cache_loc, "out_cache_loc", torch.int64, 1, dev)
+    T, Hkv, D = k.shape
+    T = T if num_tokens is None else int(num_tokens)
+    num_pages, page_size = k_cache.shape[:2]
+    if v.shape[1:] != k.shape[1:] or v_cache.shape != k_cache.shape \
+            or k_cache.shape[2:] != k.shape[1:]:
+        raise ValueError("k, v and their caches differ in heads or head_dim")
+    H = 0
+    qs = os_ = (0, 0)
+    if q is not None:
+        _need(q, "q", dtype, 3, dev)
+        H = q.shape[1]
+        if q.shape[2] != D:
+            raise ValueError(f"q has head_dim {q.shape[2]}, k {D}")
+        if q_out is None:
+            q_out = _new((T, H, D), dtype, dev, stream)
+        else:
+            _need(q_out, "q_out", dtype, 3, dev)
+            if q_out.shape[0] < T or q_out.shape[1:] != q.shape[1:]:
+                raise ValueError("q_out must be [T, H, D]")
+        qs, os_ = q.stride(), q_out.stride()
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    for name, t in (("q", q), ("k", k), ("v", v), ("positions", positions),
+                    ("out_cache_loc", out_cache_loc)):
+        if t is not None and t.shape[0] < T:
+            raise ValueError(f"{name} has fewer than {T} rows")
+    for name, t in (("q_gamma", q_gamma), ("k_gamma", k_gamma)):
+        if t is not None:
+            _need(t, name, torch.float32, 1, dev)
+            if t.shape[0] != D:
+                raise ValueError(f"{name} must hold {D} values")
+    cs_stride, rows = 0, 1 << 62
+    if rope_dim:
+        _need(cos_cache, "cos_cache", torch.float32, 2, dev)
+        _need(sin_cache, "sin_cache", torch.float32, 2, dev)
+        cs_stride, rows = cos_cache.stride(0), cos_cache.shape[0]
+        if sin_cache.stride(0) != cs_stride or sin_cache.shape[0] != rows:
+            raise ValueError("cos_cache and sin_cache must share rows and row stride")
+        if min(cos_cache.shape[1], sin_cache.shape[1]) < rope_dim // 2:
+            raise ValueError("cos_cache and sin_cache must hold rope_dim / 2 values a row")
+        if max_position is not None and int(max_position) > rows:
+            raise ValueError("max_position passes the rows of cos_cache")
+    ks, vs, kcs, vcs = k.stride(), v.stride(), k_cache.stride(), v_cache.stride()
+    args = (_ptr(q), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+            positions.data_ptr(), out_cache_loc.data_ptr(), _ptr(cos_cache) if rope_dim else None,
+            _ptr(sin_cache) if rope_dim else None, cs_stride,
+            rows if max_position is None else int(max_position), _ptr(q_gamma), _ptr(k_gamma), eps,
+            _ptr(q_out), os_[0], os_[1], k_cache.data_ptr(), v_cache.data_ptr(), kcs[0], kcs[1],
+            kcs[2], vcs[0], vcs[1], vcs[2], num_pages, page_size, T, H, Hkv, D, rope_dim,
+            int(rope_style), _DTYPES[dtype], FLAG_PDL if pdl else 0, _err_ptr(err_flags, dev),
+            _stream(stream, dev))
+    return args, (q_out[:T] if q_out is not None and q_out.shape[0] != T else q_out)
+
+
+def dsa_kv_append(q, k, v, positions, out_cache_loc, cos_cache, sin_cache, k_cache, v_cache, *,
+                  rope_dim=64, rope_style=NEOX, q_gamma=None, k_gamma=None, eps=1e-6, q_out=None,
+                  num_tokens=None, max_position=None, err_flags=None, pdl=False, stream=None):
+    """Appends tokens to a paged K/V cache and rotates their q (one launch).
+
+    q [T, H, D] (or None), k, v [T, Hkv, D] bf16 or fp16, D 64 or 128, of any
+    strides (slices of one projection); positions, out_cache_loc [T] int64;
+    cos/sin caches [max_position, >= rope_dim / 2] fp32; k_cache, v_cache
+    [num_pages, page_size, Hkv, D] views of any strides, written in place at
+    slot out_cache_loc[t].  ``q_gamma``, ``k_gamma`` [D] fp32: an RMS norm of
+    every head of q or k (with ``eps``) before the rotation.  Returns the rotated
+    q [T, H, D] (``q_out``, which may be q itself)."""
+    args, q_out = _append_args(q, k, v, positions, out_cache_loc, cos_cache, sin_cache, k_cache,
+                               v_cache, rope_dim, rope_style, q_gamma, k_gamma, eps, q_out,
+                               num_tokens, max_position, err_flags, pdl, stream)
+    with _on(k.device):
+        st = library().dsa_kv_append(*args)
+    if st != 0:
+        raise DsaError(st, "dsa_kv_append")
+    return q_out
+
+
+def prepare_kv_append(q, k, v, positions, out_cache_loc, cos_cache, sin_cache, k_cache, v_cache, *,
+                      rope_dim=64, rope_style=NEOX, q_gamma=None, k_gamma=None, eps=1e-6,
+                      q_out=None, num_tokens=None, max_position=None, err_flags=None, pdl=False,
+                      stream=None):
+    """dsa_kv_append checked and bound once (see PreparedCall)."""
+    args, q_out = _append_args(q, k, v, positions, out_cache_loc, cos_cache, sin_cache, k_cache,
+                               v_cache, rope_dim, rope_style, q_gamma, k_gamma, eps, q_out,
+                               num_tokens, max_position, err_flags, pdl, stream)
+    keep = (q, k, v, positions, out_cache_loc, cos_cache, sin_cache, k_cache, v_cache, q_gamma,
+            k_gamma, q_out, err_flags)
+    return PreparedCall(library().dsa_kv_append, "dsa_kv_append", args, k.device, q_out, keep)
+
+
 # ------------------------------------------------------- attention over a paged cache
 
 def _span(n) -> int:
@@ -548,9 +751,6 @@ def _span(n) -> int:
     is longer than the largest, and the library refuses any negative one."""
     n = int(n)
     return n if 0 <= n <= 0x7FFFFFFF else -1 if n < 0 else 0x7FFFFFFF
-
-
-_ATTENTION_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 
 def dsa_paged_attention_workspace_bytes(T: int, B: int, H: int, Hkv: int, head_dim: int,
@@ -616,7 +816,7 @@ def _attention_args(q, k_cache, v_cache, block_table, query_start, context_lens,
             ts if ts > cols or rows > 1 else cols, query_start.data_ptr(), context_lens.data_ptr(),
             max_context, D ** -0.5 if scale is None else scale, _span(window), _span(sinks),
             out.data_ptr(), os_[0], os_[1], lse.data_ptr(), T, B, H, Hkv, D,
-            _ATTENTION_DTYPES[dtype], FLAG_PDL if pdl else 0, ws or None, ws_bytes,
+            _DTYPES[dtype], FLAG_PDL if pdl else 0, ws or None, ws_bytes,
             _err_ptr(err_flags, dev), _stream(stream, dev))
     return args, out, lse, workspace
 
@@ -659,6 +859,53 @@ def prepare_paged_attention(q, k_cache, v_cache, block_table, query_start, conte
     keep = (q, k_cache, v_cache, block_table, query_start, context_lens, out, lse, workspace,
             err_flags)
     return PreparedCall(library().dsa_paged_attention, "dsa_paged_attention", args, q.device,
+                        (out, lse), keep)
+
+
+def _tree_args(q, k_cache, v_cache, block_table, query_start, context_lens, max_context, tree_mask,
+               *rest):
+    """_attention_args with the mask's behind max_context."""
+    args, out, lse, workspace = _attention_args(q, k_cache, v_cache, block_table, query_start,
+                                                context_lens, max_context, *rest)
+    _need(tree_mask, "tree_mask", torch.int32, 2, q.device)
+    T, words = tree_mask.shape
+    if T < q.shape[0]:
+        raise ValueError(f"tree_mask has fewer than {q.shape[0]} rows")
+    mask = (tree_mask.data_ptr(), words, tree_mask.stride(0) if T > 1 else words)
+    return args[:18] + mask + args[18:], out, lse, workspace
+
+
+def dsa_tree_attention(q, k_cache, v_cache, block_table, query_start, context_lens, max_context,
+                       tree_mask, *, scale=None, window=0, sinks=0, out=None, lse=None,
+                       workspace=None, err_flags=None, pdl=False, stream=None):
+    """dsa_paged_attention for trees of drafted tokens.  The last n tokens of a
+    sequence, rows query_start[b] .. query_start[b + 1] of q, are its drafts,
+    their keys and values in the cache behind the others'.  tree_mask [T, words]
+    int32: bit j % 32 of word j / 32 of a row says that it sees draft j of its
+    sequence (for a tree itself and those above it).  Of the keys before the
+    drafts a row sees all or, with a ``window``, those within it of the row's
+    position in the tree (as many behind the last of them as it sees drafts) and
+    the first ``sinks``.  Everything else is as in dsa_paged_attention."""
+    args, out, lse, workspace = _tree_args(
+        q, k_cache, v_cache, block_table, query_start, context_lens, max_context, tree_mask, scale,
+        window, sinks, out, lse, workspace, err_flags, pdl, stream)
+    with _on(q.device):
+        st = library().dsa_tree_attention(*args)
+    if st != 0:
+        raise DsaError(st, "dsa_tree_attention")
+    return out, lse
+
+
+def prepare_tree_attention(q, k_cache, v_cache, block_table, query_start, context_lens, max_context,
+                           tree_mask, *, scale=None, window=0, sinks=0, out=None, lse=None,
+                           workspace=None, err_flags=None, pdl=False, stream=None):
+    """dsa_tree_attention checked and bound once (see PreparedCall)."""
+    args, out, lse, workspace = _tree_args(
+        q, k_cache, v_cache, block_table, query_start, context_lens, max_context, tree_mask, scale,
+        window, sinks, out, lse, workspace, err_flags, pdl, stream)
+    keep = (q, k_cache, v_cache, block_table, query_start, context_lens, tree_mask, out, lse,
+            workspace, err_flags)
+    return PreparedCall(library().dsa_tree_attention, "dsa_tree_attention", args, q.device,
                         (out, lse), keep)
 
 
@@ -824,3 +1071,79 @@ def dsa_cache_compact(caches, page_refs, block_table, context_lens, page_size, *
     if st != 0:
         raise DsaError(st, "dsa_cache_compact")
     return live_pages
+
+
+class TokenViews:
+    """Where the entries of a pool's tokens are in each of its caches, described
+    once for dsa_cache_keep.  caches: CUDA tensors [num_pages, page_size, ...]
+    of any strides with one or two more dimensions (K and V caches as
+    [num_pages, page_size, Hkv, D]; index_k_token_views for an index-K cache),
+    the innermost contiguous."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)  # kept alive
+        self.device = self.caches[0].device if self.caches else None
+        self.pages = tuple(self.caches[0].shape[:2]) if self.caches else None
+        shapes = []
+        for i, t in enumerate(self.caches):
+            if not t.is_cuda:
+                raise ValueError(f"caches[{i}] must live on a CUDA device (no CPU path)")
+            if t.device != self.device:
+                raise ValueError(f"caches[{i}] is on {t.device}, the others on {self.device}")
+            if t.dim() not in (3, 4) or tuple(t.shape[:2]) != self.pages:
+                raise ValueError(f"caches[{i}] must be [num_pages, page_size, (heads,) width]")
+            if t.shape[-1] > 1 and t.stride(-1) != 1:
+                raise ValueError(f"caches[{i}]: innermost dimension must be contiguous")
+            size = t.element_size()
+            strides, width = [size * n for n in t.stride()], t.shape[-1] * size
+            heads = t.shape[2] if t.dim() == 4 else 1
+            if heads > 1 and strides[2] == width:  # whole tokens
+                heads, width = 1, heads * width
+            shapes += [strides[0], strides[1], strides[2] if heads > 1 else 0, heads, width]
+        self._bases = array.array("Q", [t.data_ptr() for t in self.caches])
+        self._shapes = array.array("q", shapes)
+
+    def __len__(self):
+        return len(self.caches)
+
+
+def index_k_token_views(index_k_cache: torch.Tensor, page_size: int, cache_layout: str = "paged"):
+    """The tokens' entries of an index-K cache as views of it: [codes
+    [num_pages, page_size, 128], scales [num_pages, page_size, 4]] uint8 of the
+    page-blocked layout, [[num_pages, page_size, 132]] of the token-major one."""
+    pages = _num_pages(index_k_cache, page_size)
+    flat = index_k_cache.view(-1).view(torch.uint8).view(pages, page_size * ROW_BYTES)
+    if _layout(cache_layout):
+        return [flat.view(pages, page_size, ROW_BYTES)]
+    codes = page_size * HEAD_DIM
+    return [flat[:, :codes].unflatten(1, (page_size, HEAD_DIM)),
+            flat[:, codes:].unflatten(1, (page_size, 4))]
+
+
+def dsa_cache_keep(caches, page_refs, block_table, context_lens, page_size, rows, drafted, kept,
+                   n_kept, *, err_flags=None, stream=None):
+    """Keeps the accepted ones of rows' drafted tokens (in place, two launches).
+    The last drafted[i] tokens of row rows[i] are drafts, kept[i, :n_kept[i]]
+    the accepted ones among them, ascending from 0.  In every cache their
+    entries move to the front of the drafts' place; context_lens and the block
+    table shrink to them, and the pages behind go back to the pool.  caches: a
+    TokenViews, or a list of tensors for one; rows, drafted, n_kept [n] int32,
+    kept [n, most] int32."""
+    dev, num_pages, pool = _pool(page_refs, block_table, context_lens)
+    views = caches if isinstance(caches, TokenViews) else TokenViews(caches)
+    page_size = int(page_size)
+    if views.caches and (views.pages != (num_pages, page_size) or views.device != dev):
+        raise ValueError(f"caches must be [{num_pages}, {page_size}, ...] on {dev}")
+    _need(kept, "kept", torch.int32, 2, dev)
+    n, most = kept.shape
+    lists = [_list(t, name, dev) for name, t in (("rows", rows), ("drafted", drafted),
+                                                 ("n_kept", n_kept))]
+    if rows.shape[0] != n or drafted.shape[0] != n or n_kept.shape[0] != n:
+        raise ValueError("rows, drafted, kept and n_kept differ in length")
+    with _on(dev):
+        st = library().dsa_cache_keep(
+            views._bases.buffer_info()[0], views._shapes.buffer_info()[0], len(views), num_pages,
+            *pool, page_size, lists[0], lists[1], kept.data_ptr(), max(kept.stride(0), most), most,
+            lists[2], n, 0, _err_ptr(err_flags, dev), _stream(stream, dev))
+    if st != 0:
+        raise DsaError(st, "dsa_cache_keep")
