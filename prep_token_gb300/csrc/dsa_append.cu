@@ -3,15 +3,27 @@
 // on the way; q goes out rotated in the same launch.
 //
 //   x = q or k of a head, in fp32
-//   x *= gamma / sqrt(mean(x^2) + eps)                    (where gamma is given)
-//   RoPE on x[0:rope_dim): a' = fma(a, c, -(b s)), b' = fma(b, c, a s)
+//   x *= gamma / sqrt(mean(x^2) + eps)             (where gamma is given)
+//   (a, b) -> (a c - b s, b c + a s) on x[0:rope_dim)
 //   rounded once; k and v to slot out_cache_loc[t] of their caches, q to q_out
 //
 // A head's row of D values is D / 16 lanes wide, two 16-byte pieces to a lane:
 // the pieces of a lane that rotates are the two halves of its pairs (NeoX), or
-// neighbours (GPT-J and the values that pass through).  A pair is in one lane
-// and needs no shuffle; a norm's sum takes log2(D / 16) of them.  A warp works
-// on one token, whose cos/sin row it reads once, and 512 / D heads at a time.
+// neighbours (GPT-J, and the values that pass through).  A pair is in one lane
+// and needs no shuffle; a norm's sum takes log2(D / 16) of them.  c, s and gamma
+// are the same for all heads of a token's q (or k): their products are four
+// factors per pair, formed once, and the root is multiplied in at the end.
+//
+// Two kernels: few tokens take a warp to every pass of 512 / D rows, so that all
+// is in flight at once; many take warps that stay and load ahead.
+//
+// Bound: HBM for many tokens, each row read and written once; measured (6.78 TB/s):
+// 8192 tokens of 32 + 16 heads of 128, 206 MB, 37.2 us with both norms (5.5 TB/s),
+// 36.0 without; 4096 of 64 + 16, 29.7 us (5.7 TB/s).  What is missing is the stream
+// kernel's start (three round trips: position, cos/sin, first store) and its
+// instructions (60% of the issue slots at that rate): its first form, with
+// addresses formed anew for each row, took 55 us with norms, and one pass to a warp 66.  16 tokens of
+// 64 + 16 heads take 2.4 us, launch and two dependent reads.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -25,7 +37,14 @@ namespace {
 using namespace dsa_rows;
 
 constexpr int kSms = 152;
-constexpr int kWarps = 8;  // of a CTA
+constexpr int kWarps = 4;  // of a CTA of the direct kernel
+constexpr int kStreamWarps = 8, kStreamCtas = 2;  // of the stream kernel, per CTA and per SM
+// Passes per SM from which on it is the faster one (us, direct and stream): 600
+// tokens of 64 + 16 heads, 79 passes, 6.4 and 6.3; 2048 of them 20 and 16.4; 1500
+// of 24 + 48 heads of 64, 88 passes, 6.9 and 8.0.  A norm's longer arithmetic is
+// worth overlapping earlier: 256 tokens of 32 + 16 heads, 20 passes, 3.3 and 4.0;
+// 1000, 79 passes, 8.7 and 6.2.
+constexpr int stream_passes(bool norm) { return norm ? 40 : 130; }
 
 struct AppendParams {
   const uint16_t *q, *k, *v;
@@ -40,128 +59,329 @@ struct AppendParams {
   int T, H, Hkv;
   int turns;        // lanes of a row that rotate: rope_dim / 16
   int page_size, page_shift;
-  int passes;       // of a warp: it takes passes * (512 / D) heads of a token
-  int chunks;       // warps of a token
+  int passes;       // of a token: its q, k and v rows, 512 / D at a time
+  int q_passes, kv_passes;
   int* err;
 };
 
-template <bool BF16, int D, int STYLE>
-__global__ void __launch_bounds__(32 * kWarps)
-    dsa_kv_append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int kLanes = D / 16;        // of a row
-  constexpr int kRowsOf = 32 / kLanes;  // rows that a warp takes at a time
-  const int lane = threadIdx.x & 31;
-  const int l = lane % kLanes, sub = lane / kLanes;
-  const int item = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int t = item / p.chunks, chunk = item - t * p.chunks;
-  grid_dependency_wait();
-  grid_launch_dependents();
-  if (t >= p.T) return;
-  const long long pos = p.positions[t], slot = p.slots[t];
-  if (pos < 0 || pos >= p.max_position) {
-    if (lane == 0 && chunk == 0 && p.err) atomicOr(p.err, DSA_DEVERR_POSITION);
-    return;
-  }
-  const bool keep = slot >= 0 && slot < p.num_slots;
-  if (!keep && lane == 0 && chunk == 0 && p.err) atomicOr(p.err, DSA_DEVERR_SLOT);
-  long long page = 0, in_page = 0;
-  if (keep) {
-    if (p.page_shift >= 0) {
-      page = slot >> p.page_shift;
-      in_page = slot & (p.page_size - 1);
-    } else {
-      page = slot / p.page_size;
-      in_page = slot - page * p.page_size;
-    }
-  }
-  const bool turns = l < p.turns;
-  const int first = STYLE == DSA_ROPE_NEOX && turns ? l : 2 * l;  // the lane's pieces
-  const int second = STYLE == DSA_ROPE_NEOX && turns ? l + p.turns : 2 * l + 1;
-  float c[8], s[8];
+// Two pieces of neighbouring pairs as the pairs' first values and their second ones.
+__device__ __forceinline__ void split_pairs(float2 (&x)[4], float2 (&y)[4]) {
+  const float2 a[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = 1.0f, s[i] = 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    x[i] = make_float2(a[2 * i].x, a[2 * i + 1].x);
+    y[i] = make_float2(a[2 * i].y, a[2 * i + 1].y);
+  }
+}
+
+// Eight floats of a row as four pairs.
+__device__ __forceinline__ void load8(const float* p, float2 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float4 x = *(reinterpret_cast<const float4*>(p) + i);
+    v[2 * i] = make_float2(x.x, x.y), v[2 * i + 1] = make_float2(x.z, x.w);
+  }
+}
+
+// x' = xx x + xy y, y' = yy y + yx x for a lane's pairs: the rotation and gamma,
+// which are the same for every row of a token's q (or k).
+struct Turn {
+  float2 xx[4], xy[4], yy[4], yx[4];
+};
+
+template <int STYLE, bool NORM>
+__device__ __forceinline__ void make_turn(Turn& r, bool turns, const float* cos, const float* sin,
+                                          const float* gamma, int first, int second) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r.xx[i] = r.yy[i] = make_float2(1.0f, 1.0f), r.yx[i] = r.xy[i] = make_float2(0.0f, 0.0f);
   if (turns) {
+    load8(cos, r.xx);
+    load8(sin, r.yx);
 #pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-      const float4 u = __ldg(reinterpret_cast<const float4*>(p.cos + pos * p.cs_stride + 8 * l + i));
-      const float4 w = __ldg(reinterpret_cast<const float4*>(p.sin + pos * p.cs_stride + 8 * l + i));
-      c[i] = u.x, c[i + 1] = u.y, c[i + 2] = u.z, c[i + 3] = u.w;
-      s[i] = w.x, s[i + 1] = w.y, s[i + 2] = w.z, s[i + 3] = w.w;
-    }
+    for (int i = 0; i < 4; ++i)
+      r.yy[i] = r.xx[i], r.xy[i] = make_float2(-r.yx[i].x, -r.yx[i].y);
   }
-  const int rows = p.H + 2 * p.Hkv;
-  for (int pass = 0; pass < p.passes; ++pass) {
-    const int row = (chunk * p.passes + pass) * kRowsOf + sub;
-    const bool is_q = row < p.H, is_v = row >= p.H + p.Hkv;
-    const int h = is_q ? row : is_v ? row - p.H - p.Hkv : row - p.H;
-    const bool some = row < rows && (is_q || keep);
-    const uint16_t* from = is_q ? p.q + t * p.q_t + h * p.q_h
-                         : is_v ? p.v + t * p.v_t + h * p.v_h : p.k + t * p.k_t + h * p.k_h;
-    uint16_t* to = is_q ? p.q_out + t * p.out_t + h * p.out_h
-                 : is_v ? p.v_cache + page * p.vc_page + in_page * p.vc_token + h * p.vc_head
-                        : p.k_cache + page * p.kc_page + in_page * p.kc_token + h * p.kc_head;
-    uint4 u = make_uint4(0, 0, 0, 0), w = u;
-    if (some) {
-      u = load_piece(from + 8 * first);
-      w = load_piece(from + 8 * second);
-    }
-    float a[8], b[8];
-    unpack8<BF16>(u, a);
-    unpack8<BF16>(w, b);
-    const float* gamma = is_v ? nullptr : is_q ? p.q_gamma : p.k_gamma;
-    if (p.q_gamma || p.k_gamma) {  // the whole warp: its rows may be of more than one kind
-      float sum = 0.0f;
+  if (NORM && gamma) {
+    float2 gx[4], gy[4];
+    load8(gamma + first, gx);
+    load8(gamma + second, gy);
+    if (STYLE == DSA_ROPE_GPTJ) split_pairs(gx, gy);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(a[i], a[i], fmaf(b[i], b[i], sum));
-#pragma unroll
-      for (int o = kLanes / 2; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-      if (gamma) {
-        const float rs = 1.0f / sqrtf(fmaf(sum, 1.0f / D, p.eps));
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const float4 g = __ldg(reinterpret_cast<const float4*>(gamma + 8 * first + i));
-          const float4 f = __ldg(reinterpret_cast<const float4*>(gamma + 8 * second + i));
-          a[i] *= rs * g.x, a[i + 1] *= rs * g.y, a[i + 2] *= rs * g.z, a[i + 3] *= rs * g.w;
-          b[i] *= rs * f.x, b[i + 1] *= rs * f.y, b[i + 2] *= rs * f.z, b[i + 3] *= rs * f.w;
-        }
-      }
-    }
-    if (turns && !is_v) {
-      if (STYLE == DSA_ROPE_NEOX) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x = a[i], y = b[i];
-          a[i] = fmaf(x, c[i], -__fmul_rn(y, s[i]));
-          b[i] = fmaf(y, c[i], __fmul_rn(x, s[i]));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x = a[2 * i], y = a[2 * i + 1];
-          a[2 * i] = fmaf(x, c[i], -__fmul_rn(y, s[i]));
-          a[2 * i + 1] = fmaf(y, c[i], __fmul_rn(x, s[i]));
-          x = b[2 * i], y = b[2 * i + 1];
-          b[2 * i] = fmaf(x, c[4 + i], -__fmul_rn(y, s[4 + i]));
-          b[2 * i + 1] = fmaf(y, c[4 + i], __fmul_rn(x, s[4 + i]));
-        }
-      }
-    }
-    if (gamma || (turns && !is_v)) {
-      u = pack8<BF16>(a);
-      w = pack8<BF16>(b);
-    }
-    if (some) {
-      store_piece(to + 8 * first, u);
-      store_piece(to + 8 * second, w);
+    for (int i = 0; i < 4; ++i) {
+      r.xx[i] = __fmul2_rn(r.xx[i], gx[i]), r.yx[i] = __fmul2_rn(r.yx[i], gx[i]);
+      r.yy[i] = __fmul2_rn(r.yy[i], gy[i]), r.xy[i] = __fmul2_rn(r.xy[i], gy[i]);
     }
   }
 }
 
+// A lane's two pieces of a row, turned; the lanes of a row call it together.
+template <bool BF16, int D, int STYLE, bool NORM>
+__device__ __forceinline__ void turn_row(uint4& u, uint4& w, const Turn& r, bool turns, bool norm,
+                                         float eps) {
+  float2 x[4], y[4];
+  unpack8<BF16>(u, x);
+  unpack8<BF16>(w, y);
+  if (STYLE == DSA_ROPE_GPTJ) split_pairs(x, y);
+  float2 rs = make_float2(1.0f, 1.0f);
+  if (NORM && norm) {
+    float2 sum = __fmul2_rn(x[0], x[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) sum = __ffma2_rn(x[i], x[i], sum);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum = __ffma2_rn(y[i], y[i], sum);
+    float all = sum.x + sum.y;
+#pragma unroll
+    for (int o = D / 32; o; o >>= 1) all += __shfl_xor_sync(kFull, all, o);
+    rs.x = rs.y = rsqrtf(fmaf(all, 1.0f / D, eps));
+  }
+  if (!(turns || (NORM && norm))) return;  // as it is, NaN and all
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = x[i], b = y[i];
+    x[i] = __ffma2_rn(a, r.xx[i], __fmul2_rn(b, r.xy[i]));
+    y[i] = __ffma2_rn(b, r.yy[i], __fmul2_rn(a, r.yx[i]));
+    if (NORM) x[i] = __fmul2_rn(x[i], rs), y[i] = __fmul2_rn(y[i], rs);
+  }
+  if (STYLE == DSA_ROPE_NEOX) {
+    u = pack8<BF16>(x);
+    w = pack8<BF16>(y);
+  } else {
+    u = make_uint4(pack2<BF16>(x[0].x, y[0].x), pack2<BF16>(x[0].y, y[0].y),
+                   pack2<BF16>(x[1].x, y[1].x), pack2<BF16>(x[1].y, y[1].y));
+    w = make_uint4(pack2<BF16>(x[2].x, y[2].x), pack2<BF16>(x[2].y, y[2].y),
+                   pack2<BF16>(x[3].x, y[3].x), pack2<BF16>(x[3].y, y[3].y));
+  }
+}
+
+// Where a lane's values are in a row: the pieces at `first` and `second`.
+template <int D, int STYLE>
+struct Lane {
+  static constexpr int kLanes = D / 16;        // of a row
+  static constexpr int kRowsOf = 32 / kLanes;  // rows that a warp takes at a time
+  int l, sub, first, second;
+  bool turns;
+  __device__ __forceinline__ explicit Lane(const AppendParams& p) {
+    const int lane = threadIdx.x & 31;
+    l = lane % kLanes, sub = lane / kLanes;
+    turns = l < p.turns;
+    first = 8 * (STYLE == DSA_ROPE_NEOX && turns ? l : 2 * l);
+    second = 8 * (STYLE == DSA_ROPE_NEOX && turns ? l + p.turns : 2 * l + 1);
+  }
+};
+
+// The token's place in a cache.
+__device__ __forceinline__ long long place_of(const AppendParams& p, long long slot,
+                                              long long page_stride, long long token_stride) {
+  long long page, in_page;
+  if (p.page_shift >= 0) {
+    page = slot >> p.page_shift;
+    in_page = slot & (p.page_size - 1);
+  } else {
+    page = slot / p.page_size;
+    in_page = slot - page * p.page_size;
+  }
+  return page * page_stride + in_page * token_stride;
+}
+
+// Few tokens: a warp to each pass of a token (512 / D rows of q, k or v).
+template <bool BF16, int D, int STYLE, bool NORM>
+__global__ void __launch_bounds__(32 * kWarps)
+    dsa_kv_append_kernel(const __grid_constant__ AppendParams p) {
+  const int item = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int t = item / p.passes, pass = item - t * p.passes;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (t >= p.T) return;
+  const Lane<D, STYLE> at(p);
+  const bool is_q = pass < p.q_passes, is_v = pass >= p.q_passes + p.kv_passes;
+  const int row = (pass - (is_q ? 0 : is_v ? p.q_passes + p.kv_passes : p.q_passes)) *
+                      at.kRowsOf + at.sub;
+  const bool some = row < (is_q ? p.H : p.Hkv);
+  const uint16_t* const from = is_q   ? p.q + t * p.q_t + row * p.q_h
+                               : is_v ? p.v + t * p.v_t + row * p.v_h
+                                      : p.k + t * p.k_t + row * p.k_h;
+  // the rows travel beside the position and the slot that they wait for
+  const long long pos = __ldg(p.positions + t), slot = __ldg(p.slots + t);
+  uint4 u = make_uint4(0, 0, 0, 0), w = u;
+  if (some) {
+    u = load_piece(from + at.first);
+    w = load_piece(from + at.second);
+  }
+  const bool first_lane = (threadIdx.x & 31) == 0 && pass == 0;
+  if (pos < 0 || pos >= p.max_position) {
+    if (first_lane && p.err) atomicOr(p.err, DSA_DEVERR_POSITION);
+    return;
+  }
+  const bool keep = slot >= 0 && slot < p.num_slots;
+  if (!keep && first_lane && p.err) atomicOr(p.err, DSA_DEVERR_SLOT);
+  if (!is_q && !keep) return;
+  if (!is_v) {
+    const float* const gamma = is_q ? p.q_gamma : p.k_gamma;
+    Turn r;
+    make_turn<STYLE, NORM>(r, at.turns, p.cos + pos * p.cs_stride + 8 * at.l,
+                           p.sin + pos * p.cs_stride + 8 * at.l, gamma, at.first, at.second);
+    turn_row<BF16, D, STYLE, NORM>(u, w, r, at.turns, gamma != nullptr, p.eps);
+  }
+  if (some) {
+    uint16_t* const to =
+        is_q   ? p.q_out + t * p.out_t + row * p.out_h
+        : is_v ? p.v_cache + place_of(p, slot, p.vc_page, p.vc_token) + row * p.vc_head
+               : p.k_cache + place_of(p, slot, p.kc_page, p.kc_token) + row * p.kc_head;
+    store_piece(to + at.first, u);
+    store_piece(to + at.second, w);
+  }
+}
+
+// Many tokens: warps that stay, each on an equal run of all tokens' passes.  A
+// lane's pieces of the passes ahead travel into its own places of a ring in
+// shared memory (cp.async; nobody else reads them), a token's cos/sin row into
+// one of two places of the warp while the token before is worked on.
+constexpr int kDepth = 4;                          // passes in flight, and this one
+constexpr int kWarpBytes = kDepth * 1024 + 2 * 512;  // the ring; cos and sin of two tokens
+
+template <bool BF16, int D, int STYLE, bool NORM>
+__global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
+    dsa_kv_append_stream_kernel(const __grid_constant__ AppendParams p) {
+  __shared__ __align__(16) unsigned char smem[kStreamWarps * kWarpBytes];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Lane<D, STYLE> at(p);
+  unsigned char* const ring = smem + warp * kWarpBytes;
+  float* const angles = reinterpret_cast<float*>(ring + kDepth * 1024);
+  const long long total = static_cast<long long>(p.T) * p.passes;
+  const int warps = gridDim.x * kStreamWarps, me = blockIdx.x * kStreamWarps + warp;
+  const int begin = static_cast<int>(total * me / warps);
+  const int n = static_cast<int>(total * (me + 1) / warps) - begin;
+  if (n == 0) return;
+  int t = begin / p.passes;
+  const int pass = begin - t * p.passes;
+  const int last = (begin + n - 1) / p.passes;  // this warp's last token
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  // Where the loads are: so many passes of q (0), k (1) or v (2) of a token are
+  // left, the next one's row and place; addresses move by the pass within a kind.
+  int fetch_t = t, fetch_kind, fetch_left, fetch_rows, fetch_n = n;
+  uint32_t fetch_to = smem_u32(ring + 16 * lane);
+  const uint32_t ring_end = fetch_to + kDepth * 1024;
+  const uint16_t* fetch_from;
+  long long fetch_step;
+  auto enter = [&](int kind, int skip) {  // `skip` passes of it are done
+    fetch_kind = kind;
+    fetch_left = (kind == 0 ? p.q_passes : p.kv_passes) - skip;
+    const int row = skip * at.kRowsOf + at.sub;
+    fetch_rows = (kind == 0 ? p.H : p.Hkv) - row;
+    fetch_step = kind == 0 ? p.q_h : kind == 1 ? p.k_h : p.v_h;
+    fetch_from = (kind == 0   ? p.q + fetch_t * p.q_t
+                  : kind == 1 ? p.k + fetch_t * p.k_t
+                              : p.v + fetch_t * p.v_t) + row * fetch_step + at.first;
+    fetch_step *= at.kRowsOf;
+  };
+  const int apart = at.second - at.first;
+  auto fetch = [&]() {  // the next pass, if there is one
+    if (fetch_left == 0) {
+      if (fetch_kind == 2) ++fetch_t;
+      enter(fetch_kind == 2 ? (p.q_passes > 0 ? 0 : 1) : fetch_kind + 1, 0);
+    }
+    if (fetch_n > 0 && fetch_rows > 0) {
+      cp_async16_cg(fetch_to, fetch_from);
+      cp_async16_cg(fetch_to + 512, fetch_from + apart);
+    }
+    cp_async_commit();
+    --fetch_n, --fetch_left;
+    fetch_rows -= at.kRowsOf;
+    fetch_from += fetch_step;
+    fetch_to += 1024;
+    if (fetch_to == ring_end) fetch_to -= kDepth * 1024;
+  };
+  auto position = [&](int token) { return token <= last ? __ldg(p.positions + token) : -1; };
+  auto slot_of = [&](int token) { return token <= last ? __ldg(p.slots + token) : -1; };
+  auto valid = [&](long long pos) { return pos >= 0 && pos < p.max_position; };
+  auto fetch_angles = [&](int token, long long pos) {  // 2 * turns pieces each of cos and sin
+    const int piece = lane & 15;
+    if (valid(pos) && piece < 2 * p.turns)
+      cp_async16_ca(smem_u32(angles + (token & 1) * 128 + 4 * lane),
+                    (lane < 16 ? p.cos : p.sin) + pos * p.cs_stride + 4 * piece);
+  };
+  long long slot = slot_of(t), next_slot = slot_of(t + 1), pos = position(t + 1);
+  const long long pos0 = position(t);
+  bool ok = valid(pos0), next_ok = valid(pos);
+  fetch_angles(t, pos0);
+  fetch_angles(t + 1, pos);
+  pos = position(t + 2);  // that of the token behind the next one
+  int kind = pass < p.q_passes ? 0 : pass < p.q_passes + p.kv_passes ? 1 : 2;
+  int skip = pass - (kind == 0 ? 0 : kind == 1 ? p.q_passes : p.q_passes + p.kv_passes);
+  enter(kind, skip);
+#pragma unroll
+  for (int i = 0; i < kDepth - 1; ++i) fetch();
+  cp_async_wait<kDepth - 2>();
+  int stage = 0;
+  // one kind of a token's rows after the other
+#pragma unroll 1
+  for (int left = n;;) {
+    __syncwarp();  // this token's cos and sin have landed for every lane of the warp
+    const bool keep = slot >= 0 && slot < p.num_slots;
+    if (lane == 0 && p.err && !(ok && keep))
+      atomicOr(p.err, ok ? DSA_DEVERR_SLOT : DSA_DEVERR_POSITION);
+    const int row = skip * at.kRowsOf + at.sub;
+    int rows = ok && (kind == 0 || keep) ? (kind == 0 ? p.H : p.Hkv) - row : 0;
+    long long step = kind == 0 ? p.out_h : kind == 1 ? p.kc_head : p.vc_head;
+    uint16_t* to = kind == 0   ? p.q_out + t * p.out_t
+                   : kind == 1 ? p.k_cache + place_of(p, keep ? slot : 0, p.kc_page, p.kc_token)
+                               : p.v_cache + place_of(p, keep ? slot : 0, p.vc_page, p.vc_token);
+    to += row * step + at.first;
+    step *= at.kRowsOf;
+    const float* const gamma = kind == 0 ? p.q_gamma : p.k_gamma;
+    Turn r;
+    if (kind < 2) {
+      const float* const cos = angles + (t & 1) * 128 + 8 * at.l;
+      make_turn<STYLE, NORM>(r, at.turns, cos, cos + 64, gamma, at.first, at.second);
+    }
+    int m = min(left, (kind == 0 ? p.q_passes : p.kv_passes) - skip);
+    left -= m;
+#pragma unroll 1
+    for (; m > 0; --m) {
+      fetch();
+      cp_async_wait<kDepth - 1>();
+      const unsigned char* const from = ring + stage * 1024 + 16 * lane;
+      uint4 u = *reinterpret_cast<const uint4*>(from);
+      uint4 w = *reinterpret_cast<const uint4*>(from + 512);
+      if (kind < 2)
+        turn_row<BF16, D, STYLE, NORM>(u, w, r, at.turns, gamma != nullptr, p.eps);
+      if (rows > 0) {
+        store_piece(to, u);
+        store_piece(to + apart, w);
+      }
+      rows -= at.kRowsOf;
+      to += step;
+      stage = stage + 1 == kDepth ? 0 : stage + 1;
+    }
+    if (left == 0) break;
+    skip = 0;
+    if (++kind == 3) {  // the next token: the one behind it takes the last one's place for cos and sin
+      kind = p.q_passes > 0 ? 0 : 1;
+      ++t;
+      slot = next_slot, ok = next_ok;
+      next_slot = slot_of(t + 1), next_ok = valid(pos);
+      fetch_angles(t + 1, pos);
+      pos = position(t + 2);
+    }
+  }
+}
+
+template <bool BF16, int D, int STYLE, bool NORM>
+cudaError_t launch_one(const AppendParams& p, bool stream, const cudaLaunchConfig_t& cfg) {
+  return stream ? cudaLaunchKernelEx(&cfg, dsa_kv_append_stream_kernel<BF16, D, STYLE, NORM>, p)
+                : cudaLaunchKernelEx(&cfg, dsa_kv_append_kernel<BF16, D, STYLE, NORM>, p);
+}
+
 template <bool BF16, int D>
-cudaError_t launch(const AppendParams& p, int style, const cudaLaunchConfig_t& cfg) {
-  return style == DSA_ROPE_NEOX
-             ? cudaLaunchKernelEx(&cfg, dsa_kv_append_kernel<BF16, D, DSA_ROPE_NEOX>, p)
-             : cudaLaunchKernelEx(&cfg, dsa_kv_append_kernel<BF16, D, DSA_ROPE_GPTJ>, p);
+cudaError_t launch(const AppendParams& p, int style, bool stream, const cudaLaunchConfig_t& cfg) {
+  if (p.q_gamma || p.k_gamma)
+    return style == DSA_ROPE_NEOX ? launch_one<BF16, D, DSA_ROPE_NEOX, true>(p, stream, cfg)
+                                  : launch_one<BF16, D, DSA_ROPE_GPTJ, true>(p, stream, cfg);
+  return style == DSA_ROPE_NEOX ? launch_one<BF16, D, DSA_ROPE_NEOX, false>(p, stream, cfg)
+                                : launch_one<BF16, D, DSA_ROPE_GPTJ, false>(p, stream, cfg);
 }
 
 }  // namespace
@@ -248,25 +468,30 @@ extern "C" dsa_status dsa_kv_append(
   p.turns = rope_dim / 16;
   p.page_size = page_size;
   p.page_shift = page_shift_of(page_size);
-  const int passes = (H + 2 * Hkv + 512 / head_dim - 1) / (512 / head_dim);  // of a token
-  p.passes = 1;
-  p.chunks = (passes + p.passes - 1) / p.passes;
+  const int rows_of = 512 / head_dim;  // that a warp takes at a time
+  p.q_passes = (H + rows_of - 1) / rows_of;
+  p.kv_passes = (Hkv + rows_of - 1) / rows_of;
+  p.passes = p.q_passes + 2 * p.kv_passes;
   p.err = err_flags;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  const long long warps = static_cast<long long>(T) * p.chunks;
-  cfg.gridDim = dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps));
-  cfg.blockDim = dim3(32 * kWarps);
+  const long long all = static_cast<long long>(T) * p.passes;
+  const bool norm = q_gamma || k_gamma;
+  // a token's cos/sin are fetched a token ahead, which has to be kDepth passes at least
+  const bool stream_kernel = all >= stream_passes(norm) * kSms && p.passes >= kDepth;
+  cfg.gridDim = dim3(stream_kernel ? kSms * kStreamCtas
+                                   : static_cast<unsigned>((all + kWarps - 1) / kWarps));
+  cfg.blockDim = dim3(32 * (stream_kernel ? kStreamWarps : kWarps));
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = flags & DSA_FLAG_PDL ? 1 : 0;
   const bool bf16 = dtype == DSA_DTYPE_BF16;
   cudaError_t e;
   if (head_dim == 64)
-    e = bf16 ? launch<true, 64>(p, rope_style, cfg) : launch<false, 64>(p, rope_style, cfg);
+    e = bf16 ? launch<true, 64>(p, rope_style, stream_kernel, cfg) : launch<false, 64>(p, rope_style, stream_kernel, cfg);
   else
-    e = bf16 ? launch<true, 128>(p, rope_style, cfg) : launch<false, 128>(p, rope_style, cfg);
+    e = bf16 ? launch<true, 128>(p, rope_style, stream_kernel, cfg) : launch<false, 128>(p, rope_style, stream_kernel, cfg);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_LAUNCH;
 }

@@ -13,6 +13,12 @@
 // 16-byte pieces of eight values, `threads of the row` pieces apart, so that
 // a group's pieces (16 of 128 values, 4 of 32) sit in neighbouring lanes and
 // its amax takes shuffles only.
+//
+// Bound: HBM.  Measured (6.78 TB/s): 16384 rows of 7168 with a residual, to e4m3,
+// 823 MB, 125.5 us (6.56 TB/s, 0.97); 4096 of them 35.6 us (0.85); one row 2.8 us, launch
+// and one round trip.  No ring and no rows ahead: CTAs that stay and load the next
+// row with cp.async took 141 us, as what counts is how many rows are resident (56
+// registers: five CTAs of 224 threads per SM; 64 registers, four, 131 us).
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -46,67 +52,71 @@ struct NormParams {
 };
 
 // blockDim.x threads for a row, blockDim.y rows.
-template <bool BF16, int PIECES>
-__global__ void __launch_bounds__(kMaxRowThreads) dsa_rms_norm_kernel(const NormParams p) {
-  __shared__ float sums[32];
+template <bool BF16, int PIECES, bool RES>
+__global__ void __maxnreg__(PIECES == 4 ? 56 : 40) dsa_rms_norm_kernel(const NormParams p) {
+  __shared__ float part[32];
+  const int lane = threadIdx.x & 31;
+  const int warps = blockDim.x >> 5, first_warp = threadIdx.y * warps;
   const int row = blockIdx.x * blockDim.y + threadIdx.y;
   const bool mine = row < p.T;
-  const int lane = threadIdx.x & 31;
   grid_dependency_wait();
   grid_launch_dependents();
-  float z[PIECES][8];
-  float sum = 0.0f;
+  uint4 a[PIECES], b[PIECES];
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
     const int at = threadIdx.x + i * blockDim.x;
-    const bool some = mine && at < p.pieces;
-    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-    if (some) {
-      a = load_piece(p.x + row * p.x_stride + 8 * at);
-      if (p.residual) b = load_piece(p.residual + row * p.residual_stride + 8 * at);
+    a[i] = b[i] = make_uint4(0, 0, 0, 0);
+    if (mine && at < p.pieces) {
+      a[i] = load_piece(p.x + row * p.x_stride + 8 * at);
+      if (RES) b[i] = load_piece(p.residual + row * p.residual_stride + 8 * at);
     }
-    unpack8<BF16>(a, z[i]);
-    if (p.residual) {
-      float r[8];
-      unpack8<BF16>(b, r);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) z[i][j] += r[j];
-    }
-    if (p.residual_out && some)
-      store_piece(p.residual_out + row * p.residual_out_stride + 8 * at, pack8<BF16>(z[i]));
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum = fmaf(z[i][j], z[i][j], sum);
   }
+  float2 z[PIECES][4];
+  float2 sum2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const int at = threadIdx.x + i * blockDim.x;
+    unpack8<BF16>(a[i], z[i]);
+    if (RES) {
+      float2 r[4];
+      unpack8<BF16>(b[i], r);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[i][j] = __fadd2_rn(z[i][j], r[j]);
+      if (p.residual_out && mine && at < p.pieces)
+        store_piece(p.residual_out + row * p.residual_out_stride + 8 * at, pack8<BF16>(z[i]));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum2 = __ffma2_rn(z[i][j], z[i][j], sum2);
+  }
+  float sum = sum2.x + sum2.y;
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-  const int warps = blockDim.x >> 5;
   if (warps > 1) {
-    const int first = threadIdx.y * warps;
-    if (lane == 0) sums[first + (threadIdx.x >> 5)] = sum;
+    if (lane == 0) part[first_warp + (threadIdx.x >> 5)] = sum;
     __syncthreads();
-    sum = lane < warps ? sums[first + lane] : 0.0f;
+    sum = lane < warps ? part[first_warp + lane] : 0.0f;
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
   }
   const float rs = 1.0f / sqrtf(fmaf(sum, p.inv_n, p.eps));
+  const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
     const int at = threadIdx.x + i * blockDim.x;
     const bool some = mine && at < p.pieces;
-    float g[8] = {};
+    float amax = 0.0f;
     if (some) {
-      const float4 lo = __ldg(reinterpret_cast<const float4*>(p.gamma + 8 * at));
-      const float4 hi = __ldg(reinterpret_cast<const float4*>(p.gamma + 8 * at + 4));
-      g[0] = lo.x, g[1] = lo.y, g[2] = lo.z, g[3] = lo.w;
-      g[4] = hi.x, g[5] = hi.y, g[6] = hi.z, g[7] = hi.w;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float4 g = __ldg(reinterpret_cast<const float4*>(p.gamma + 8 * at) + j);
+        z[i][2 * j] = __fmul2_rn(__fmul2_rn(z[i][2 * j], rs2), make_float2(g.x, g.y));
+        z[i][2 * j + 1] = __fmul2_rn(__fmul2_rn(z[i][2 * j + 1], rs2), make_float2(g.z, g.w));
+      }
+      if (p.out) store_piece(p.out + row * p.out_stride + 8 * at, pack8<BF16>(z[i]));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) amax = max3f(amax, fabsf(z[i][j].x), fabsf(z[i][j].y));
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) z[i][j] = z[i][j] * rs * g[j];
-    if (p.out && some) store_piece(p.out + row * p.out_stride + 8 * at, pack8<BF16>(z[i]));
     if (p.codes) {
-      float amax = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(z[i][j]));
       amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
       if (p.group_lanes == 16) {
@@ -114,14 +124,16 @@ __global__ void __launch_bounds__(kMaxRowThreads) dsa_rms_norm_kernel(const Norm
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 8));
       }
       const int e = exponent_of_amax(amax);
-      const float down = pow2f(-e);
+      const float2 down = make_float2(pow2f(-e), pow2f(-e));
       if (some) {
-        uint2 c;
-        c.x = cvt_e4m3x2(z[i][0] * down, z[i][1] * down) |
-              cvt_e4m3x2(z[i][2] * down, z[i][3] * down) << 16;
-        c.y = cvt_e4m3x2(z[i][4] * down, z[i][5] * down) |
-              cvt_e4m3x2(z[i][6] * down, z[i][7] * down) << 16;
-        *reinterpret_cast<uint2*>(p.codes + row * p.codes_stride + 8 * at) = c;
+        uint32_t c[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = __fmul2_rn(z[i][j], down);
+          c[j] = cvt_e4m3x2(x.x, x.y);
+        }
+        *reinterpret_cast<uint2*>(p.codes + row * p.codes_stride + 8 * at) =
+            make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
         if (lane % p.group_lanes == 0) {
           const long long s = row * p.scales_stride + at / p.group_lanes;
           if (p.scale_bytes == 1)
@@ -134,13 +146,28 @@ __global__ void __launch_bounds__(kMaxRowThreads) dsa_rms_norm_kernel(const Norm
   }
 }
 
-template <bool BF16>
-cudaError_t launch(const NormParams& p, int pieces, cudaLaunchConfig_t& cfg) {
+template <bool BF16, bool RES>
+cudaError_t launch(const NormParams& p, int pieces, const cudaLaunchConfig_t& cfg) {
   switch (pieces) {
-    case 1: return cudaLaunchKernelEx(&cfg, dsa_rms_norm_kernel<BF16, 1>, p);
-    case 2: return cudaLaunchKernelEx(&cfg, dsa_rms_norm_kernel<BF16, 2>, p);
-    default: return cudaLaunchKernelEx(&cfg, dsa_rms_norm_kernel<BF16, 4>, p);
+    case 1: return cudaLaunchKernelEx(&cfg, dsa_rms_norm_kernel<BF16, 1, RES>, p);
+    case 2: return cudaLaunchKernelEx(&cfg, dsa_rms_norm_kernel<BF16, 2, RES>, p);
+    default: return cudaLaunchKernelEx(&cfg, dsa_rms_norm_kernel<BF16, 4, RES>, p);
   }
+}
+
+// Pieces of a thread: one where all rows are resident at once with it (least
+// latency), four where they are many times that (most bytes in flight for the
+// instructions), two between, unless that makes large CTAs.  In us with 1, 2 and 4
+// pieces, rows x N: 304 x 7168 4.5 4.4 5.2; 608 x 5120 6.7 5.6 6.0; 1216 x 4096 8.8
+// 8.5 8.4; 4096 x 4096 22.5 19.7 20.6; 4096 x 7168 44.7 37.7 35.7; 304 x 16384 - 10.2
+// 8.5; 16384 x 2048 42 38 40; 16384 x 7168 166 137 125.5.
+template <class F>
+int choose_pieces(int T, F row_threads) {
+  auto per_sm = [&](int n) { return static_cast<double>(T) * row_threads(n) / kSms; };
+  if (row_threads(1) <= kMaxRowThreads && per_sm(1) <= 1750) return 1;
+  if (row_threads(2) <= kMaxRowThreads && per_sm(2) <= (row_threads(2) <= 512 ? 4096 : 1750))
+    return 2;
+  return 4;
 }
 
 }  // namespace
@@ -194,14 +221,10 @@ extern "C" dsa_status dsa_rms_norm(
   p.pieces = N / 8;
   p.group_lanes = group / 8;
   p.scale_bytes = scale_format == DSA_SCALE_UE8M0 ? 1 : 4;
-  // Few rows: a piece a thread, for the shortest way through.  Many: four, so
-  // that the bytes in flight come from few warps.
-  int pieces = T <= 2 * kSms ? 1 : kMaxPieces;
   auto row_threads = [&](int n) { return ((p.pieces + n - 1) / n + 31) / 32 * 32; };
-  while (row_threads(pieces) > kMaxRowThreads) pieces *= 2;
+  const int pieces = choose_pieces(T, row_threads);
   const int threads = row_threads(pieces);
-  const int rows = T > 2 * kSms && threads < 256 ? 256 / threads : 1;
-  while (pieces > 1 && (pieces / 2) * threads >= p.pieces) pieces /= 2;
+  const int rows = threads < 128 && T > kSms ? 128 / threads : 1;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -211,7 +234,11 @@ extern "C" dsa_status dsa_rms_norm(
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = flags & DSA_FLAG_PDL ? 1 : 0;
-  const cudaError_t e = dtype == DSA_DTYPE_BF16 ? launch<true>(p, pieces, cfg)
-                                                : launch<false>(p, pieces, cfg);
+  cudaError_t e;
+  if (dtype == DSA_DTYPE_BF16)
+    e = residual ? launch<true, true>(p, pieces, cfg) : launch<true, false>(p, pieces, cfg);
+  else
+    e = residual ? launch<false, true>(p, pieces, cfg)
+                 : launch<false, false>(p, pieces, cfg);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_LAUNCH;
 }

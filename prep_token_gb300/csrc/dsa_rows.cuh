@@ -57,9 +57,21 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
 }
 
 template <bool BF16>
+__device__ __forceinline__ void unpack8(const uint4& v, float2 (&x)[4]) {
+  x[0] = unpack2<BF16>(v.x), x[1] = unpack2<BF16>(v.y);
+  x[2] = unpack2<BF16>(v.z), x[3] = unpack2<BF16>(v.w);
+}
+
+template <bool BF16>
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]), pack2<BF16>(x[4], x[5]),
                     pack2<BF16>(x[6], x[7]));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
+  return make_uint4(pack2<BF16>(x[0].x, x[0].y), pack2<BF16>(x[1].x, x[1].y),
+                    pack2<BF16>(x[2].x, x[2].y), pack2<BF16>(x[3].x, x[3].y));
 }
 
 // Host side: the checks that these rows' pointers and strides share.
