@@ -1228,9 +1228,10 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
 // Joins the parts of the items that a cut divides: with M the largest m of a
 // row's parts, out = sum 2^(m - M) O / sum 2^(m - M) l.  Which items those are
 // stands in meta; every CTA counts their rows and the rows are dealt out
-// evenly, one to a warp at a time, or where they are fewer than the CTAs and
-// have many parts one to a CTA, whose warps take an eighth of the parts each.  Bound: the waits
-// for meta, (m, l) and O, one behind the other.  Every sum has a fixed order.
+// evenly: four to a warp at a time where they have up to four parts, one to a warp
+// where they have more, one to a CTA, whose warps take an eighth of the parts each,
+// where they have more than eight and are fewer than the CTAs.  Bound: the waits for
+// meta, (m, l) and O, one behind the other.  Every sum has a fixed order.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinCtas = 8 * kSms;
 
@@ -1286,23 +1287,97 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     before[e + 1] = upto - rows[1];
   }
   const bool long_rows = __syncthreads_or(most > kJoinWarps);
+  const bool few_parts = !__syncthreads_or(most > 4);
+
+  // A row's part i in ml and part, of the item that starts in CTA `first`.
+  auto part_at = [&](int first, int row, int i) {
+    return (i == 0 ? 2LL * first + 1 : 2LL * (first + i)) * (QT * kRows) + row;
+  };
+  auto item_of = [&](int n) {  // the last entry with before <= n: the CTA in which the item starts
+    int first = 0;
+#pragma unroll
+    for (int o = 256; o; o >>= 1)
+      if (first + o < kMost && before[first + o] <= n) first += o;
+    return first;
+  };
+  auto out_at = [&](const int4& meta, int row) {
+    const long long token = meta.y + row / p.G;
+    const int h = meta.z * p.G + row % p.G;
+    return static_cast<uint16_t*>(p.out) + token * p.out_stride_t + h * p.out_stride_h;
+  };
+  auto lse_at = [&](const int4& meta, int row) {
+    return p.lse + (meta.y + row / p.G) * static_cast<long long>(p.Hkv * p.G) + meta.z * p.G +
+           row % p.G;
+  };
+
+  if (few_parts) {
+    // Eight lanes to a row, four rows to a warp: what counts is how many rows are
+    // on their way at once.  Where rows have more parts their loads do it: 32 x 16
+    // drafts over 8000 (two or three parts) 199 -> 189 us, 1 x 64 over 60000 (38)
+    // 107 -> 114.
+    constexpr int kV4 = D / 32;  // float4s of a row per lane, 32 values apart
+    const int l = lane & 7;
+    const int step = gridDim.x * kJoinWarps * 4;
+    for (int n0 = (blockIdx.x * kJoinWarps + warp) * 4; n0 < total; n0 += step) {
+      const int n = n0 + (lane >> 3);
+      const bool mine = n < total;
+      const int first = item_of(min(n, total - 1));
+      const int4 meta = metas[first];
+      const int row = n - before[first], parts = mine ? meta.x - first + 1 : 0;
+      const int most_parts = __reduce_max_sync(kFull, parts);
+      float top = -INFINITY;
+      for (int i = l; i < parts; i += 8) top = fmaxf(top, p.ml[part_at(first, row, i)].x);
+      __syncwarp();
+#pragma unroll
+      for (int o = 4; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      const float ref = top == -INFINITY ? 0.0f : top;
+      float4 acc[kV4];
+#pragma unroll
+      for (int j = 0; j < kV4; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float sum = 0.0f;
+#pragma unroll 2
+      for (int i = 0; i < most_parts; ++i) {
+        if (i >= parts) continue;
+        const long long at = part_at(first, row, i);
+        const float2 ml = p.ml[at];
+        const float4* const from = reinterpret_cast<const float4*>(p.part + at * D) + l;
+        float4 o[kV4];
+#pragma unroll
+        for (int j = 0; j < kV4; ++j) o[j] = from[8 * j];
+        const float f = exp2_approx(ml.x - ref);
+        sum = fmaf(f, ml.y, sum);
+#pragma unroll
+        for (int j = 0; j < kV4; ++j) {
+          acc[j].x = fmaf(f, o[j].x, acc[j].x);
+          acc[j].y = fmaf(f, o[j].y, acc[j].y);
+          acc[j].z = fmaf(f, o[j].z, acc[j].z);
+          acc[j].w = fmaf(f, o[j].w, acc[j].w);
+        }
+      }
+      if (!mine) continue;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      uint2* const to = reinterpret_cast<uint2*>(out_at(meta, row)) + l;
+#pragma unroll
+      for (int j = 0; j < kV4; ++j)
+        to[8 * j] = sum == 0.0f ? make_uint2(0, 0)
+                                : make_uint2(pack2<BF16>(acc[j].x * inv, acc[j].y * inv),
+                                             pack2<BF16>(acc[j].z * inv, acc[j].w * inv));
+      if (l == 0 && p.lse)
+        *lse_at(meta, row) = sum == 0.0f ? -INFINITY : ref * kLn2 + logf(sum);
+    }
+    return;
+  }
 
   constexpr int kV = D / 32;  // values of a row per lane
   using V = typename Vec<kV>::type;
   const bool alone = !long_rows || total > static_cast<int>(gridDim.x);  // a row to a warp
   const int step = gridDim.x * (alone ? kJoinWarps : 1);
   for (int n = alone ? blockIdx.x * kJoinWarps + warp : blockIdx.x; n < total; n += step) {
-    int first = 0;  // the last entry with before <= n: the CTA in which the item starts
-#pragma unroll
-    for (int o = 256; o; o >>= 1)
-      if (first + o < kMost && before[first + o] <= n) first += o;
+    const int first = item_of(n);
     const int4 meta = metas[first];
     const int row = n - before[first], parts = meta.x - first + 1;
-    auto at = [&](int i) {  // the row's part i in ml and part
-      return (i == 0 ? 2LL * first + 1 : 2LL * (first + i)) * (QT * kRows) + row;
-    };
     float top = -INFINITY;
-    for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.ml[at(i)].x);
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.ml[part_at(first, row, i)].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
     const float ref = top == -INFINITY ? 0.0f : top;
@@ -1310,8 +1385,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     float l = 0.0f;
 #pragma unroll 8
     for (int i = alone ? 0 : warp; i < parts; i += alone ? 1 : kJoinWarps) {
-      const float2 ml = p.ml[at(i)];
-      const V o = *reinterpret_cast<const V*>(p.part + at(i) * D + lane * kV);
+      const long long at = part_at(first, row, i);
+      const float2 ml = p.ml[at];
+      const V o = *reinterpret_cast<const V*>(p.part + at * D + lane * kV);
       const float f = exp2_approx(ml.x - ref);
       l = fmaf(f, ml.y, l);
 #pragma unroll
@@ -1334,16 +1410,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
       }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const long long token = meta.y + row / p.G;
-    const int h = meta.z * p.G + row % p.G;
-    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
-                                                token * p.out_stride_t + h * p.out_stride_h) +
-                    lane * (kV / 2);
+    uint32_t* const out = reinterpret_cast<uint32_t*>(out_at(meta, row)) + lane * (kV / 2);
 #pragma unroll
     for (int j = 0; j < kV; j += 2)
       out[j / 2] = l == 0.0f ? 0u : pack2<BF16>(acc[j] * inv, acc[j + 1] * inv);
-    if (lane == 0 && p.lse)
-      p.lse[token * (p.Hkv * p.G) + h] = l == 0.0f ? -INFINITY : ref * kLn2 + logf(l);
+    if (lane == 0 && p.lse) *lse_at(meta, row) = l == 0.0f ? -INFINITY : ref * kLn2 + logf(l);
   }
 }
 
@@ -1463,7 +1534,7 @@ struct Plan {
 };
 
 Plan make_plan(int T, int B, int Hkv, int D, int q_tokens, int max_context, int window, int sinks,
-               bool may, bool tree) {
+               bool may) {
   constexpr double kItem[2] = {3.5, 5.0}, kCut[2] = {12.0, 15.0}, kRagged = 0.05;
   const double block[2] = {D == 64 ? 1.6 : 2.6, D == 64 ? 1.1 : 1.7};
   const int most_tiles = 2LL * T < static_cast<long long>(q_tokens) * B ? 1 : 2;
@@ -1476,7 +1547,7 @@ Plan make_plan(int T, int B, int Hkv, int D, int q_tokens, int max_context, int 
     if (window) {
       const double most = static_cast<double>(window) + sinks + tile_tokens;
       keys = most < keys ? most : keys;
-    } else if (!tree) {  // a tree's rows all see up to its end
+    } else {
       const double new_tokens = static_cast<double>(T) / B;
       keys -= (new_tokens < keys ? new_tokens : keys) / 2;
       keys = keys < kKeys ? kKeys : keys;
@@ -1486,6 +1557,47 @@ Plan make_plan(int T, int B, int Hkv, int D, int q_tokens, int max_context, int 
     if (tiles == 1 || whole < best_us) best = {tiles, false}, best_us = whole;
     if (!may || tiles < most_tiles) continue;
     const double cut = items / ctas * one + (items / ctas + 1) * kItem[tiles - 1] + kCut[tiles - 1];
+    if (cut < best_us) best = {tiles, true}, best_us = cut;
+  }
+  return best;
+}
+
+// The same for trees.  Requests are many and tiles small, so that the bytes and the
+// join count:
+//   bytes   what all items read at 6.5 TB/s, below which no division gets, for
+//           contexts of three quarters of max_context on average;
+//   join    the parts' rows, 8 bytes per value at 8 TB/s;
+//   ragged  a fifth of an item, as requests' contexts differ.
+// Either number of tiles may be cut.  In us, measured:
+//                                        whole, 1 and 2 tiles; cut, 1 and 2
+//   1 x 8 over 1000, 64 on 8                  20    19    16    16
+//   64 x 16 over up to 8192, 64 on 8         231   309   207   233
+//   32 x 16 over 8000, 64 on 8               162   199   189   191
+//   64 x 5 over 4000, 32 on 4                 89   106   101   104
+//   16 x 60, window 2048, 32 on 8             54    46    72    60
+//   16 x 30 over 8000, 32 on 4               104   104   104    71
+//   24 x 32 over 1000, 16 on 16, D 64         35    42    36    47
+Plan make_tree_plan(int T, int B, int Hkv, int G, int D, int q_tokens, int max_context, int window,
+                    int sinks, bool may) {
+  constexpr double kItem[2] = {3.5, 5.0}, kCut[2] = {10.0, 10.0}, kRagged = 0.2;
+  const double block[2] = {D == 64 ? 1.6 : 2.6, D == 64 ? 1.1 : 1.7};
+  const double drafts = static_cast<double>(T) / B;
+  double keys = max_context;
+  if (window && window + sinks + drafts < keys) keys = window + sinks + drafts;
+  const double bytes = 3.0 * D * Hkv * keys * B / 6.5e6;
+  Plan best = {1, false};
+  double best_us = 0;
+  for (int tiles = 1; tiles <= 2; ++tiles) {
+    const double items = std::ceil(drafts / (tiles * q_tokens)) * B * Hkv;
+    const double ctas = 2 / tiles * kSms, one = std::ceil(keys / kKeys) * block[tiles - 1];
+    const double rounds = std::ceil(items / ctas) * (one + kItem[tiles - 1]);
+    const double whole = (rounds > bytes ? rounds : bytes) + kRagged * one;
+    if (tiles == 1 || whole < best_us) best = {tiles, false}, best_us = whole;
+    if (!may) continue;
+    const double share = items / ctas * one;
+    const double join = 8.0 * T * G * Hkv * (1 + ctas / items) * D / 8e6;
+    const double cut = (share > bytes ? share : bytes) + (items / ctas + 1) * kItem[tiles - 1] +
+                       kCut[tiles - 1] + join;
     if (cut < best_us) best = {tiles, true}, best_us = cut;
   }
   return best;
@@ -1681,7 +1793,9 @@ dsa_status attend(
   p.G = G;
   p.window = window < max_context ? window : 0;  // such a window hides nothing
   p.sinks = p.window ? (sinks < max_context ? sinks : max_context) : 0;
-  const Plan plan = make_plan(T, B, Hkv, head_dim, q_tokens, max_context, p.window, p.sinks, need > 0, TREE);
+  const Plan plan =
+      TREE ? make_tree_plan(T, B, Hkv, G, head_dim, q_tokens, max_context, p.window, p.sinks, need > 0)
+           : make_plan(T, B, Hkv, head_dim, q_tokens, max_context, p.window, p.sinks, need > 0);
   const int tiles = plan.tiles;
   p.q_tokens = q_tokens;
   p.tile_tokens = tiles * q_tokens;
