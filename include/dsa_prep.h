@@ -371,7 +371,8 @@ dsa_status dsa_rms_norm(
  * dsa_tree_attention read, and rotates q for them, in one launch.  For every
  * head's row x of q and k, in fp32:
  *   x *= gamma / sqrt(mean(x^2) + norm_eps)       (where q_gamma or k_gamma is given)
- *   RoPE on x[0:rope_dim) as in dsa_indexer_qk_prepare_store
+ *   (a, b) -> (a c - b s, b c + a s) for the pairs of x[0:rope_dim), with the
+ *     pairs and frequencies of dsa_indexer_qk_prepare_store
  * rounded once.  k and v rows go to slot out_cache_loc[t] of their caches (slot
  * s is token s % page_size of page s / page_size), q rows to q_out.
  *
@@ -646,6 +647,8 @@ dsa_status dsa_cache_compact(
  *
  *   which, drafted, n_kept  int32 [n], n <= DSA_MAX_KEEPS; every row named once.
  *   kept           int32 [n, kept_stride >= max_kept]; NULL if max_kept is 0.
+ *   workspace      dsa_cache_keep_workspace_bytes(n, max_kept) bytes, 16-byte
+ *                  aligned, contents scratch.
  * An entry of the list whose row is out of range or was named before, whose
  * drafts pass the row's length, whose length passes the table, or whose kept
  * are more than max_kept or drafted, not ascending or not among the drafts sets
@@ -656,12 +659,15 @@ dsa_status dsa_cache_compact(
 #define DSA_MAX_VIEWS 256
 #define DSA_MAX_KEEPS 1024
 
+size_t dsa_cache_keep_workspace_bytes(int32_t n, int32_t max_kept);
+
 dsa_status dsa_cache_keep(
     void* const* bases, const int64_t* shapes, int32_t n_views, int64_t num_pages,
     int32_t* page_refs, int32_t* block_table, int32_t bt_cols, int64_t bt_stride,
     int32_t* context_lens, int32_t rows, int32_t page_size, const int32_t* which,
     const int32_t* drafted, const int32_t* kept, int64_t kept_stride, int32_t max_kept,
-    const int32_t* n_kept, int32_t n, uint32_t flags, int32_t* err_flags, void* stream);
+    const int32_t* n_kept, int32_t n, uint32_t flags, void* workspace,
+    size_t workspace_bytes, int32_t* err_flags, void* stream);
 
 /* A static, NUL-terminated description of a status code. */
 const char* dsa_status_string(dsa_status status);

@@ -37,7 +37,7 @@ __all__ = [
     "dsa_cache_copy_pages", "dsa_cache_fork", "dsa_cache_free", "dsa_cache_compact",
     "dsa_cache_fork_workspace_bytes", "dsa_cache_compact_workspace_bytes",
     "dsa_rms_norm", "dsa_rms_norm_fp8", "dsa_kv_append", "prepare_kv_append",
-    "dsa_tree_attention", "prepare_tree_attention", "dsa_cache_keep", "TokenViews",
+    "dsa_tree_attention", "prepare_tree_attention", "dsa_cache_keep", "dsa_cache_keep_workspace_bytes", "TokenViews",
     "index_k_token_views",
     "library", "cache_bytes", "cache_views",
     "PreparedCall", "prepare_qk_prepare_store", "prepare_k_prepare_store",
@@ -135,8 +135,10 @@ def library() -> ctypes.CDLL:
             P, I64, I64, P, I64, I64, P, I64, I64, P, P, P, P, I64, I64, P, P, F32, P, I64, I64, P,
             P, I64, I64, I64, I64, I64, I64, I64, I32, I32, I32, I32, I32, I32, I32, I32, U32, P, P]
         lib.dsa_kv_append.restype = ctypes.c_int
+        lib.dsa_cache_keep_workspace_bytes.argtypes = [I32, I32]
+        lib.dsa_cache_keep_workspace_bytes.restype = SZ
         lib.dsa_cache_keep.argtypes = [
-            P, P, I32, I64, P, P, I32, I64, P, I32, I32, P, P, P, I64, I32, P, I32, U32, P, P]
+            P, P, I32, I64, P, P, I32, I64, P, I32, I32, P, P, P, I64, I32, P, I32, U32, P, SZ, P, P]
         lib.dsa_cache_keep.restype = ctypes.c_int
         lib.dsa_status_string.argtypes = [ctypes.c_int]
         lib.dsa_status_string.restype = ctypes.c_char_p
@@ -1120,8 +1122,12 @@ def index_k_token_views(index_k_cache: torch.Tensor, page_size: int, cache_layou
             flat[:, codes:].unflatten(1, (page_size, 4))]
 
 
+def dsa_cache_keep_workspace_bytes(n: int, max_kept: int) -> int:
+    return int(library().dsa_cache_keep_workspace_bytes(int(n), int(max_kept)))
+
+
 def dsa_cache_keep(caches, page_refs, block_table, context_lens, page_size, rows, drafted, kept,
-                   n_kept, *, err_flags=None, stream=None):
+                   n_kept, *, workspace=None, err_flags=None, stream=None):
     """Keeps the accepted ones of rows' drafted tokens (in place, two launches).
     The last drafted[i] tokens of row rows[i] are drafts, kept[i, :n_kept[i]]
     the accepted ones among them, ascending from 0.  In every cache their
@@ -1140,10 +1146,12 @@ def dsa_cache_keep(caches, page_refs, block_table, context_lens, page_size, rows
                                                  ("n_kept", n_kept))]
     if rows.shape[0] != n or drafted.shape[0] != n or n_kept.shape[0] != n:
         raise ValueError("rows, drafted, kept and n_kept differ in length")
+    lib = library()
+    keep, ws, ws_bytes = _scratch(workspace, lib.dsa_cache_keep_workspace_bytes(n, most), dev, stream)
     with _on(dev):
-        st = library().dsa_cache_keep(
+        st = lib.dsa_cache_keep(
             views._bases.buffer_info()[0], views._shapes.buffer_info()[0], len(views), num_pages,
             *pool, page_size, lists[0], lists[1], kept.data_ptr(), max(kept.stride(0), most), most,
-            lists[2], n, 0, _err_ptr(err_flags, dev), _stream(stream, dev))
+            lists[2], n, 0, ws, ws_bytes, _err_ptr(err_flags, dev), _stream(stream, dev))
     if st != 0:
         raise DsaError(st, "dsa_cache_keep")

@@ -11,8 +11,13 @@
 // A cache is described by the addresses of its entries: token t of page p at
 // base + p * page + t * token + h * head for each of its heads, `bytes` each.
 //
+// The first kernel, a CTA to a row, checks the list, writes where the entries
+// move to the workspace, and then changes the row's table and length, which
+// nobody else reads.  The second, a CTA to a row and a cache, moves: what it
+// waits for is one read of the workspace and one of the entries.
+//
 // Bound: the moved bytes where rows and layers are many, two launches and their
-// chains of dependent reads (row, list, table, entry) where they are few.
+// chains of dependent reads where they are few.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -24,16 +29,17 @@ namespace {
 
 using namespace dsa_dev;
 
-constexpr int kMaxViews = DSA_MAX_VIEWS;
 constexpr int kThreads = 128;
-constexpr int kStep = 128;  // entries whose addresses a CTA has in shared memory
-constexpr int kBatch = 4;   // entries that a thread has in flight
+constexpr int kBatch = 4;  // entries that a thread has in flight
 
+// CAP: what a launch carries for; a call of few caches takes the small one.
+template <int CAP>
 struct Views {
-  char* base[kMaxViews];
-  long long page[kMaxViews], token[kMaxViews], head[kMaxViews];  // strides in bytes
-  int heads[kMaxViews], bytes[kMaxViews];
+  char* base[CAP];
+  long long page[CAP], token[CAP], head[CAP];  // strides in bytes
+  int heads[CAP], bytes[CAP];
 };
+constexpr int kFewViews = 64;
 
 struct KeepParams {
   int* refs;
@@ -42,6 +48,8 @@ struct KeepParams {
   const int *which, *drafted, *kept, *n_kept;
   long long bt_stride, kept_stride;
   int bt_cols, rows, num_pages, page_size, n, max_kept;
+  int4* moves;  // workspace [n, max_kept]: page and token of an entry, and of its new place; page -1: none
+  int2* runs;   // workspace [n]: the moves of a row, [x, y)
   int* err;
 };
 
@@ -49,35 +57,70 @@ __device__ __forceinline__ void report(int* err, int bit) {
   if (err) atomicOr(err, bit);
 }
 
-struct Kept {
-  int row, before, count, length;  // the row's length before the drafts, and with them
-};
-
-// Entry i of the list; false if it may not be carried out.  A whole CTA calls it.
-__device__ __forceinline__ bool read_kept(const KeepParams& p, int i, Kept& k) {
-  k.row = __ldg(p.which + i);
-  const int d = __ldg(p.drafted + i);
-  k.count = __ldg(p.n_kept + i);
-  const int* list = p.kept + i * p.kept_stride;
-  bool bad = k.row < 0 || k.row >= p.rows || d < 0 || k.count < 0 || k.count > p.max_kept ||
-             k.count > d;
+// One CTA per entry of the list.
+__global__ void __launch_bounds__(kThreads) dsa_cache_keep_plan_kernel(const KeepParams p) {
+  const int i = blockIdx.x;
+  const int row = __ldg(p.which + i), d = __ldg(p.drafted + i), count = __ldg(p.n_kept + i);
+  const int* const list = p.kept + i * p.kept_stride;
+  bool bad = row < 0 || row >= p.rows || d < 0 || count < 0 || count > p.max_kept || count > d;
+  int length = 0;
   if (!bad) {
-    k.length = p.lens[k.row];
-    k.before = k.length - d;
-    bad = k.before < 0 ||
-          (static_cast<long long>(k.length) + p.page_size - 1) / p.page_size > p.bt_cols;
-    for (int j = threadIdx.x; j < k.count; j += kThreads) {
+    length = p.lens[row];
+    bad = length < d ||
+          (static_cast<long long>(length) + p.page_size - 1) / p.page_size > p.bt_cols;
+    for (int j = threadIdx.x; j < count; j += kThreads) {
       const int a = __ldg(list + j);
       bad = bad || a >= d || a <= (j > 0 ? __ldg(list + j - 1) : -1);
     }
     for (int j = threadIdx.x; j < i; j += kThreads)  // a row named before
-      bad = bad || __ldg(p.which + j) == k.row;
+      bad = bad || __ldg(p.which + j) == row;
   }
-  return !__syncthreads_or(bad);
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) {
+      report(p.err, DSA_DEVERR_ROW);
+      p.runs[i] = make_int2(0, 0);
+    }
+    return;
+  }
+  const int before = length - d;
+  int* const entry = p.table + row * p.bt_stride;
+  int still = 0;  // entries that stay, all of them in front
+  for (int j0 = 0; j0 < count; j0 += kThreads) {
+    const int j = j0 + threadIdx.x;
+    const int a = j < count ? __ldg(list + j) : -1;
+    if (j < count && a != j) {
+      const int from = before + a, to = before + j;
+      const int fp = entry[from / p.page_size], tp = entry[to / p.page_size];
+      const bool ok = fp >= 0 && fp < p.num_pages && tp >= 0 && tp < p.num_pages;
+      if (!ok) report(p.err, DSA_DEVERR_SLOT);
+      p.moves[static_cast<long long>(i) * p.max_kept + j] =
+          make_int4(ok ? fp : -1, from % p.page_size, tp, to % p.page_size);
+    }
+    still += __syncthreads_count(j < count && a == j);
+  }
+  if (threadIdx.x == 0) p.runs[i] = make_int2(still, count);
+  // the table has been read
+  const int shorter = before + count;
+  auto blocks = [&](int tokens) {
+    return static_cast<int>((static_cast<long long>(tokens) + p.page_size - 1) / p.page_size);
+  };
+  __syncthreads();
+  for (int j = blocks(shorter) + threadIdx.x; j < blocks(length); j += kThreads) {
+    const int e = entry[j];
+    if (e < 0) continue;
+    entry[j] = -1;
+    if (e >= p.num_pages) {
+      report(p.err, DSA_DEVERR_SLOT);
+    } else if (atomicSub(p.refs + e, 1) <= 0) {
+      atomicAdd(p.refs + e, 1);
+      report(p.err, DSA_DEVERR_REFS);
+    }
+  }
+  if (threadIdx.x == 0) p.lens[row] = shorter;
 }
 
-template <class V>
-__device__ __forceinline__ void move_columns(const Views& vs, int v, const longlong2* at, int n) {
+template <class V, class Vs>
+__device__ __forceinline__ void move_columns(const Vs& vs, int v, const longlong2* at, int n) {
   const int pieces = vs.bytes[v] / static_cast<int>(sizeof(V));  // of a head
   const int columns = vs.heads[v] * pieces;
   for (int c = threadIdx.x; c < columns; c += kThreads) {
@@ -96,38 +139,27 @@ __device__ __forceinline__ void move_columns(const Views& vs, int v, const longl
 }
 
 // blockIdx.x: the cache; blockIdx.y: the entry of the list.
+template <int CAP>
 __global__ void __launch_bounds__(kThreads)
-    dsa_cache_keep_kernel(const __grid_constant__ Views vs, const KeepParams p) {
-  __shared__ longlong2 at[kStep];  // from and to, in bytes; from < 0: not moved
-  const int v = blockIdx.x;
-  Kept k;
-  if (!read_kept(p, blockIdx.y, k)) return;
-  const int* list = p.kept + blockIdx.y * p.kept_stride;
-  const int* table = p.table + k.row * p.bt_stride;
-  for (int j0 = 0; j0 < k.count; j0 += kStep) {
-    const int n = min(kStep, k.count - j0);
-    __syncthreads();  // the step before is done with `at`
-    bool moves = false;
+    dsa_cache_keep_kernel(const __grid_constant__ Views<CAP> vs, const int4* moves,
+                          const int2* runs, int max_kept) {
+  __shared__ longlong2 at[kThreads];  // from and to, in bytes; from < 0: not moved
+  const int v = blockIdx.x, i = blockIdx.y;
+  const long long page = vs.page[v], token = vs.token[v];
+  const long long bits = reinterpret_cast<long long>(vs.base[v]) | page | token | vs.head[v] |
+                         vs.bytes[v];
+  moves += static_cast<long long>(i) * max_kept;
+  grid_dependency_wait();
+  const int2 run = runs[i];
+  for (int j0 = run.x; j0 < run.y; j0 += kThreads) {
+    const int n = min(kThreads, run.y - j0);
+    if (j0 > run.x) __syncthreads();  // the step before is done with `at`
     if (static_cast<int>(threadIdx.x) < n) {
-      const int j = j0 + threadIdx.x;
-      const int a = __ldg(list + j);
-      longlong2 x = make_longlong2(-1, -1);
-      if (a != j) {
-        const int from = k.before + a, to = k.before + j;
-        const int fp = table[from / p.page_size], tp = table[to / p.page_size];
-        if (fp < 0 || fp >= p.num_pages || tp < 0 || tp >= p.num_pages) {
-          report(p.err, DSA_DEVERR_SLOT);
-        } else {
-          x.x = fp * vs.page[v] + from % p.page_size * vs.token[v];
-          x.y = tp * vs.page[v] + to % p.page_size * vs.token[v];
-          moves = true;
-        }
-      }
-      at[threadIdx.x] = x;
+      const int4 m = moves[j0 + threadIdx.x];
+      at[threadIdx.x] = m.x < 0 ? make_longlong2(-1, -1)
+                                : make_longlong2(m.x * page + m.y * token, m.z * page + m.w * token);
     }
-    if (!__syncthreads_or(moves)) continue;
-    const long long bits = reinterpret_cast<long long>(vs.base[v]) | vs.page[v] | vs.token[v] |
-                           vs.head[v] | vs.bytes[v];
+    __syncthreads();
     if ((bits & 15) == 0)
       move_columns<uint4>(vs, v, at, n);
     else
@@ -135,45 +167,15 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// One CTA per entry of the list: the row's length, and its pages behind that.
-__global__ void __launch_bounds__(kThreads) dsa_cache_keep_tables_kernel(const KeepParams p) {
-  grid_dependency_wait();
-  Kept k;
-  if (!read_kept(p, blockIdx.x, k)) {
-    if (threadIdx.x == 0) report(p.err, DSA_DEVERR_ROW);
-    return;
-  }
-  const int length = k.before + k.count;
-  auto blocks = [&](int tokens) {
-    return static_cast<int>((static_cast<long long>(tokens) + p.page_size - 1) / p.page_size);
-  };
-  int* entry = p.table + k.row * p.bt_stride;
-  for (int j = blocks(length) + threadIdx.x; j < blocks(k.length); j += kThreads) {
-    const int e = entry[j];
-    if (e < 0) continue;
-    entry[j] = -1;
-    if (e >= p.num_pages) {
-      report(p.err, DSA_DEVERR_SLOT);
-    } else if (atomicSub(p.refs + e, 1) <= 0) {
-      atomicAdd(p.refs + e, 1);
-      report(p.err, DSA_DEVERR_REFS);
-    }
-  }
-  if (threadIdx.x == 0) p.lens[k.row] = length;  // read by all before read_kept's barrier
-}
-
 bool misaligned(const void* ptr, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) != 0;
 }
 
-// views[i] as page, token and head stride, heads and bytes; strides of one entry
-// are never used and become 0.
+// shapes[5 i ..]: page, token and head stride, heads and bytes; strides of one
+// entry are never used and become 0.
+template <int CAP>
 dsa_status read_views(void* const* bases, const int64_t* shapes, int32_t n_views,
-                      int64_t num_pages, int32_t page_size, Views* out) {
-  if (n_views < 0 || n_views > kMaxViews || num_pages < 1 || num_pages > 0x7fffffffLL ||
-      page_size < 1)
-    return DSA_ERR_SHAPE;
-  if (n_views > 0 && (!bases || !shapes)) return DSA_ERR_NULL;
+                      int64_t num_pages, int32_t page_size, Views<CAP>* out) {
   for (int i = 0; i < n_views; ++i) {
     const int64_t* s = shapes + 5 * i;
     if (!bases[i]) return DSA_ERR_NULL;
@@ -198,30 +200,75 @@ dsa_status read_views(void* const* bases, const int64_t* shapes, int32_t n_views
   return DSA_OK;
 }
 
+// The runs in front, 16 bytes aligned behind them the moves.
+size_t runs_bytes(int32_t n) { return (static_cast<size_t>(n) * sizeof(int2) + 15) / 16 * 16; }
+
+template <int CAP>
+dsa_status keep(void* const* bases, const int64_t* shapes, int32_t n_views, int64_t num_pages,
+                KeepParams p, bool checked, cudaStream_t s) {
+  Views<CAP> vs;
+  const dsa_status st = read_views<CAP>(bases, shapes, n_views, num_pages, p.page_size, &vs);
+  if (st != DSA_OK || checked) return st;
+  dsa_cache_keep_plan_kernel<<<static_cast<unsigned>(p.n), kThreads, 0, s>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return DSA_ERR_LAUNCH;
+  if (n_views == 0 || p.max_kept == 0) return DSA_OK;
+  // waits for the first one's memory before it reads anything
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(n_views), static_cast<unsigned>(p.n));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, dsa_cache_keep_kernel<CAP>, vs,
+                                           static_cast<const int4*>(p.moves),
+                                           static_cast<const int2*>(p.runs), p.max_kept);
+  return e == cudaSuccess ? DSA_OK : DSA_ERR_LAUNCH;
+}
+
 }  // namespace
 
-extern "C" dsa_status dsa_cache_keep(
+extern "C" {
+
+size_t dsa_cache_keep_workspace_bytes(int32_t n, int32_t max_kept) {
+  if (n < 1 || max_kept < 0) return 0;
+  return runs_bytes(n) + static_cast<size_t>(n) * max_kept * sizeof(int4);
+}
+
+dsa_status dsa_cache_keep(
     void* const* bases, const int64_t* shapes, int32_t n_views, int64_t num_pages,
     int32_t* page_refs, int32_t* block_table, int32_t bt_cols, int64_t bt_stride,
     int32_t* context_lens, int32_t rows, int32_t page_size, const int32_t* which,
     const int32_t* drafted, const int32_t* kept, int64_t kept_stride, int32_t max_kept,
-    const int32_t* n_kept, int32_t n, uint32_t flags, int32_t* err_flags, void* stream) {
-  Views vs;
-  const dsa_status st = read_views(bases, shapes, n_views, num_pages, page_size, &vs);
-  if (st != DSA_OK) return st;
+    const int32_t* n_kept, int32_t n, uint32_t flags, void* workspace, size_t workspace_bytes,
+    int32_t* err_flags, void* stream) {
+  if (n_views < 0 || n_views > DSA_MAX_VIEWS || num_pages < 1 || num_pages > 0x7fffffffLL ||
+      page_size < 1)
+    return DSA_ERR_SHAPE;
+  if (n_views > 0 && (!bases || !shapes)) return DSA_ERR_NULL;
+  KeepParams p = {};
+  p.page_size = page_size;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto call = [&](bool checked) {
+    return n_views <= kFewViews
+               ? keep<kFewViews>(bases, shapes, n_views, num_pages, p, checked, s)
+               : keep<DSA_MAX_VIEWS>(bases, shapes, n_views, num_pages, p, checked, s);
+  };
   if (n < 0 || n > DSA_MAX_KEEPS || max_kept < 0 || kept_stride < max_kept || rows < 0 ||
       bt_cols < 0 || bt_stride < bt_cols)
     return DSA_ERR_SHAPE;
   if (flags) return DSA_ERR_UNSUPPORTED;
-  if (n == 0) return DSA_OK;
+  if (n == 0) return call(true);
   if (!page_refs || !block_table || !context_lens || !which || !drafted || !n_kept ||
-      (!kept && max_kept > 0))
+      (!kept && max_kept > 0) || !workspace)
     return DSA_ERR_NULL;
   if (misaligned(page_refs, 4) || misaligned(block_table, 4) || misaligned(context_lens, 4) ||
       misaligned(which, 4) || misaligned(drafted, 4) || misaligned(kept, 4) ||
-      misaligned(n_kept, 4) || misaligned(err_flags, 4))
+      misaligned(n_kept, 4) || misaligned(workspace, 16) || misaligned(err_flags, 4))
     return DSA_ERR_ALIGN;
-  KeepParams p = {};
+  if (workspace_bytes < dsa_cache_keep_workspace_bytes(n, max_kept)) return DSA_ERR_SHAPE;
   p.refs = page_refs;
   p.table = block_table;
   p.lens = context_lens;
@@ -234,26 +281,12 @@ extern "C" dsa_status dsa_cache_keep(
   p.bt_cols = bt_cols;
   p.rows = rows;
   p.num_pages = static_cast<int>(num_pages);
-  p.page_size = page_size;
   p.n = n;
   p.max_kept = max_kept;
+  p.runs = static_cast<int2*>(workspace);
+  p.moves = reinterpret_cast<int4*>(static_cast<char*>(workspace) + runs_bytes(n));
   p.err = err_flags;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (n_views > 0 && max_kept > 0) {
-    const dim3 grid(static_cast<unsigned>(n_views), static_cast<unsigned>(n));
-    dsa_cache_keep_kernel<<<grid, kThreads, 0, s>>>(vs, p);
-    if (cudaGetLastError() != cudaSuccess) return DSA_ERR_LAUNCH;
-  }
-  // the tables change only once every entry has moved
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(n));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = n_views > 0 && max_kept > 0 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, dsa_cache_keep_tables_kernel, p) == cudaSuccess ? DSA_OK
-                                                                                  : DSA_ERR_LAUNCH;
+  return call(false);
 }
+
+}  // extern "C"

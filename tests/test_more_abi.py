@@ -96,13 +96,13 @@ def test_tree(lib, over, status):
 
 def _keep(lib, bases=(A,), shapes=((4096, 256, 128, 2, 128),), n_views=None, pages=8, refs=A, bt=A,
           cols=4, stride=4, lens=A, rows=3, ps=16, which=A, drafted=A, kept=A, ks=8, most=8, nk=A,
-          n=2, flags=0, err=None, null=False):
+          n=2, flags=0, ws=A, wsb=272, err=None, null=False):
     b = (ctypes.c_void_p * max(1, len(bases)))(*bases)
     flat = [x for s in shapes for x in s]
     s = (ctypes.c_int64 * max(1, len(flat)))(*flat)
     return lib.dsa_cache_keep(None if null else b, s, len(bases) if n_views is None else n_views,
                               pages, refs, bt, cols, stride, lens, rows, ps, which, drafted, kept, ks,
-                              most, nk, n, flags, err, None)
+                              most, nk, n, flags, ws, wsb, err, None)
 
 
 @pytest.mark.parametrize("over,status", [
@@ -118,7 +118,8 @@ def _keep(lib, bases=(A,), shapes=((4096, 256, 128, 2, 128),), n_views=None, pag
     (dict(lens=None), 1), (dict(which=None), 1), (dict(drafted=None), 1), (dict(kept=None), 1),
     (dict(nk=None), 1), (dict(refs=A + 2), 2), (dict(bt=A + 2), 2), (dict(lens=A + 2), 2),
     (dict(which=A + 1), 2), (dict(drafted=A + 2), 2), (dict(kept=A + 2), 2), (dict(nk=A + 2), 2),
-    (dict(err=A + 2), 2), (dict(n=0, refs=None, kept=None), 0)])
+    (dict(err=A + 2), 2), (dict(ws=None), 1), (dict(ws=A + 8), 2), (dict(wsb=271), 3),
+    (dict(n=0, refs=None, kept=None), 0)])
 def test_keep(lib, over, status):
     assert _keep(lib, **over) == status
 
