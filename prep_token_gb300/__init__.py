@@ -144,8 +144,33 @@ def library() -> ctypes.CDLL:
         lib.dsa_status_string.restype = ctypes.c_char_p
         lib.dsa_prep_version.argtypes = []
         lib.dsa_prep_version.restype = ctypes.c_int32
+        _bind(lib)
         _lib = lib
     return _lib
+
+
+_usual = None  # the module of _marshal, once the library is loaded
+
+
+def _bind(lib):
+    """Loads the calls' marshalling in C++ and hands it their entry points."""
+    global _usual
+    from . import _binding
+    _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.dsa_rms_norm, lib.dsa_kv_append, lib.dsa_tree_attention,
+        lib.dsa_paged_attention_workspace_bytes, lib.dsa_cache_keep,
+        lib.dsa_cache_keep_workspace_bytes)))
+    _usual = _binding
+
+
+def _marshal():
+    """The marshalling in C++ of calls in their usual form (outputs allocated, the
+    current stream and device).  Its functions return NotImplemented for any
+    other call, which then takes the way through ctypes, and a status that is not
+    DSA_OK as an int."""
+    if _usual is None:
+        library()
+    return _usual
 
 
 def dsa_status_string(status: int) -> str:
@@ -564,6 +589,7 @@ def dsa_indexer_mqa_logits(q_fp8, weights, index_k_cache, page_size, block_table
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 _16BIT = (torch.bfloat16, torch.float16)
+_USUAL_SCALES = (torch.float32, torch.float8_e8m0fnu)
 _SCALES = {torch.float32: 0, torch.float8_e8m0fnu: 1, torch.uint8: 1}
 
 
@@ -614,6 +640,12 @@ def dsa_rms_norm(x, gamma, eps, *, residual=None, residual_out=None, out=None, p
     fp16 (N a multiple of 8, rows of any stride), gamma [N] fp32.  Returns out,
     or (out, residual_out) with residual_out = z rounded once if a residual is
     given; residual_out may be the residual, out may be x."""
+    if stream is None and out is None and residual_out is None:
+        got = _marshal().rms_norm(x, gamma, eps, residual, 0, False, pdl)
+        if got is not NotImplemented:
+            if type(got) is int:
+                raise DsaError(got, "dsa_rms_norm")
+            return got
     _need(x, "x", _16BIT, 2)
     out = _row_output(out, "out", *x.shape, x.dtype, x.device, stream)
     z = _rms_norm(x, gamma, eps, residual, residual_out, out, None, None, 0, 128, pdl, stream)
@@ -627,6 +659,14 @@ def dsa_rms_norm_fp8(x, gamma, eps, *, residual=None, group=128, scale_dtype=tor
     as ``scale_dtype``: torch.float32, or torch.float8_e8m0fnu (torch.uint8:
     the same bytes).  ``out`` takes the 16-bit output too.  Returns (codes,
     scales), and residual_out behind them if a residual is given."""
+    if stream is None and out is None and codes is None and scales is None \
+            and residual_out is None and group and scale_dtype in _USUAL_SCALES:
+        got = _marshal().rms_norm(x, gamma, eps, residual, group,
+                                  scale_dtype is torch.float8_e8m0fnu, pdl)
+        if got is not NotImplemented:
+            if type(got) is int:
+                raise DsaError(got, "dsa_rms_norm")
+            return got
     _need(x, "x", _16BIT, 2)
     if group not in (32, 128):
         raise ValueError("group must be 32 or 128")
@@ -723,6 +763,14 @@ def dsa_kv_append(q, k, v, positions, out_cache_loc, cos_cache, sin_cache, k_cac
     slot out_cache_loc[t].  ``q_gamma``, ``k_gamma`` [D] fp32: an RMS norm of
     every head of q or k (with ``eps``) before the rotation.  Returns the rotated
     q [T, H, D] (``q_out``, which may be q itself)."""
+    if stream is None and q_out is None and num_tokens is None and max_position is None:
+        got = _marshal().kv_append(k, v, k_cache, v_cache, positions, out_cache_loc, q, cos_cache,
+                                   sin_cache, rope_dim, rope_style, q_gamma, k_gamma, eps,
+                                   err_flags, pdl)
+        if got is not NotImplemented:
+            if type(got) is int:
+                raise DsaError(got, "dsa_kv_append")
+            return got
     args, q_out = _append_args(q, k, v, positions, out_cache_loc, cos_cache, sin_cache, k_cache,
                                v_cache, rope_dim, rope_style, q_gamma, k_gamma, eps, q_out,
                                num_tokens, max_position, err_flags, pdl, stream)
@@ -888,6 +936,13 @@ def dsa_tree_attention(q, k_cache, v_cache, block_table, query_start, context_le
     drafts a row sees all or, with a ``window``, those within it of the row's
     position in the tree (as many behind the last of them as it sees drafts) and
     the first ``sinks``.  Everything else is as in dsa_paged_attention."""
+    if stream is None and out is None and lse is None and workspace is None:
+        got = _marshal().tree_attention(q, k_cache, v_cache, block_table, query_start, context_lens,
+                                        max_context, tree_mask, scale, window, sinks, err_flags, pdl)
+        if got is not NotImplemented:
+            if type(got) is int:
+                raise DsaError(got, "dsa_tree_attention")
+            return got
     args, out, lse, workspace = _tree_args(
         q, k_cache, v_cache, block_table, query_start, context_lens, max_context, tree_mask, scale,
         window, sinks, out, lse, workspace, err_flags, pdl, stream)
@@ -1104,6 +1159,9 @@ class TokenViews:
             shapes += [strides[0], strides[1], strides[2] if heads > 1 else 0, heads, width]
         self._bases = array.array("Q", [t.data_ptr() for t in self.caches])
         self._shapes = array.array("q", shapes)
+        self._where = (self._bases.buffer_info()[0], self._shapes.buffer_info()[0],
+                       len(self.caches), *(self.pages or (0, 0)),
+                       self.device.index if self.caches else -1)
 
     def __len__(self):
         return len(self.caches)
@@ -1135,8 +1193,15 @@ def dsa_cache_keep(caches, page_refs, block_table, context_lens, page_size, rows
     table shrink to them, and the pages behind go back to the pool.  caches: a
     TokenViews, or a list of tensors for one; rows, drafted, n_kept [n] int32,
     kept [n, most] int32."""
-    dev, num_pages, pool = _pool(page_refs, block_table, context_lens)
     views = caches if isinstance(caches, TokenViews) else TokenViews(caches)
+    if stream is None and workspace is None:
+        got = _marshal().cache_keep(*views._where, page_refs, block_table, context_lens, page_size,
+                                    rows, drafted, kept, n_kept, err_flags)
+        if got is not NotImplemented:
+            if got:
+                raise DsaError(got, "dsa_cache_keep")
+            return
+    dev, num_pages, pool = _pool(page_refs, block_table, context_lens)
     page_size = int(page_size)
     if views.caches and (views.pages != (num_pages, page_size) or views.device != dev):
         raise ValueError(f"caches must be [{num_pages}, {page_size}, ...] on {dev}")

@@ -1,14 +1,18 @@
 """Builds libdsaprep.so in-tree with nvcc for sm_103a (no torch extension
-machinery: the library is plain C ABI over CUDA)."""
+machinery: the library is plain C ABI over CUDA), and beside it _binding.so, the
+marshalling in C++ of the calls that a decode step makes eagerly."""
 from __future__ import annotations
 
 import glob
 import os
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB_PATH = os.path.join(PKG, "libdsaprep.so")
+BINDING_PATH = os.path.join(PKG, "_binding.so")
+BINDING_SOURCE = os.path.join(PKG, "csrc", "binding.cpp")
 INCLUDE = os.path.join(ROOT, "include")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
@@ -28,21 +32,54 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(PKG, "csrc", "*.cu")))
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+def _older(path: str, deps: list[str]) -> bool:
+    if not os.path.exists(path):
         return True
-    deps = sources() + glob.glob(os.path.join(PKG, "csrc", "*.cuh")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h"))
-    t = os.path.getmtime(LIB_PATH)
+    t = os.path.getmtime(path)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _headers() -> list[str]:
+    return glob.glob(os.path.join(INCLUDE, "*.h"))
+
+
+def _stale() -> bool:
+    return _older(LIB_PATH, sources() + glob.glob(os.path.join(PKG, "csrc", "*.cuh")) + _headers())
+
+
+def _binding_command(out: str) -> list[str]:
+    import torch
+    at = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    return ["g++", "-O1", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
+            "-I", os.path.join(at, "include"),
+            "-I", os.path.join(at, "include", "torch", "csrc", "api", "include"),
+            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-o", out, BINDING_SOURCE, "-L", os.path.join(at, "lib"),
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
     """Compile every .cu under csrc/ (in parallel, one nvcc per file) and
-    link them into one shared library."""
-    if not force and not _stale():
-        return LIB_PATH
+    link them into one shared library, and the binding beside them."""
     tag = f"{os.getpid()}"
+    binding = None
+    if force or _older(BINDING_PATH, [BINDING_SOURCE] + _headers()):
+        binding = subprocess.Popen(_binding_command(BINDING_PATH + f".tmp{tag}"))
+    try:
+        if force or _stale():
+            _build_cuda(tag, verbose)
+    finally:
+        code = binding.wait() if binding else 0
+    if code:
+        raise subprocess.CalledProcessError(code, "g++ binding.cpp")
+    if binding:
+        os.replace(BINDING_PATH + f".tmp{tag}", BINDING_PATH)
+    return LIB_PATH
+
+
+def _build_cuda(tag: str, verbose: bool) -> None:
     objs, procs = [], []
     compile_flags = [f for f in NVCC_FLAGS if f not in ("-shared",)]
     for src in sources():
@@ -63,4 +100,3 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         for obj in objs:
             if os.path.exists(obj):
                 os.remove(obj)
-    return LIB_PATH
