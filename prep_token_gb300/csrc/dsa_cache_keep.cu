@@ -32,12 +32,15 @@ using namespace dsa_dev;
 constexpr int kThreads = 128;
 constexpr int kBatch = 4;  // entries that a thread has in flight
 
+struct View {
+  char* base;
+  long long page, token, head;  // strides in bytes
+  int heads, bytes;
+};
 // CAP: what a launch carries for; a call of few caches takes the small one.
 template <int CAP>
 struct Views {
-  char* base[CAP];
-  long long page[CAP], token[CAP], head[CAP];  // strides in bytes
-  int heads[CAP], bytes[CAP];
+  View v[CAP];
 };
 constexpr int kFewViews = 64;
 
@@ -49,7 +52,7 @@ struct KeepParams {
   long long bt_stride, kept_stride;
   int bt_cols, rows, num_pages, page_size, n, max_kept;
   int4* moves;  // workspace [n, max_kept]: page and token of an entry, and of its new place; page -1: none
-  int2* runs;   // workspace [n]: the moves of a row, [x, y)
+  int* runs;    // workspace [n]: how many moves a row has
   int* err;
 };
 
@@ -60,6 +63,7 @@ __device__ __forceinline__ void report(int* err, int bit) {
 // One CTA per entry of the list.
 __global__ void __launch_bounds__(kThreads) dsa_cache_keep_plan_kernel(const KeepParams p) {
   const int i = blockIdx.x;
+  grid_launch_dependents();  // the second kernel's CTAs start, and wait for this one's end
   const int row = __ldg(p.which + i), d = __ldg(p.drafted + i), count = __ldg(p.n_kept + i);
   const int* const list = p.kept + i * p.kept_stride;
   bool bad = row < 0 || row >= p.rows || d < 0 || count < 0 || count > p.max_kept || count > d;
@@ -78,27 +82,27 @@ __global__ void __launch_bounds__(kThreads) dsa_cache_keep_plan_kernel(const Kee
   if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0) {
       report(p.err, DSA_DEVERR_ROW);
-      p.runs[i] = make_int2(0, 0);
+      p.runs[i] = 0;
     }
     return;
   }
   const int before = length - d;
   int* const entry = p.table + row * p.bt_stride;
   int still = 0;  // entries that stay, all of them in front
+  int4* const moves = p.moves + static_cast<long long>(i) * p.max_kept;
   for (int j0 = 0; j0 < count; j0 += kThreads) {
     const int j = j0 + threadIdx.x;
     const int a = j < count ? __ldg(list + j) : -1;
+    still += __syncthreads_count(j < count && a == j);
     if (j < count && a != j) {
       const int from = before + a, to = before + j;
       const int fp = entry[from / p.page_size], tp = entry[to / p.page_size];
       const bool ok = fp >= 0 && fp < p.num_pages && tp >= 0 && tp < p.num_pages;
       if (!ok) report(p.err, DSA_DEVERR_SLOT);
-      p.moves[static_cast<long long>(i) * p.max_kept + j] =
-          make_int4(ok ? fp : -1, from % p.page_size, tp, to % p.page_size);
+      moves[j - still] = make_int4(ok ? fp : -1, from % p.page_size, tp, to % p.page_size);
     }
-    still += __syncthreads_count(j < count && a == j);
   }
-  if (threadIdx.x == 0) p.runs[i] = make_int2(still, count);
+  if (threadIdx.x == 0) p.runs[i] = count - still;
   // the table has been read
   const int shorter = before + count;
   auto blocks = [&](int tokens) {
@@ -119,13 +123,13 @@ __global__ void __launch_bounds__(kThreads) dsa_cache_keep_plan_kernel(const Kee
   if (threadIdx.x == 0) p.lens[row] = shorter;
 }
 
-template <class V, class Vs>
-__device__ __forceinline__ void move_columns(const Vs& vs, int v, const longlong2* at, int n) {
-  const int pieces = vs.bytes[v] / static_cast<int>(sizeof(V));  // of a head
-  const int columns = vs.heads[v] * pieces;
+template <class V>
+__device__ __forceinline__ void move_columns(const View& view, const longlong2* at, int n) {
+  const int pieces = view.bytes / static_cast<int>(sizeof(V));  // of a head
+  const int columns = view.heads * pieces;
   for (int c = threadIdx.x; c < columns; c += kThreads) {
     const int h = c / pieces;
-    char* const base = vs.base[v] + h * vs.head[v] + (c - h * pieces) * sizeof(V);
+    char* const base = view.base + h * view.head + (c - h * pieces) * sizeof(V);
     for (int j = 0; j < n; j += kBatch) {
       V x[kBatch];
 #pragma unroll
@@ -138,32 +142,35 @@ __device__ __forceinline__ void move_columns(const Vs& vs, int v, const longlong
   }
 }
 
-// blockIdx.x: the cache; blockIdx.y: the entry of the list.
+// blockIdx.x: the cache; blockIdx.y: the entry of the list.  The first moves are
+// read beside their number.
 template <int CAP>
 __global__ void __launch_bounds__(kThreads)
     dsa_cache_keep_kernel(const __grid_constant__ Views<CAP> vs, const int4* moves,
-                          const int2* runs, int max_kept) {
+                          const int* runs, int max_kept) {
   __shared__ longlong2 at[kThreads];  // from and to, in bytes; from < 0: not moved
-  const int v = blockIdx.x, i = blockIdx.y;
-  const long long page = vs.page[v], token = vs.token[v];
-  const long long bits = reinterpret_cast<long long>(vs.base[v]) | page | token | vs.head[v] |
-                         vs.bytes[v];
+  const View view = vs.v[blockIdx.x];
+  const int i = blockIdx.y;
+  const long long bits = reinterpret_cast<long long>(view.base) | view.page | view.token |
+                         view.head | view.bytes;
   moves += static_cast<long long>(i) * max_kept;
   grid_dependency_wait();
-  const int2 run = runs[i];
-  for (int j0 = run.x; j0 < run.y; j0 += kThreads) {
-    const int n = min(kThreads, run.y - j0);
-    if (j0 > run.x) __syncthreads();  // the step before is done with `at`
-    if (static_cast<int>(threadIdx.x) < n) {
-      const int4 m = moves[j0 + threadIdx.x];
-      at[threadIdx.x] = m.x < 0 ? make_longlong2(-1, -1)
-                                : make_longlong2(m.x * page + m.y * token, m.z * page + m.w * token);
+  const int n = runs[i];
+  for (int j0 = 0; j0 == 0 || j0 < n; j0 += kThreads) {
+    if (j0 > 0) __syncthreads();  // the step before is done with `at`
+    const int j = j0 + threadIdx.x;
+    if (j < max_kept) {
+      const int4 m = moves[j];
+      at[threadIdx.x] =
+          m.x < 0 ? make_longlong2(-1, -1)
+                  : make_longlong2(m.x * view.page + m.y * view.token,
+                                   m.z * view.page + m.w * view.token);
     }
     __syncthreads();
     if ((bits & 15) == 0)
-      move_columns<uint4>(vs, v, at, n);
+      move_columns<uint4>(view, at, min(kThreads, n - j0));
     else
-      move_columns<uint32_t>(vs, v, at, n);
+      move_columns<uint32_t>(view, at, min(kThreads, n - j0));
   }
 }
 
@@ -190,18 +197,14 @@ dsa_status read_views(void* const* bases, const int64_t* shapes, int32_t n_views
       if (stride[d] % 4) return DSA_ERR_ALIGN;
     }
     if (misaligned(bases[i], 4) || s[4] % 4) return DSA_ERR_ALIGN;
-    out->base[i] = static_cast<char*>(bases[i]);
-    out->page[i] = stride[0];
-    out->token[i] = stride[1];
-    out->head[i] = stride[2];
-    out->heads[i] = static_cast<int>(s[3]);
-    out->bytes[i] = static_cast<int>(s[4]);
+    out->v[i] = {static_cast<char*>(bases[i]), stride[0], stride[1], stride[2],
+                 static_cast<int>(s[3]), static_cast<int>(s[4])};
   }
   return DSA_OK;
 }
 
 // The runs in front, 16 bytes aligned behind them the moves.
-size_t runs_bytes(int32_t n) { return (static_cast<size_t>(n) * sizeof(int2) + 15) / 16 * 16; }
+size_t runs_bytes(int32_t n) { return (static_cast<size_t>(n) * sizeof(int) + 15) / 16 * 16; }
 
 template <int CAP>
 dsa_status keep(void* const* bases, const int64_t* shapes, int32_t n_views, int64_t num_pages,
@@ -224,7 +227,7 @@ dsa_status keep(void* const* bases, const int64_t* shapes, int32_t n_views, int6
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, dsa_cache_keep_kernel<CAP>, vs,
                                            static_cast<const int4*>(p.moves),
-                                           static_cast<const int2*>(p.runs), p.max_kept);
+                                           static_cast<const int*>(p.runs), p.max_kept);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_LAUNCH;
 }
 
@@ -283,7 +286,7 @@ dsa_status dsa_cache_keep(
   p.num_pages = static_cast<int>(num_pages);
   p.n = n;
   p.max_kept = max_kept;
-  p.runs = static_cast<int2*>(workspace);
+  p.runs = static_cast<int*>(workspace);
   p.moves = reinterpret_cast<int4*>(static_cast<char*>(workspace) + runs_bytes(n));
   p.err = err_flags;
   return call(false);
