@@ -63,6 +63,7 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "dsa_common.cuh"
 #include "dsa_prep.h"
@@ -362,18 +363,16 @@ __device__ __noinline__ long long divide(long long a, long long b) {
 
 // Key blocks of all tiles of a sequence, for one kv head.  A whole warp calls
 // it with each lane's own sequence.
-template <bool TREE>
 __device__ __noinline__ long long seq_blocks(const AParams& p, int n, int ctx, int tiles) {
   const int lane = threadIdx.x & 31;
-  long long mine = tiles > 0 ? make_tile<TREE>(p, 0, n, ctx, 0).blocks : 0;
-  if (TREE) mine *= tiles;  // which all see the same keys
-  for (unsigned todo = TREE ? 0 : __ballot_sync(kFull, tiles > 1); todo; todo &= todo - 1) {
+  long long mine = tiles > 0 ? make_tile<false>(p, 0, n, ctx, 0).blocks : 0;
+  for (unsigned todo = __ballot_sync(kFull, tiles > 1); todo; todo &= todo - 1) {
     const int src = __ffs(todo) - 1;
     const int n1 = __shfl_sync(kFull, n, src), ctx1 = __shfl_sync(kFull, ctx, src);
     const int tiles1 = __shfl_sync(kFull, tiles, src);
     long long sum = 0;
 #pragma unroll 1
-    for (int t = lane; t < tiles1; t += 32) sum += make_tile<TREE>(p, 0, n1, ctx1, t).blocks;
+    for (int t = lane; t < tiles1; t += 32) sum += make_tile<false>(p, 0, n1, ctx1, t).blocks;
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
     if (lane == src) mine = sum;
@@ -398,7 +397,6 @@ struct Share {
 };
 
 // A whole warp calls it.
-template <bool TREE>
 __device__ __forceinline__ Share my_share(const AParams& p) {
   const int lane = threadIdx.x & 31;
   long long total = 0;
@@ -406,7 +404,7 @@ __device__ __forceinline__ Share my_share(const AParams& p) {
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     Seq s = {0, 0, 0, 0};
     if (b0 + lane < p.B) s = load_seq(p, b0 + lane);
-    total += seq_blocks<TREE>(p, s.n, s.ctx, s.tiles);
+    total += seq_blocks(p, s.n, s.ctx, s.tiles);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
@@ -446,7 +444,6 @@ __device__ __forceinline__ void take_tile(const AParams& p, Cursor& c, int begin
 
 // Puts the cursor at key block `want` (split; `budget` of them are taken) or at
 // item `want`.  A whole warp calls it; every lane gets the same.
-template <bool TREE>
 __device__ __forceinline__ bool seek(const AParams& p, Cursor& c, long long want, long long budget) {
   const int lane = threadIdx.x & 31;
   long long before = 0;
@@ -454,7 +451,7 @@ __device__ __forceinline__ bool seek(const AParams& p, Cursor& c, long long want
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     Seq s = {0, 0, 0, 0};
     if (b0 + lane < p.B) s = load_seq(p, b0 + lane);
-    const long long per_head = p.split ? seq_blocks<TREE>(p, s.n, s.ctx, s.tiles) : s.tiles;
+    const long long per_head = p.split ? seq_blocks(p, s.n, s.ctx, s.tiles) : s.tiles;
     const long long upto = before + warp_inclusive(per_head * p.Hkv);
     const unsigned past = __ballot_sync(kFull, upto > want);
     if (past) {
@@ -474,7 +471,7 @@ __device__ __forceinline__ bool seek(const AParams& p, Cursor& c, long long want
 #pragma unroll 1
         for (int t0 = 0;; t0 += 32) {
           const int t = t0 + lane;
-          const int n = t < c.s.tiles ? make_tile<TREE>(p, 0, c.s.n, c.s.ctx, t).blocks : 0;
+          const int n = t < c.s.tiles ? make_tile<false>(p, 0, c.s.n, c.s.ctx, t).blocks : 0;
           const int up = seen + static_cast<int>(warp_inclusive(n));
           const unsigned over = __ballot_sync(kFull, up > r);
           if (over) {
@@ -486,12 +483,96 @@ __device__ __forceinline__ bool seek(const AParams& p, Cursor& c, long long want
           seen = __shfl_sync(kFull, up, 31);
         }
       }
-      take_tile<TREE>(p, c, p.split ? r : 0, budget);
+      take_tile<false>(p, c, p.split ? r : 0, budget);
       return true;
     }
     before = __shfl_sync(kFull, upto, 31);
   }
   return false;
+}
+
+// The work of trees: as all tiles of a sequence see the same keys, a sequence's
+// key blocks (or items) are a product, and a place in them three divisions.  Their
+// sum passes no 32 bits (attend takes whole items else), and one scan of the
+// sequences serves both the share and the place: what a call of few blocks waits
+// for first.  Lane l holds sequence base + l.
+struct TreeWork {
+  Seq s;
+  unsigned blocks;  // of a tile; 1 where items are counted
+  unsigned weight, upto;
+  int base;
+};
+
+// The sequences from `base` on, `before` having come so far.  A whole warp calls it.
+__device__ __forceinline__ void load_trees(const AParams& p, TreeWork& w, int base, unsigned before) {
+  const int lane = threadIdx.x & 31;
+  w.base = base;
+  w.s = Seq{0, 0, 0, 0};
+  if (base + lane < p.B) w.s = load_seq(p, base + lane);
+  w.blocks = p.split ? make_tile<true>(p, 0, w.s.n, w.s.ctx, 0).blocks : 1;
+  w.weight = w.blocks * static_cast<unsigned>(w.s.tiles * p.Hkv);
+  w.upto = w.weight;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned y = __shfl_up_sync(kFull, w.upto, o);
+    if (lane >= o) w.upto += y;
+  }
+  w.upto += before;
+}
+
+// The CTA's share of all trees' key blocks, [begin, end); `w` is left at the first ones.
+struct TreeShare {
+  unsigned each, extra, begin, end;
+};
+
+__device__ __forceinline__ TreeShare share_trees(const AParams& p, TreeWork& w) {
+  load_trees(p, w, 0, 0);
+  unsigned total = __shfl_sync(kFull, w.upto, 31);
+  if (p.B > 32) {
+#pragma unroll 1
+    for (int base = 32; base < p.B; base += 32) {
+      load_trees(p, w, base, total);
+      total = __shfl_sync(kFull, w.upto, 31);
+    }
+    load_trees(p, w, 0, 0);
+  }
+  TreeShare r;
+  r.each = total / gridDim.x;
+  r.extra = total - r.each * gridDim.x;
+  r.begin = blockIdx.x * r.each + min(blockIdx.x, r.extra);
+  r.end = r.begin + r.each + (blockIdx.x < r.extra ? 1 : 0);
+  return r;
+}
+
+__device__ __forceinline__ int cta_of(const TreeShare& s, unsigned at) {
+  const unsigned longer = s.extra * (s.each + 1);
+  return static_cast<int>(at < longer ? at / (s.each + 1) : s.extra + (at - longer) / s.each);
+}
+
+// seek for trees: `want` does not fall from call to call.
+__device__ __forceinline__ bool seek_trees(const AParams& p, TreeWork& w, Cursor& c, unsigned want,
+                                           long long budget) {
+#pragma unroll 1
+  for (;;) {
+    const unsigned past = __ballot_sync(kFull, w.upto > want);
+    if (past) {
+      const int src = __ffs(past) - 1;
+      c.b = w.base + src;
+      c.s.q0 = __shfl_sync(kFull, w.s.q0, src);
+      c.s.n = __shfl_sync(kFull, w.s.n, src);
+      c.s.ctx = __shfl_sync(kFull, w.s.ctx, src);
+      c.s.tiles = __shfl_sync(kFull, w.s.tiles, src);
+      const unsigned blocks = __shfl_sync(kFull, w.blocks, src);
+      const unsigned rest = want - __shfl_sync(kFull, w.upto - w.weight, src);
+      const unsigned tile = rest / blocks;  // of all kv heads
+      c.h = tile / c.s.tiles;
+      c.t = tile - c.h * c.s.tiles;
+      take_tile<true>(p, c, p.split ? rest - tile * blocks : 0, budget);
+      return true;
+    }
+    if (w.base + 32 >= p.B) return false;
+    load_trees(p, w, w.base + 32, __shfl_sync(kFull, w.upto, 31));
+  }
 }
 
 // The next tile, kv head or sequence with tokens, while key blocks are left.
@@ -662,14 +743,20 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
       // of 16 keys a block takes 32 copies, which one warp issues too slowly.
       const bool keys = warp == 0;
       Cursor c = {};
-      Share share = {0, 0, 0, 0};
+      TreeWork work;
+      std::conditional_t<TREE, TreeShare, Share> share = {0, 0, 0, 0};
       long long want = blockIdx.x;  // an item, or a key block
       bool more = true, placed = false;
       if (keys && p.split) {
-        share = my_share<TREE>(p);
+        if constexpr (TREE)
+          share = share_trees(p, work);
+        else
+          share = my_share(p);
         want = share.begin;
         more = share.begin < share.end;
         if (lane == 0) p.meta[blockIdx.x].x = -1;
+      } else if (TREE && keys) {
+        load_trees(p, work, 0, 0);
       }
       const int boxes = kKeys / p.box;
       const uint32_t box_bytes = static_cast<uint32_t>(p.box) * 128u;  // of one panel
@@ -678,16 +765,38 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
       int slot = unit, loads = 0, queries = 0;
       uint32_t phase = 1;                    // parity of the place's last release
       bool ok = true;
+      int begin = 0, end = 0, hi = 0, lo = 0, h = 0, sink_blocks = 0, skip = 0;  // of the segment
+      const int* table = p.block_table;
+      // box l of a block: its page, -1 if no row sees any of its keys, -2 if
+      // the table names no page of the pool for it
+      auto lookup = [&](int key0) {
+        const int key = key0 + lane * p.box;
+        if (lane >= boxes || key >= hi || (key + p.box <= lo && key >= p.sinks)) return -1;
+        const int page = __ldg(table + key / p.page);
+        return page >= 0 && page < p.num_pages ? page : -2;
+      };
+      auto first_key = [&](int k) { return (k < sink_blocks ? k : k + skip) * kKeys; };
       for (int seg = 0; ok; ++seg) {
+        int page = -1;
         if (keys) {
           if (seg > 0) ok = __all_sync(kFull, wait_soon(qempty, (seg & 1) ^ 1, abort_flag));
           if (!ok) break;
           if (more && !placed) {
-            more = seek<TREE>(p, c, want, p.split ? share.end - share.begin : 1LL << 40);
+            const long long budget = p.split ? share.end - share.begin : 1LL << 40;
+            if constexpr (TREE)
+              more = seek_trees(p, work, c, static_cast<unsigned>(want), budget);
+            else
+              more = seek(p, c, want, budget);
             placed = p.split;
           }
+          const Tile& tile = c.tile;
+          if (TREE) {  // the first block's pages are on their way while the segment is published
+            begin = c.begin, end = more ? c.end : -1, hi = tile.hi, lo = tile.lo, h = c.h;
+            sink_blocks = tile.sink_blocks, skip = tile.main_block - sink_blocks;
+            table = p.block_table + c.b * p.bt_stride;
+            if (more) page = lookup(first_key(begin));
+          }
           if (lane == 0) {
-            const Tile& tile = c.tile;
             Segment& g = segments[seg % kSegments];
             g.begin = c.begin;
             g.end = more ? c.end : -1;
@@ -719,21 +828,14 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
           ok = __all_sync(kFull, wait_soon(segment_ready(seg), (seg / kSegments) & 1, abort_flag));
           if (!ok) break;
         }
-        const Segment& g = segments[seg % kSegments];
-        const int begin = g.begin, end = g.end, hi = g.hi, lo = g.lo, h = g.h;
-        const int sink_blocks = g.sink_blocks, skip = g.main_block - sink_blocks;
+        if (!TREE || !keys) {
+          const Segment& g = segments[seg % kSegments];
+          begin = g.begin, end = g.end, hi = g.hi, lo = g.lo, h = g.h;
+          sink_blocks = g.sink_blocks, skip = g.main_block - sink_blocks;
+          table = p.block_table + g.b * p.bt_stride;
+          if (end >= 0) page = lookup(first_key(begin));
+        }
         if (end < 0) break;
-        const int* table = p.block_table + g.b * p.bt_stride;
-        // box l of a block: its page, -1 if no row sees any of its keys, -2 if
-        // the table names no page of the pool for it
-        auto lookup = [&](int key0) {
-          const int key = key0 + lane * p.box;
-          if (lane >= boxes || key >= hi || (key + p.box <= lo && key >= p.sinks)) return -1;
-          const int page = __ldg(table + key / p.page);
-          return page >= 0 && page < p.num_pages ? page : -2;
-        };
-        auto first_key = [&](int k) { return (k < sink_blocks ? k : k + skip) * kKeys; };
-        int page = lookup(first_key(begin));
         for (int k = begin; k < end; ++k) {
           const int in_page = (first_key(k) + lane * p.box) % p.page;
           const int next = k + 1 < end ? lookup(first_key(k + 1)) : -1;
@@ -1793,8 +1895,12 @@ dsa_status attend(
   p.G = G;
   p.window = window < max_context ? window : 0;  // such a window hides nothing
   p.sinks = p.window ? (sinks < max_context ? sinks : max_context) : 0;
+  // trees count all key blocks in 32 bits
+  const bool counted =
+      static_cast<double>(max_items(T, B, Hkv, q_tokens)) * ((max_context + kKeys - 1) / kKeys + 1) < 2e9;
   const Plan plan =
-      TREE ? make_tree_plan(T, B, Hkv, G, head_dim, q_tokens, max_context, p.window, p.sinks, need > 0)
+      TREE ? make_tree_plan(T, B, Hkv, G, head_dim, q_tokens, max_context, p.window, p.sinks,
+                            need > 0 && counted)
            : make_plan(T, B, Hkv, head_dim, q_tokens, max_context, p.window, p.sinks, need > 0);
   const int tiles = plan.tiles;
   p.q_tokens = q_tokens;

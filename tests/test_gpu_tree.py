@@ -79,6 +79,16 @@ def test_long_contexts_are_cut_and_joined():
         go([16, 1], [30000, 5], 8, 1, 64, masks=masks, poison=False, seed=2)
 
 
+@pytest.mark.parametrize("batch,dim", [(33, 128), (70, 64), (100, 128)])
+def test_many_sequences_cut(batch, dim):
+    """More sequences than a warp has lanes, idle ones and unequal ones among them."""
+    r = np.random.RandomState(batch)
+    n = r.randint(0, 9, batch) * (r.rand(batch) < 0.8)
+    ctx = np.where(n > 0, n + r.randint(0, 3000, batch), 0)
+    ctx[batch // 2], n[batch // 2] = 9000, 8
+    go(n.tolist(), ctx.tolist(), 8, 2, dim, page=16, seed=batch, poison=dim == 64)
+
+
 def test_whole_items():
     go([20] * 100, [150] * 100, 32, 8, 64, page=16, seed=3)
     go([64] * 60, list(range(64, 124)), 32, 8, 128, seed=4)
