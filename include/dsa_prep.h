@@ -354,8 +354,8 @@ dsa_status dsa_indexer_mqa_logits(
  *   codes, scales  e4m3 bytes [T, N], 8-byte aligned, and [T, ceil(N / group)]
  *                  scales as scale_format says (fp32: 4-byte aligned), or both
  *                  NULL.  At least one of out and codes is given.
- *   N a multiple of 8, at most 32768; group 32 or 128; flags may hold
- *   DSA_FLAG_PDL.  The 16-bit rows are 16-byte aligned; their strides and
+ *   T <= 2^30; N a multiple of 8, at most 32768; group 32 or 128; flags may
+ *   hold DSA_FLAG_PDL.  The 16-bit rows are 16-byte aligned; their strides and
  *   codes_stride are multiples of 8.  Rows of an output may not overlap.
  * The squares are summed in fp32, which holds rows with sqrt(sum z^2) < 1.8e19.
  */
@@ -642,8 +642,9 @@ dsa_status dsa_cache_compact(
  * HOST arrays, read during the call; with s = shapes + 5 * v, token t of page p
  * of view v is at bases[v] + p * s[0] + t * s[1] + h * s[2], s[4] bytes for each
  * head h < s[3].  All are multiples of 4 (of 16: 16 bytes move at a time).  A
- * page-blocked index-K cache is two views, its codes and its scales.  0 <=
- * n_views <= DSA_MAX_VIEWS; with none only the tables are kept.
+ * page-blocked index-K cache is two views, its codes and its scales.  No two
+ * views share a byte.  0 <= n_views <= DSA_MAX_VIEWS; with none only the tables
+ * are kept.
  *
  *   which, drafted, n_kept  int32 [n], n <= DSA_MAX_KEEPS; every row named once.
  *   kept           int32 [n, kept_stride >= max_kept]; NULL if max_kept is 0.

@@ -22,7 +22,7 @@ import os
 
 import torch
 
-from ._build import LIB_PATH
+from ._build import BINDING_PATH, LIB_PATH
 
 __all__ = [
     "DsaError", "NEOX", "GPTJ", "HEAD_DIM", "DEVERR_POSITION", "DEVERR_SLOT", "DEVERR_TIMEOUT",
@@ -155,7 +155,11 @@ _usual = None  # the module of _marshal, once the library is loaded
 def _bind(lib):
     """Loads the calls' marshalling in C++ and hands it their entry points."""
     global _usual
-    from . import _binding
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise RuntimeError(f"{BINDING_PATH} is missing or does not fit this torch: build it first "
+                           "(python -c 'import __graft_entry__ as g; g.build()')") from e
     _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.dsa_rms_norm, lib.dsa_kv_append, lib.dsa_tree_attention,
         lib.dsa_paged_attention_workspace_bytes, lib.dsa_cache_keep,

@@ -4,6 +4,7 @@ marshalling in C++ of the calls that a decode step makes eagerly."""
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sysconfig
@@ -65,7 +66,8 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     link them into one shared library, and the binding beside them."""
     tag = f"{os.getpid()}"
     binding = None
-    if force or _older(BINDING_PATH, [BINDING_SOURCE] + _headers()):
+    torch_file = importlib.util.find_spec("torch").origin  # another torch, another binding
+    if force or _older(BINDING_PATH, [BINDING_SOURCE, torch_file] + _headers()):
         binding = subprocess.Popen(_binding_command(BINDING_PATH + f".tmp{tag}"))
     try:
         if force or _stale():

@@ -98,6 +98,10 @@ struct Args {
   }
   double number() {
     PyObject* o = *at++;
+    if (!PyFloat_Check(o) && !PyLong_Check(o)) {
+      ok = false;
+      return 0;
+    }
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) ok = false;
     return v;

@@ -26,7 +26,7 @@ def _norm(lib, **over):
 
 
 @pytest.mark.parametrize("over,status", [
-    (dict(T=-1), 3), (dict(N=0), 3), (dict(N=60), 3), (dict(N=32776), 3), (dict(dtype=2), 4),
+    (dict(T=-1), 3), (dict(T=(1 << 30) + 1), 3), (dict(N=0), 3), (dict(N=60), 3), (dict(N=32776), 3), (dict(dtype=2), 4),
     (dict(flags=2), 4), (dict(flags=8), 4), (dict(eps=0.0), 4), (dict(eps=-1.0), 4),
     (dict(eps=INF), 4), (dict(eps=NAN), 4), (dict(group=64), 4), (dict(group=0), 4),
     (dict(fmt=2), 4), (dict(fmt=-1), 4), (dict(xs=56), 3), (dict(rs=56), 3), (dict(ros=56), 3),
