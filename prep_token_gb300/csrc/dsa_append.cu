@@ -7,10 +7,8 @@
 //   (a, b) -> (a c - b s, b c + a s) on x[0:rope_dim)
 //   rounded once; k and v to slot out_cache_loc[t] of their caches, q to q_out
 //
-// A head's row of D values is D / 16 lanes wide, two 16-byte pieces to a lane:
-// the pieces of a lane that rotates are the two halves of its pairs (NeoX), or
-// neighbours (GPT-J, and the values that pass through).  A pair is in one lane
-// and needs no shuffle; a norm's sum takes log2(D / 16) of them.  c, s and gamma
+// A head's row of D values is D / 16 lanes wide, two 16-byte pieces to a lane.  A
+// pair is in one lane and needs no shuffle; a norm's sum takes log2(D / 16) of them.  c, s and gamma
 // are the same for all heads of a token's q (or k): their products are four
 // factors per pair, formed once, and the root is multiplied in at the end.
 //
@@ -18,12 +16,13 @@
 // is in flight at once; many take warps that stay and load ahead.
 //
 // Bound: HBM for many tokens, each row read and written once; measured (6.78 TB/s):
-// 8192 tokens of 32 + 16 heads of 128, 206 MB, 37.2 us with both norms (5.5 TB/s),
-// 36.0 without; 4096 of 64 + 16, 29.7 us (5.7 TB/s).  What is missing is the stream
-// kernel's start (three round trips: position, cos/sin, first store) and its
-// instructions (60% of the issue slots at that rate): its first form, with
-// addresses formed anew for each row, took 55 us with norms, and one pass to a warp 66.  16 tokens of
-// 64 + 16 heads take 2.4 us, launch and two dependent reads.
+// 8192 tokens of 32 + 16 heads of 128, 206 MB, 37 us with both norms (5.5 TB/s),
+// 36 without; 4096 of 64 + 16, 29.5 us (5.7 TB/s).  With nothing to compute the
+// same rows take 34.7: what is missing is the start (three round trips: position,
+// cos/sin, first store) and the mix of reads and writes in rows of 256 bytes.  The
+// first form of the stream kernel, with addresses formed anew for each row, took 55
+// us with norms, one pass to a warp takes 56.  16 tokens of 64 + 16 heads take 2.1
+// us, launch and two dependent reads.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -39,12 +38,12 @@ using namespace dsa_rows;
 constexpr int kSms = 152;
 constexpr int kWarps = 4;  // of a CTA of the direct kernel
 constexpr int kStreamWarps = 8, kStreamCtas = 2;  // of the stream kernel, per CTA and per SM
-// Passes per SM from which on it is the faster one (us, direct and stream): 600
-// tokens of 64 + 16 heads, 79 passes, 6.4 and 6.3; 2048 of them 20 and 16.4; 1500
-// of 24 + 48 heads of 64, 88 passes, 6.9 and 8.0.  A norm's longer arithmetic is
-// worth overlapping earlier: 256 tokens of 32 + 16 heads, 20 passes, 3.3 and 4.0;
-// 1000, 79 passes, 8.7 and 6.2.
-constexpr int stream_passes(bool norm) { return norm ? 40 : 130; }
+// Passes per SM from which on it is the faster one (us, direct and stream): 400
+// tokens of 64 + 16 heads, 53 passes, 4.7 and 5.1; 600 of them, 79, 6.1 and 5.4; 1500
+// of 24 + 48 heads of 64, 88, 6.6 and 6.1; 8192 of 32 + 16, 647, 40 and 36.  A norm's
+// longer arithmetic is worth overlapping earlier: 256 tokens of 32 + 16 heads, 20
+// passes, 3.3 and 4.0; 1000, 79, 7.9 and 6.1.
+constexpr int stream_passes(bool norm) { return norm ? 40 : 70; }
 
 struct AppendParams {
   const uint16_t *q, *k, *v;
@@ -74,13 +73,43 @@ __device__ __forceinline__ void split_pairs(float2 (&x)[4], float2 (&y)[4]) {
   }
 }
 
+// Where a lane's values are in a row: the pieces of eight at `first` and `second`.
+// Whatever pieces a lane has, neighbouring lanes have neighbouring ones, so that a
+// load or store of the warp covers whole sectors (with a lane's two side by side
+// each took all sectors of the rows, twice: 8192 tokens of 32 + 16 heads, nothing
+// to rotate, 50 us instead of 36).  NeoX: the lanes that rotate have the two
+// halves of their pairs, piece l and l + rope_dim / 16; the others share the rest.
+// GPT-J: pieces l and l + D / 16, whose pairs are within them.
+template <int D, int STYLE>
+struct Lane {
+  static constexpr int kLanes = D / 16;        // of a row
+  static constexpr int kRowsOf = 32 / kLanes;  // rows that a warp takes at a time
+  int l, sub, first, second;
+  bool turns_first, turns_second;
+  __device__ __forceinline__ explicit Lane(const AppendParams& p) {
+    const int lane = threadIdx.x & 31;
+    l = lane % kLanes, sub = lane / kLanes;
+    if (STYLE == DSA_ROPE_NEOX) {
+      turns_first = turns_second = l < p.turns;
+      first = 8 * (l < p.turns ? l : l + p.turns);
+      second = 8 * (l < p.turns ? l + p.turns : l + kLanes);
+    } else {
+      turns_first = l < 2 * p.turns;
+      turns_second = l + kLanes < 2 * p.turns;
+      first = 8 * l;
+      second = 8 * (l + kLanes);
+    }
+  }
+};
+
+__device__ __forceinline__ void load4(const float* p, float2& a, float2& b) {
+  const float4 x = *reinterpret_cast<const float4*>(p);
+  a = make_float2(x.x, x.y), b = make_float2(x.z, x.w);
+}
 // Eight floats of a row as four pairs.
 __device__ __forceinline__ void load8(const float* p, float2 (&v)[4]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float4 x = *(reinterpret_cast<const float4*>(p) + i);
-    v[2 * i] = make_float2(x.x, x.y), v[2 * i + 1] = make_float2(x.z, x.w);
-  }
+  load4(p, v[0], v[1]);
+  load4(p + 4, v[2], v[3]);
 }
 
 // x' = xx x + xy y, y' = yy y + yx x for a lane's pairs: the rotation and gamma,
@@ -89,23 +118,35 @@ struct Turn {
   float2 xx[4], xy[4], yy[4], yx[4];
 };
 
-template <int STYLE, bool NORM>
-__device__ __forceinline__ void make_turn(Turn& r, bool turns, const float* cos, const float* sin,
-                                          const float* gamma, int first, int second) {
+// cos, sin: the token's rows.
+template <int STYLE, bool NORM, class L>
+__device__ __forceinline__ void make_turn(Turn& r, const L& at, const float* cos, const float* sin,
+                                          const float* gamma) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    r.xx[i] = r.yy[i] = make_float2(1.0f, 1.0f), r.yx[i] = r.xy[i] = make_float2(0.0f, 0.0f);
-  if (turns) {
-    load8(cos, r.xx);
-    load8(sin, r.yx);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      r.yy[i] = r.xx[i], r.xy[i] = make_float2(-r.yx[i].x, -r.yx[i].y);
+    r.xx[i] = make_float2(1.0f, 1.0f), r.yx[i] = make_float2(0.0f, 0.0f);
+  if (STYLE == DSA_ROPE_NEOX) {
+    if (at.turns_first) {
+      load8(cos + 8 * at.l, r.xx);
+      load8(sin + 8 * at.l, r.yx);
+    }
+  } else {
+    if (at.turns_first) {
+      load4(cos + at.first / 2, r.xx[0], r.xx[1]);
+      load4(sin + at.first / 2, r.yx[0], r.yx[1]);
+    }
+    if (at.turns_second) {
+      load4(cos + at.second / 2, r.xx[2], r.xx[3]);
+      load4(sin + at.second / 2, r.yx[2], r.yx[3]);
+    }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r.yy[i] = r.xx[i], r.xy[i] = make_float2(-r.yx[i].x, -r.yx[i].y);
   if (NORM && gamma) {
     float2 gx[4], gy[4];
-    load8(gamma + first, gx);
-    load8(gamma + second, gy);
+    load8(gamma + at.first, gx);
+    load8(gamma + at.second, gy);
     if (STYLE == DSA_ROPE_GPTJ) split_pairs(gx, gy);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -117,8 +158,8 @@ __device__ __forceinline__ void make_turn(Turn& r, bool turns, const float* cos,
 
 // A lane's two pieces of a row, turned; the lanes of a row call it together.
 template <bool BF16, int D, int STYLE, bool NORM>
-__device__ __forceinline__ void turn_row(uint4& u, uint4& w, const Turn& r, bool turns, bool norm,
-                                         float eps) {
+__device__ __forceinline__ void turn_row(uint4& u, uint4& w, const Turn& r,
+                                         const Lane<D, STYLE>& at, bool norm, float eps) {
   float2 x[4], y[4];
   unpack8<BF16>(u, x);
   unpack8<BF16>(w, y);
@@ -135,7 +176,9 @@ __device__ __forceinline__ void turn_row(uint4& u, uint4& w, const Turn& r, bool
     for (int o = D / 32; o; o >>= 1) all += __shfl_xor_sync(kFull, all, o);
     rs.x = rs.y = rsqrtf(fmaf(all, 1.0f / D, eps));
   }
-  if (!(turns || (NORM && norm))) return;  // as it is, NaN and all
+  // a piece with neither stays as it is, NaN and all
+  const bool first = at.turns_first || (NORM && norm), second = at.turns_second || (NORM && norm);
+  if (!first) return;  // nor does the second
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 a = x[i], b = y[i];
@@ -149,26 +192,11 @@ __device__ __forceinline__ void turn_row(uint4& u, uint4& w, const Turn& r, bool
   } else {
     u = make_uint4(pack2<BF16>(x[0].x, y[0].x), pack2<BF16>(x[0].y, y[0].y),
                    pack2<BF16>(x[1].x, y[1].x), pack2<BF16>(x[1].y, y[1].y));
-    w = make_uint4(pack2<BF16>(x[2].x, y[2].x), pack2<BF16>(x[2].y, y[2].y),
-                   pack2<BF16>(x[3].x, y[3].x), pack2<BF16>(x[3].y, y[3].y));
+    if (second)
+      w = make_uint4(pack2<BF16>(x[2].x, y[2].x), pack2<BF16>(x[2].y, y[2].y),
+                     pack2<BF16>(x[3].x, y[3].x), pack2<BF16>(x[3].y, y[3].y));
   }
 }
-
-// Where a lane's values are in a row: the pieces at `first` and `second`.
-template <int D, int STYLE>
-struct Lane {
-  static constexpr int kLanes = D / 16;        // of a row
-  static constexpr int kRowsOf = 32 / kLanes;  // rows that a warp takes at a time
-  int l, sub, first, second;
-  bool turns;
-  __device__ __forceinline__ explicit Lane(const AppendParams& p) {
-    const int lane = threadIdx.x & 31;
-    l = lane % kLanes, sub = lane / kLanes;
-    turns = l < p.turns;
-    first = 8 * (STYLE == DSA_ROPE_NEOX && turns ? l : 2 * l);
-    second = 8 * (STYLE == DSA_ROPE_NEOX && turns ? l + p.turns : 2 * l + 1);
-  }
-};
 
 // The token's place in a cache.
 __device__ __forceinline__ long long place_of(const AppendParams& p, long long slot,
@@ -219,9 +247,8 @@ __global__ void __launch_bounds__(32 * kWarps)
   if (!is_v) {
     const float* const gamma = is_q ? p.q_gamma : p.k_gamma;
     Turn r;
-    make_turn<STYLE, NORM>(r, at.turns, p.cos + pos * p.cs_stride + 8 * at.l,
-                           p.sin + pos * p.cs_stride + 8 * at.l, gamma, at.first, at.second);
-    turn_row<BF16, D, STYLE, NORM>(u, w, r, at.turns, gamma != nullptr, p.eps);
+    make_turn<STYLE, NORM>(r, at, p.cos + pos * p.cs_stride, p.sin + pos * p.cs_stride, gamma);
+    turn_row<BF16, D, STYLE, NORM>(u, w, r, at, gamma != nullptr, p.eps);
   }
   if (some) {
     uint16_t* const to =
@@ -316,6 +343,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
   for (int i = 0; i < kDepth - 1; ++i) fetch();
   cp_async_wait<kDepth - 2>();
   int stage = 0;
+  Turn r;  // without a norm k's is q's
   // one kind of a token's rows after the other
 #pragma unroll 1
   for (int left = n;;) {
@@ -332,10 +360,9 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
     to += row * step + at.first;
     step *= at.kRowsOf;
     const float* const gamma = kind == 0 ? p.q_gamma : p.k_gamma;
-    Turn r;
-    if (kind < 2) {
-      const float* const cos = angles + (t & 1) * 128 + 8 * at.l;
-      make_turn<STYLE, NORM>(r, at.turns, cos, cos + 64, gamma, at.first, at.second);
+    if (kind < 2 && (NORM || kind == 0 || p.q_passes == 0 || left == n)) {
+      const float* const cos = angles + (t & 1) * 128;
+      make_turn<STYLE, NORM>(r, at, cos, cos + 64, gamma);
     }
     int m = min(left, (kind == 0 ? p.q_passes : p.kv_passes) - skip);
     left -= m;
@@ -347,7 +374,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
       uint4 u = *reinterpret_cast<const uint4*>(from);
       uint4 w = *reinterpret_cast<const uint4*>(from + 512);
       if (kind < 2)
-        turn_row<BF16, D, STYLE, NORM>(u, w, r, at.turns, gamma != nullptr, p.eps);
+        turn_row<BF16, D, STYLE, NORM>(u, w, r, at, gamma != nullptr, p.eps);
       if (rows > 0) {
         store_piece(to, u);
         store_piece(to + apart, w);
