@@ -16,9 +16,9 @@
 // is in flight at once; many take warps that stay and load ahead.
 //
 // Bound: HBM for many tokens, each row read and written once; measured (6.78 TB/s):
-// 8192 tokens of 32 + 16 heads of 128, 206 MB, 37 us with both norms (5.5 TB/s),
-// 36 without; 4096 of 64 + 16, 29.5 us (5.7 TB/s).  With nothing to compute the
-// same rows take 34.7: what is missing is the start (three round trips: position,
+// 8192 tokens of 32 + 16 heads of 128, 206 MB, 36.3 us with both norms (5.7 TB/s),
+// 35.6 without; 16384 67.7 us (6.1 TB/s).  With nothing to compute the same rows
+// take 32 (direct) to 35: what is missing is the start (three round trips: position,
 // cos/sin, first store) and the mix of reads and writes in rows of 256 bytes.  The
 // first form of the stream kernel, with addresses formed anew for each row, took 55
 // us with norms, one pass to a warp takes 56.  16 tokens of 64 + 16 heads take 2.1
@@ -38,12 +38,12 @@ using namespace dsa_rows;
 constexpr int kSms = 152;
 constexpr int kWarps = 4;  // of a CTA of the direct kernel
 constexpr int kStreamWarps = 8, kStreamCtas = 2;  // of the stream kernel, per CTA and per SM
-// Passes per SM from which on it is the faster one (us, direct and stream): 400
-// tokens of 64 + 16 heads, 53 passes, 4.7 and 5.1; 600 of them, 79, 6.1 and 5.4; 1500
-// of 24 + 48 heads of 64, 88, 6.6 and 6.1; 8192 of 32 + 16, 647, 40 and 36.  A norm's
-// longer arithmetic is worth overlapping earlier: 256 tokens of 32 + 16 heads, 20
-// passes, 3.3 and 4.0; 1000, 79, 7.9 and 6.1.
-constexpr int stream_passes(bool norm) { return norm ? 40 : 70; }
+// Passes per SM from which on it is the faster one (us, direct and stream): 1500
+// tokens of 24 + 48 heads of 64, 88 passes, 6.2 and 6.7; 8192 of 8 + 2 of 128, 161,
+// 11.0 and 12.6; 4096 of 64 + 16, 539, 31.0 and 29.7; 8192 of 32 + 16, 647, 37.5
+// and 35.6.  A norm's longer arithmetic is worth overlapping earlier: 256 tokens of
+// 32 + 16 heads, 20 passes, 3.3 and 4.0; 1000, 79, 8.0 and 6.6; 8192, 647, 56 and 36.
+constexpr int stream_passes(bool norm) { return norm ? 40 : 250; }
 
 struct AppendParams {
   const uint16_t *q, *k, *v;
@@ -60,6 +60,7 @@ struct AppendParams {
   int page_size, page_shift;
   int passes;       // of a token: its q, k and v rows, 512 / D at a time
   int q_passes, kv_passes;
+  int merged;       // k and v rows are few enough to share a pass, k's first
   int* err;
 };
 
@@ -156,10 +157,11 @@ __device__ __forceinline__ void make_turn(Turn& r, const L& at, const float* cos
   }
 }
 
-// A lane's two pieces of a row, turned; the lanes of a row call it together.
+// A lane's two pieces of a row, turned if it is `active`; a whole warp calls it.
 template <bool BF16, int D, int STYLE, bool NORM>
 __device__ __forceinline__ void turn_row(uint4& u, uint4& w, const Turn& r,
-                                         const Lane<D, STYLE>& at, bool norm, float eps) {
+                                         const Lane<D, STYLE>& at, bool active, bool norm,
+                                         float eps) {
   float2 x[4], y[4];
   unpack8<BF16>(u, x);
   unpack8<BF16>(w, y);
@@ -178,7 +180,7 @@ __device__ __forceinline__ void turn_row(uint4& u, uint4& w, const Turn& r,
   }
   // a piece with neither stays as it is, NaN and all
   const bool first = at.turns_first || (NORM && norm), second = at.turns_second || (NORM && norm);
-  if (!first) return;  // nor does the second
+  if (!first || !active) return;  // without the first nor does the second
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 a = x[i], b = y[i];
@@ -212,6 +214,14 @@ __device__ __forceinline__ long long place_of(const AppendParams& p, long long s
   return page * page_stride + in_page * token_stride;
 }
 
+// The rows of a kind: q (0), k (1) and v (2), or k and v (1).
+__device__ __forceinline__ int rows_of(const AppendParams& p, int kind) {
+  return kind == 0 ? p.H : kind == 1 && p.merged ? 2 * p.Hkv : p.Hkv;
+}
+__device__ __forceinline__ bool is_value(const AppendParams& p, int kind, int row) {
+  return kind == 2 || (kind == 1 && p.merged && row >= p.Hkv);
+}
+
 // Few tokens: a warp to each pass of a token (512 / D rows of q, k or v).
 template <bool BF16, int D, int STYLE, bool NORM>
 __global__ void __launch_bounds__(32 * kWarps)
@@ -222,10 +232,12 @@ __global__ void __launch_bounds__(32 * kWarps)
   grid_launch_dependents();
   if (t >= p.T) return;
   const Lane<D, STYLE> at(p);
-  const bool is_q = pass < p.q_passes, is_v = pass >= p.q_passes + p.kv_passes;
-  const int row = (pass - (is_q ? 0 : is_v ? p.q_passes + p.kv_passes : p.q_passes)) *
-                      at.kRowsOf + at.sub;
-  const bool some = row < (is_q ? p.H : p.Hkv);
+  const int kind = pass < p.q_passes ? 0 : pass < p.q_passes + p.kv_passes ? 1 : 2;
+  const bool is_q = kind == 0;
+  int row = (pass - (is_q ? 0 : kind == 1 ? p.q_passes : p.q_passes + p.kv_passes)) * at.kRowsOf +
+            at.sub;
+  const bool some = row < rows_of(p, kind), is_v = is_value(p, kind, row);
+  if (kind == 1 && is_v) row -= p.Hkv;
   const uint16_t* const from = is_q   ? p.q + t * p.q_t + row * p.q_h
                                : is_v ? p.v + t * p.v_t + row * p.v_h
                                       : p.k + t * p.k_t + row * p.k_h;
@@ -244,11 +256,11 @@ __global__ void __launch_bounds__(32 * kWarps)
   const bool keep = slot >= 0 && slot < p.num_slots;
   if (!keep && first_lane && p.err) atomicOr(p.err, DSA_DEVERR_SLOT);
   if (!is_q && !keep) return;
-  if (!is_v) {
+  if (kind < 2) {
     const float* const gamma = is_q ? p.q_gamma : p.k_gamma;
     Turn r;
     make_turn<STYLE, NORM>(r, at, p.cos + pos * p.cs_stride, p.sin + pos * p.cs_stride, gamma);
-    turn_row<BF16, D, STYLE, NORM>(u, w, r, at, gamma != nullptr, p.eps);
+    turn_row<BF16, D, STYLE, NORM>(u, w, r, at, !is_v, gamma != nullptr, p.eps);
   }
   if (some) {
     uint16_t* const to =
@@ -264,7 +276,7 @@ __global__ void __launch_bounds__(32 * kWarps)
 // lane's pieces of the passes ahead travel into its own places of a ring in
 // shared memory (cp.async; nobody else reads them), a token's cos/sin row into
 // one of two places of the warp while the token before is worked on.
-constexpr int kDepth = 4;                          // passes in flight, and this one
+constexpr int kDepth = 3;                          // passes in flight, and this one
 constexpr int kWarpBytes = kDepth * 1024 + 2 * 512;  // the ring; cos and sin of two tokens
 
 template <bool BF16, int D, int STYLE, bool NORM>
@@ -288,6 +300,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
 
   // Where the loads are: so many passes of q (0), k (1) or v (2) of a token are
   // left, the next one's row and place; addresses move by the pass within a kind.
+  const int last_kind = p.merged ? 1 : 2;
   int fetch_t = t, fetch_kind, fetch_left, fetch_rows, fetch_n = n;
   uint32_t fetch_to = smem_u32(ring + 16 * lane);
   const uint32_t ring_end = fetch_to + kDepth * 1024;
@@ -296,19 +309,22 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
   auto enter = [&](int kind, int skip) {  // `skip` passes of it are done
     fetch_kind = kind;
     fetch_left = (kind == 0 ? p.q_passes : p.kv_passes) - skip;
-    const int row = skip * at.kRowsOf + at.sub;
-    fetch_rows = (kind == 0 ? p.H : p.Hkv) - row;
-    fetch_step = kind == 0 ? p.q_h : kind == 1 ? p.k_h : p.v_h;
-    fetch_from = (kind == 0   ? p.q + fetch_t * p.q_t
-                  : kind == 1 ? p.k + fetch_t * p.k_t
-                              : p.v + fetch_t * p.v_t) + row * fetch_step + at.first;
+    int row = skip * at.kRowsOf + at.sub;
+    fetch_rows = rows_of(p, kind) - row;
+    const bool value = is_value(p, kind, row);
+    if (kind == 1 && value) row -= p.Hkv;
+    fetch_step = kind == 0 ? p.q_h : value ? p.v_h : p.k_h;
+    fetch_from = (kind == 0 ? p.q + fetch_t * p.q_t
+                  : value   ? p.v + fetch_t * p.v_t
+                            : p.k + fetch_t * p.k_t) + row * fetch_step + at.first;
     fetch_step *= at.kRowsOf;
   };
   const int apart = at.second - at.first;
   auto fetch = [&]() {  // the next pass, if there is one
     if (fetch_left == 0) {
-      if (fetch_kind == 2) ++fetch_t;
-      enter(fetch_kind == 2 ? (p.q_passes > 0 ? 0 : 1) : fetch_kind + 1, 0);
+      const bool done = fetch_kind == last_kind;
+      if (done) ++fetch_t;
+      enter(done ? (p.q_passes > 0 ? 0 : 1) : fetch_kind + 1, 0);
     }
     if (fetch_n > 0 && fetch_rows > 0) {
       cp_async16_cg(fetch_to, fetch_from);
@@ -351,12 +367,14 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
     const bool keep = slot >= 0 && slot < p.num_slots;
     if (lane == 0 && p.err && !(ok && keep))
       atomicOr(p.err, ok ? DSA_DEVERR_SLOT : DSA_DEVERR_POSITION);
-    const int row = skip * at.kRowsOf + at.sub;
-    int rows = ok && (kind == 0 || keep) ? (kind == 0 ? p.H : p.Hkv) - row : 0;
-    long long step = kind == 0 ? p.out_h : kind == 1 ? p.kc_head : p.vc_head;
-    uint16_t* to = kind == 0   ? p.q_out + t * p.out_t
-                   : kind == 1 ? p.k_cache + place_of(p, keep ? slot : 0, p.kc_page, p.kc_token)
-                               : p.v_cache + place_of(p, keep ? slot : 0, p.vc_page, p.vc_token);
+    int row = skip * at.kRowsOf + at.sub;
+    int rows = ok && (kind == 0 || keep) ? rows_of(p, kind) - row : 0;
+    const bool value = is_value(p, kind, row);
+    if (kind == 1 && value) row -= p.Hkv;
+    long long step = kind == 0 ? p.out_h : value ? p.vc_head : p.kc_head;
+    uint16_t* to = kind == 0 ? p.q_out + t * p.out_t
+                   : value   ? p.v_cache + place_of(p, keep ? slot : 0, p.vc_page, p.vc_token)
+                             : p.k_cache + place_of(p, keep ? slot : 0, p.kc_page, p.kc_token);
     to += row * step + at.first;
     step *= at.kRowsOf;
     const float* const gamma = kind == 0 ? p.q_gamma : p.k_gamma;
@@ -374,7 +392,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
       uint4 u = *reinterpret_cast<const uint4*>(from);
       uint4 w = *reinterpret_cast<const uint4*>(from + 512);
       if (kind < 2)
-        turn_row<BF16, D, STYLE, NORM>(u, w, r, at, gamma != nullptr, p.eps);
+        turn_row<BF16, D, STYLE, NORM>(u, w, r, at, !value, gamma != nullptr, p.eps);
       if (rows > 0) {
         store_piece(to, u);
         store_piece(to + apart, w);
@@ -385,8 +403,9 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
     }
     if (left == 0) break;
     skip = 0;
-    if (++kind == 3) {  // the next token: the one behind it takes the last one's place for cos and sin
+    if (kind++ == last_kind) {  // the next token: the one behind it takes the last one's place for cos and sin
       kind = p.q_passes > 0 ? 0 : 1;
+      __syncwarp();  // which every lane has read
       ++t;
       slot = next_slot, ok = next_ok;
       next_slot = slot_of(t + 1), next_ok = valid(pos);
@@ -495,17 +514,18 @@ extern "C" dsa_status dsa_kv_append(
   p.turns = rope_dim / 16;
   p.page_size = page_size;
   p.page_shift = page_shift_of(page_size);
-  const int rows_of = 512 / head_dim;  // that a warp takes at a time
-  p.q_passes = (H + rows_of - 1) / rows_of;
-  p.kv_passes = (Hkv + rows_of - 1) / rows_of;
-  p.passes = p.q_passes + 2 * p.kv_passes;
+  const int at_once = 512 / head_dim;  // rows that a warp takes at a time
+  p.q_passes = (H + at_once - 1) / at_once;
+  p.kv_passes = (Hkv + at_once - 1) / at_once;
+  p.merged = 2 * Hkv <= at_once;
+  p.passes = p.q_passes + (p.merged ? 1 : 2 * p.kv_passes);
   p.err = err_flags;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  const long long all = static_cast<long long>(T) * p.passes;
   const bool norm = q_gamma || k_gamma;
+  const long long all = static_cast<long long>(T) * p.passes;
   // a token's cos/sin are fetched a token ahead, which has to be kDepth passes at least
   const bool stream_kernel = all >= stream_passes(norm) * kSms && p.passes >= kDepth;
   cfg.gridDim = dim3(stream_kernel ? kSms * kStreamCtas

@@ -129,8 +129,32 @@ def test_pages_and_layouts(page, layout):
     go(Call(150, 8, 4, 128, page=page, layout=layout, seed=page))
 
 
-def test_many_tokens():
-    go(Call(9000, 8, 2, 128, page=64, rope=128, norms=3, max_position=9000))
+@pytest.mark.parametrize("H,kv,D", [(8, 2, 128), (32, 8, 128), (4, 1, 128), (16, 2, 64), (9, 5, 64),
+                                    (0, 1, 128), (0, 7, 64), (1, 1, 64)])
+@pytest.mark.parametrize("norms", [0, 1, 2, 3])
+def test_many_tokens(H, kv, D, norms):
+    go(Call(9000, H, kv, D, page=64, rope=D // 2, style=kv % 2, norms=norms, max_position=9000,
+            dtype=FP if norms == 1 else BF))
+
+
+def test_bad_positions_and_slots_of_many():
+    c = Call(9000, 8, 2, norms=2, seed=5)
+    old = c.k_cache.clone(), c.v_cache.clone()
+    good = c.run()
+    c.k_cache.copy_(old[0]), c.v_cache.copy_(old[1])
+    r = np.random.RandomState(1)
+    bad_pos = torch.from_numpy(r.rand(9000) < 0.1).cuda()
+    bad_slot = torch.from_numpy(r.rand(9000) < 0.1).cuda()
+    c.positions[bad_pos] = torch.tensor([-1, 500, 2 ** 50], device="cuda")[
+        torch.arange(int(bad_pos.sum()), device="cuda") % 3]
+    c.slots[bad_slot] = torch.tensor([-1, 2 ** 40], device="cuda")[
+        torch.arange(int(bad_slot.sum()), device="cuda") % 2]
+    out = torch.full_like(good, 9.0)
+    c.run(q_out=out)
+    assert int(c.err) == 1 | 2
+    assert (out[bad_pos] == 9).all() and torch.equal(out[~bad_pos], good[~bad_pos])
+    c.q = None
+    c.check(None, *old, live=~bad_pos & ~bad_slot)
 
 
 def test_q_in_place_and_given():
