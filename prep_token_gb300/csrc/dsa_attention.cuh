@@ -1,6 +1,7 @@
 // Attention of new tokens over a paged K/V cache on the 5th-generation tensor
 // cores: a chunk of a prompt, single tokens, or both in one call, over the
-// whole context or a sliding window with the first tokens kept visible.
+// whole context or a sliding window with the first tokens kept visible; and for
+// trees of drafted tokens, with a mask.
 //
 // With G = H / Hkv query heads per kv head, query i of sequence b is the token
 // at pos = context_lens[b] - n_b + i, and for each of its heads
@@ -51,6 +52,18 @@
 // which a second kernel joins in a fixed order.  (make_plan and may_split say when
 // CTAs take whole items instead: then in the order of the batch, so that unequal
 // ones leave CTAs idle at the end.)
+//
+// Trees of drafted tokens (TREE): the last n_b keys of a sequence are its drafts',
+// and a row sees those whose bits its mask has, and the keys before them (within a
+// window of its position in the tree, which the mask's bits count).  The masks are
+// read where blocks are at an edge, as the blocks with drafts always are; what
+// differs else is that all tiles of a sequence see the same keys, so that the
+// division of the work is a product and a scan (TreeWork).  Measured: 64 x up to 16
+// drafts over up to 8192 keys, 64 heads on 8, 1.2 GB: 206 us (5.9 TB/s); 4 x 60 over
+// 32768, 32 on 4: 119 us (1080 TFLOP/s, each tile pair reads the keys anew);
+// 8 drafts over 1000: 14.7 us, of which the first scores take 4, softmax, values and
+// parts 3, launches and join the rest; 24 x 32 with a window of 1024, 16 heads of 64 on
+// as many: 44 us, 368 items of ten blocks in two rounds of 304.
 //
 // Every wait is bounded in time; TMEM is always released before exit.
 #ifndef DSA_ATTENTION_CUH

@@ -130,7 +130,7 @@ def test_pages_and_layouts(page, layout):
 
 
 @pytest.mark.parametrize("H,kv,D", [(8, 2, 128), (32, 8, 128), (4, 1, 128), (16, 2, 64), (9, 5, 64),
-                                    (0, 1, 128), (0, 7, 64), (1, 1, 64)])
+                                    (0, 1, 128), (0, 24, 128), (1, 1, 64), (64, 1, 128)])
 @pytest.mark.parametrize("norms", [0, 1, 2, 3])
 def test_many_tokens(H, kv, D, norms):
     go(Call(9000, H, kv, D, page=64, rope=D // 2, style=kv % 2, norms=norms, max_position=9000,

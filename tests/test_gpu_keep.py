@@ -260,6 +260,24 @@ def test_captured():
     assert all(np.array_equal(g.cpu().numpy(), w) for g, w in zip(now, (p.refs, p.table, p.lens)))
 
 
+def test_two_pools_at_once():
+    """Calls on two streams, each with a pool and a workspace of its own."""
+    import prep_token_gb300 as dp
+    pools = [Pool(*random_case(30, np.random.RandomState(20 + i)), seed=i, page=8) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in pools]
+    state = [p.device() for p in pools]
+    want = [[v.cpu().clone() for v in p.views] for p in pools]
+    torch.cuda.synchronize()
+    for p, d, s in zip(pools, state, streams):
+        with torch.cuda.stream(s):
+            dp.dsa_cache_keep(p.views, *d[:3], p.page, *d[3:])
+    torch.cuda.synchronize()
+    for p, d, w in zip(pools, state, want):
+        p.model([x.numpy() for x in w])
+        assert all(torch.equal(v.cpu(), x) for v, x in zip(p.views, w))
+        assert all(np.array_equal(g.cpu().numpy(), x) for g, x in zip(d, (p.refs, p.table, p.lens)))
+
+
 def test_on_another_stream():
     import prep_token_gb300 as dp
     p = Pool(*random_case(8, np.random.RandomState(7)))
