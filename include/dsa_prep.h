@@ -417,8 +417,9 @@ dsa_status dsa_kv_append(
  * models that cache K and V per kv head with one width for both (multi-head,
  * grouped-query or multi-query attention; a latent cache whose scores and values
  * differ in width is not read).  dsa_kv_append writes the pages.
- * A batch of B sequences mixes chunks of prompts and single tokens.  With G = H / Hkv, query i of sequence b (row query_start[b]
- * + i of q, n_b of them) is the token at
+ * A batch of B sequences mixes chunks of prompts and single tokens.  With
+ * G = H / Hkv, query i of sequence b (row query_start[b] + i of q, n_b of them)
+ * is the token at
  *   pos = context_lens[b] - n_b + i,
  * its keys and values already in the cache, and head h of it sees kv head
  * h / G:
@@ -647,7 +648,8 @@ dsa_status dsa_cache_compact(
  * are kept.
  *
  *   which, drafted, n_kept  int32 [n], n <= DSA_MAX_KEEPS; every row named once.
- *   kept           int32 [n, kept_stride >= max_kept]; NULL if max_kept is 0.
+ *   kept           int32 [n, max_kept], row stride kept_stride >= max_kept, or 0:
+ *                  one list for all; NULL if max_kept is 0.
  *   workspace      dsa_cache_keep_workspace_bytes(n, max_kept) bytes, 16-byte
  *                  aligned, contents scratch.
  * An entry of the list whose row is out of range or was named before, whose

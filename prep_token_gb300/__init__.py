@@ -37,8 +37,8 @@ __all__ = [
     "dsa_cache_copy_pages", "dsa_cache_fork", "dsa_cache_free", "dsa_cache_compact",
     "dsa_cache_fork_workspace_bytes", "dsa_cache_compact_workspace_bytes",
     "dsa_rms_norm", "dsa_rms_norm_fp8", "dsa_kv_append", "prepare_kv_append",
-    "dsa_tree_attention", "prepare_tree_attention", "dsa_cache_keep", "dsa_cache_keep_workspace_bytes", "TokenViews",
-    "index_k_token_views",
+    "dsa_tree_attention", "prepare_tree_attention", "dsa_cache_keep",
+    "dsa_cache_keep_workspace_bytes", "TokenViews", "index_k_token_views",
     "library", "cache_bytes", "cache_views",
     "PreparedCall", "prepare_qk_prepare_store", "prepare_k_prepare_store",
 ]
@@ -1196,7 +1196,7 @@ def dsa_cache_keep(caches, page_refs, block_table, context_lens, page_size, rows
     entries move to the front of the drafts' place; context_lens and the block
     table shrink to them, and the pages behind go back to the pool.  caches: a
     TokenViews, or a list of tensors for one; rows, drafted, n_kept [n] int32,
-    kept [n, most] int32."""
+    kept [n, most] int32 (a list for all of them by expand)."""
     views = caches if isinstance(caches, TokenViews) else TokenViews(caches)
     if stream is None and workspace is None:
         got = _marshal().cache_keep(*views._where, page_refs, block_table, context_lens, page_size,
@@ -1220,7 +1220,7 @@ def dsa_cache_keep(caches, page_refs, block_table, context_lens, page_size, rows
     with _on(dev):
         st = lib.dsa_cache_keep(
             views._bases.buffer_info()[0], views._shapes.buffer_info()[0], len(views), num_pages,
-            *pool, page_size, lists[0], lists[1], kept.data_ptr(), max(kept.stride(0), most), most,
-            lists[2], n, 0, ws, ws_bytes, _err_ptr(err_flags, dev), _stream(stream, dev))
+            *pool, page_size, lists[0], lists[1], kept.data_ptr(), kept.stride(0) if n > 1 else most,
+            most, lists[2], n, 0, ws, ws_bytes, _err_ptr(err_flags, dev), _stream(stream, dev))
     if st != 0:
         raise DsaError(st, "dsa_cache_keep")

@@ -333,7 +333,7 @@ PyObject* cache_keep(PyObject*, PyObject* const* args, Py_ssize_t n) {
       table->stride(0) > cols ? table->stride(0) : cols, ptr_of<int32_t>(lens),
       static_cast<int32_t>(table_rows), page, ptr_of<const int32_t>(rows),
       ptr_of<const int32_t>(drafted), ptr_of<const int32_t>(kept),
-      kept->stride(0) > most ? kept->stride(0) : most, most, ptr_of<const int32_t>(n_kept), c, 0,
+      count > 1 ? kept->stride(0) : most, most, ptr_of<const int32_t>(n_kept), c, 0,
       ws.data_ptr(), need, err, a.stream()));
 }
 

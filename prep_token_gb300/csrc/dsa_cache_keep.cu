@@ -57,7 +57,8 @@ struct KeepParams {
   const int *which, *drafted, *kept, *n_kept;
   long long bt_stride, kept_stride;
   int bt_cols, rows, num_pages, page_size, n, max_kept;
-  int4* moves;  // workspace [n, max_kept]: page and token of an entry, and of its new place; page -1: none
+  int4* moves;  // workspace [n, max_kept]: page and token of an entry and of its new place; page
+                // -1: none
   int* runs;    // workspace [n]: how many moves a row has
   int* err;
 };
@@ -265,8 +266,8 @@ dsa_status dsa_cache_keep(
                ? keep<kFewViews>(bases, shapes, n_views, num_pages, p, checked, s)
                : keep<DSA_MAX_VIEWS>(bases, shapes, n_views, num_pages, p, checked, s);
   };
-  if (n < 0 || n > DSA_MAX_KEEPS || max_kept < 0 || kept_stride < max_kept || rows < 0 ||
-      bt_cols < 0 || bt_stride < bt_cols)
+  if (n < 0 || n > DSA_MAX_KEEPS || max_kept < 0 || (kept_stride != 0 && kept_stride < max_kept) ||
+      rows < 0 || bt_cols < 0 || bt_stride < bt_cols)
     return DSA_ERR_SHAPE;
   if (flags) return DSA_ERR_UNSUPPORTED;
   if (n == 0) return call(true);

@@ -201,6 +201,36 @@ def test_many_views():
     assert p.check() == 0
 
 
+@pytest.mark.parametrize("usual", [True, False])
+@pytest.mark.parametrize("order", ["expanded", "sliced", "overlapping"])
+def test_lists_of_other_strides(order, usual):
+    """One list for all rows by expand, lists out of wider rows; rows that overlap are refused."""
+    import prep_token_gb300 as dp
+    n = 40
+    p = Pool([7 * i for i in range(n)], [12] * n, [[1, 2, 5, 11]] * n, seed=1, shapes=((4, 64), (8,)))
+    d = p.device()
+    if order == "expanded":
+        d[5] = d[5][:1].clone().expand(n, -1)
+    elif order == "sliced":
+        wide = torch.full((n, 9), -3, dtype=torch.int32, device="cuda")
+        wide[:, 2:6] = d[5]
+        d[5] = wide[:, 2:6]
+    else:
+        d[5] = d[5].flatten().as_strided((n, 4), (2, 1))
+    want = [v.cpu().clone() for v in p.views]
+    call = lambda: dp.dsa_cache_keep(  # noqa: E731
+        p.views, *d[:3], p.page, *d[3:], err_flags=p.err,
+        stream=None if usual else torch.cuda.current_stream())
+    if order == "overlapping":
+        with pytest.raises(dp.DsaError, match="SHAPE"):
+            call()
+        return
+    call()
+    assert int(p.err) == p.model([w.numpy() for w in want]) == 0
+    assert all(torch.equal(v.cpu(), w) for v, w in zip(p.views, want))
+    assert all(np.array_equal(g.cpu().numpy(), w) for g, w in zip(d[:3], (p.refs, p.table, p.lens)))
+
+
 def test_without_caches():
     p = Pool(*random_case(6, np.random.RandomState(5)), shapes=())
     assert p.check() == 0

@@ -119,7 +119,7 @@ def _keep(lib, bases=(A,), shapes=((4096, 256, 128, 2, 128),), n_views=None, pag
     (dict(nk=None), 1), (dict(refs=A + 2), 2), (dict(bt=A + 2), 2), (dict(lens=A + 2), 2),
     (dict(which=A + 1), 2), (dict(drafted=A + 2), 2), (dict(kept=A + 2), 2), (dict(nk=A + 2), 2),
     (dict(err=A + 2), 2), (dict(ws=None), 1), (dict(ws=A + 8), 2), (dict(wsb=271), 3),
-    (dict(n=0, refs=None, kept=None), 0)])
+    (dict(ks=-1), 3), (dict(ks=0, ws=None), 1), (dict(n=0, refs=None, kept=None), 0)])
 def test_keep(lib, over, status):
     assert _keep(lib, **over) == status
 
