@@ -138,6 +138,13 @@ struct Args {
   int32_t dtype() const { return type == at::kBFloat16 ? DSA_DTYPE_BF16 : DSA_DTYPE_FP16; }
 };
 
+// Lets other Python threads run while memory is allocated and kernels are launched:
+// both may wait for the GPU, and what it waits for may need them.
+struct NoGil {
+  PyThreadState* const state = PyEval_SaveThread();
+  ~NoGil() { PyEval_RestoreThread(state); }
+};
+
 void* ptr(const at::Tensor* t) { return t ? t->data_ptr() : nullptr; }
 template <class T>
 T* ptr_of(const at::Tensor* t) {
@@ -164,20 +171,24 @@ PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return out_of_the_ordinary();
   const int64_t T = x->size(0), N = x->size(1);
   at::Tensor out, codes, scales, z;
-  if (group) {
-    codes = a.fresh({T, N}, at::kFloat8_e4m3fn);
-    scales = a.fresh({T, (N + group - 1) / group}, bytes ? at::kFloat8_e8m0fnu : at::kFloat);
-  } else {
-    out = a.fresh({T, N}, a.type);
+  dsa_status st;
+  {
+    const NoGil free;
+    if (group) {
+      codes = a.fresh({T, N}, at::kFloat8_e4m3fn);
+      scales = a.fresh({T, (N + group - 1) / group}, bytes ? at::kFloat8_e8m0fnu : at::kFloat);
+    } else {
+      out = a.fresh({T, N}, a.type);
+    }
+    if (res) z = a.fresh({T, N}, a.type);
+    st = g_rms_norm(
+        x->data_ptr(), x->stride(0), ptr(res), stride0(res), res ? z.data_ptr() : nullptr,
+        res ? N : 0, ptr_of<const float>(gamma), static_cast<float>(eps),
+        group ? nullptr : out.data_ptr(), N, group ? codes.data_ptr() : nullptr, N,
+        group ? scales.data_ptr() : nullptr, group ? scales.size(1) : 0,
+        bytes ? DSA_SCALE_UE8M0 : DSA_SCALE_FP32, group ? group : 128, static_cast<int32_t>(T),
+        static_cast<int32_t>(N), a.dtype(), pdl ? DSA_FLAG_PDL : 0u, a.stream());
   }
-  if (res) z = a.fresh({T, N}, a.type);
-  const dsa_status st = g_rms_norm(
-      x->data_ptr(), x->stride(0), ptr(res), stride0(res), res ? z.data_ptr() : nullptr,
-      res ? N : 0, ptr_of<const float>(gamma), static_cast<float>(eps),
-      group ? nullptr : out.data_ptr(), N, group ? codes.data_ptr() : nullptr, N,
-      group ? scales.data_ptr() : nullptr, group ? scales.size(1) : 0,
-      bytes ? DSA_SCALE_UE8M0 : DSA_SCALE_FP32, group ? group : 128, static_cast<int32_t>(T),
-      static_cast<int32_t>(N), a.dtype(), pdl ? DSA_FLAG_PDL : 0u, a.stream());
   if (st != DSA_OK) return status_of(st);
   if (!group && !res) return pack(out);
   PyObject* got = PyTuple_New((group ? 2 : 1) + (res ? 1 : 0));
@@ -226,17 +237,21 @@ PyObject* kv_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     rows = cos->size(0);
   }
   at::Tensor out;
-  if (q) out = a.fresh({T, H, D}, t16);
-  const dsa_status st = g_kv_append(
-      ptr(q), q ? q->stride(0) : 0, q ? q->stride(1) : 0, k->data_ptr(), k->stride(0),
-      k->stride(1), v->data_ptr(), v->stride(0), v->stride(1), ptr_of<const int64_t>(pos),
-      ptr_of<const int64_t>(slots), rope ? ptr_of<const float>(cos) : nullptr,
-      rope ? ptr_of<const float>(sin) : nullptr, cs_stride, rows, ptr_of<const float>(qg),
-      ptr_of<const float>(kg), static_cast<float>(eps), q ? out.data_ptr() : nullptr, H * D, D,
-      kc->data_ptr(), vc->data_ptr(), kc->stride(0), kc->stride(1), kc->stride(2), vc->stride(0),
-      vc->stride(1), vc->stride(2), kc->size(0), static_cast<int32_t>(kc->size(1)),
-      static_cast<int32_t>(T), static_cast<int32_t>(H), static_cast<int32_t>(Hkv),
-      static_cast<int32_t>(D), rope, style, a.dtype(), pdl ? DSA_FLAG_PDL : 0u, err, a.stream());
+  dsa_status st;
+  {
+    const NoGil free;
+    if (q) out = a.fresh({T, H, D}, t16);
+    st = g_kv_append(
+        ptr(q), q ? q->stride(0) : 0, q ? q->stride(1) : 0, k->data_ptr(), k->stride(0),
+        k->stride(1), v->data_ptr(), v->stride(0), v->stride(1), ptr_of<const int64_t>(pos),
+        ptr_of<const int64_t>(slots), rope ? ptr_of<const float>(cos) : nullptr,
+        rope ? ptr_of<const float>(sin) : nullptr, cs_stride, rows, ptr_of<const float>(qg),
+        ptr_of<const float>(kg), static_cast<float>(eps), q ? out.data_ptr() : nullptr, H * D, D,
+        kc->data_ptr(), vc->data_ptr(), kc->stride(0), kc->stride(1), kc->stride(2), vc->stride(0),
+        vc->stride(1), vc->stride(2), kc->size(0), static_cast<int32_t>(kc->size(1)),
+        static_cast<int32_t>(T), static_cast<int32_t>(H), static_cast<int32_t>(Hkv),
+        static_cast<int32_t>(D), rope, style, a.dtype(), pdl ? DSA_FLAG_PDL : 0u, err, a.stream());
+  }
   if (st != DSA_OK) return status_of(st);
   if (!q) Py_RETURN_NONE;
   return pack(out);
@@ -279,20 +294,26 @@ PyObject* tree_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
                 h = static_cast<int32_t>(H), hkv = static_cast<int32_t>(Hkv),
                 d = static_cast<int32_t>(D);
   if (own_scale) scale = std::pow(static_cast<double>(D), -0.5);
-  at::Tensor out = a.fresh({T, H, D}, a.type), lse = a.fresh({T, H}, at::kFloat), ws;
-  const size_t need = g_attention_workspace(t, b, h, hkv, d, most);
-  if (need) ws = a.fresh({static_cast<int64_t>(need)}, at::kByte);
-  const int64_t ts = table->stride(0);
-  const dsa_status st = g_tree_attention(
-      q->data_ptr(), q->stride(0), q->stride(1), kc->data_ptr(), vc->data_ptr(), kc->stride(0),
-      kc->stride(1), kc->stride(2), vc->stride(0), vc->stride(1), vc->stride(2), kc->size(0),
-      static_cast<int32_t>(page), ptr_of<const int32_t>(table),
-      ts > cols || table->size(0) > 1 ? ts : cols, ptr_of<const int32_t>(start),
-      ptr_of<const int32_t>(lens), most, ptr_of<const uint32_t>(mask),
-      static_cast<int32_t>(mask->size(1)), mask->size(0) > 1 ? mask->stride(0) : mask->size(1),
-      static_cast<float>(scale), window, sinks, out.data_ptr(), H * D, D,
-      static_cast<float*>(lse.data_ptr()), t, b, h, hkv, d, a.dtype(), pdl ? DSA_FLAG_PDL : 0u,
-      need ? ws.data_ptr() : nullptr, need, err, a.stream());
+  at::Tensor out, lse, ws;
+  dsa_status st;
+  {
+    const NoGil free;
+    out = a.fresh({T, H, D}, a.type);
+    lse = a.fresh({T, H}, at::kFloat);
+    const size_t need = g_attention_workspace(t, b, h, hkv, d, most);
+    if (need) ws = a.fresh({static_cast<int64_t>(need)}, at::kByte);
+    const int64_t ts = table->stride(0);
+    st = g_tree_attention(
+        q->data_ptr(), q->stride(0), q->stride(1), kc->data_ptr(), vc->data_ptr(), kc->stride(0),
+        kc->stride(1), kc->stride(2), vc->stride(0), vc->stride(1), vc->stride(2), kc->size(0),
+        static_cast<int32_t>(page), ptr_of<const int32_t>(table),
+        ts > cols || table->size(0) > 1 ? ts : cols, ptr_of<const int32_t>(start),
+        ptr_of<const int32_t>(lens), most, ptr_of<const uint32_t>(mask),
+        static_cast<int32_t>(mask->size(1)), mask->size(0) > 1 ? mask->stride(0) : mask->size(1),
+        static_cast<float>(scale), window, sinks, out.data_ptr(), H * D, D,
+        static_cast<float*>(lse.data_ptr()), t, b, h, hkv, d, a.dtype(), pdl ? DSA_FLAG_PDL : 0u,
+        need ? ws.data_ptr() : nullptr, need, err, a.stream());
+  }
   if (st != DSA_OK) return status_of(st);
   PyObject* got = PyTuple_New(2);
   if (!got) return nullptr;
@@ -326,15 +347,20 @@ PyObject* cache_keep(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return out_of_the_ordinary();
   const int32_t c = static_cast<int32_t>(count), most = static_cast<int32_t>(kept->size(1));
   const size_t need = g_keep_workspace(c, most);
-  const at::Tensor ws = a.fresh({static_cast<int64_t>(need ? need : 1)}, at::kByte);
-  return status_of(g_cache_keep(
-      reinterpret_cast<void* const*>(bases), reinterpret_cast<const int64_t*>(shapes), views,
-      refs->size(0), ptr_of<int32_t>(refs), ptr_of<int32_t>(table), static_cast<int32_t>(cols),
-      table->stride(0) > cols ? table->stride(0) : cols, ptr_of<int32_t>(lens),
-      static_cast<int32_t>(table_rows), page, ptr_of<const int32_t>(rows),
-      ptr_of<const int32_t>(drafted), ptr_of<const int32_t>(kept),
-      count > 1 ? kept->stride(0) : most, most, ptr_of<const int32_t>(n_kept), c, 0,
-      ws.data_ptr(), need, err, a.stream()));
+  dsa_status st;
+  {
+    const NoGil free;
+    const at::Tensor ws = a.fresh({static_cast<int64_t>(need ? need : 1)}, at::kByte);
+    st = g_cache_keep(
+        reinterpret_cast<void* const*>(bases), reinterpret_cast<const int64_t*>(shapes), views,
+        refs->size(0), ptr_of<int32_t>(refs), ptr_of<int32_t>(table), static_cast<int32_t>(cols),
+        table->stride(0) > cols ? table->stride(0) : cols, ptr_of<int32_t>(lens),
+        static_cast<int32_t>(table_rows), page, ptr_of<const int32_t>(rows),
+        ptr_of<const int32_t>(drafted), ptr_of<const int32_t>(kept),
+        count > 1 ? kept->stride(0) : most, most, ptr_of<const int32_t>(n_kept), c, 0,
+        ws.data_ptr(), need, err, a.stream());
+  }
+  return status_of(st);
 }
 
 // The addresses of the C entry points, in the order of the pointers above.

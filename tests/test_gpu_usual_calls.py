@@ -162,3 +162,32 @@ def test_on_the_current_stream_and_in_a_graph():
         t.view(torch.uint8).zero_()
     graph.replay()
     same(got, want)
+
+
+def test_threads():
+    """Calls of several Python threads at once, each on a stream of its own."""
+    import threading
+
+    import prep_token_gb300 as dp
+    sets = [inputs(64 + i, 1024, BF, 10 + i) for i in range(4)]
+    want = [dp.dsa_rms_norm_fp8(x, gamma, 1e-6, residual=res) for x, res, gamma in sets]
+    torch.cuda.synchronize()
+    got = [None] * len(sets)
+
+    def work(i):
+        x, res, gamma = sets[i]
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            got[i] = [dp.dsa_rms_norm_fp8(x, gamma, 1e-6, residual=res) for _ in range(100)]
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(sets))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+        assert not t.is_alive()
+    for w, results in zip(want, got):
+        assert len(results) == 100
+        for g in results:
+            same(g, w)
