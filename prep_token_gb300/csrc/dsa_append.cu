@@ -403,7 +403,8 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
     }
     if (left == 0) break;
     skip = 0;
-    if (kind++ == last_kind) {  // the next token: the one behind it takes the last one's place for cos and sin
+    if (kind++ == last_kind) {
+      // the next token: the one behind it takes the last one's place for cos and sin
       kind = p.q_passes > 0 ? 0 : 1;
       __syncwarp();  // which every lane has read
       ++t;
@@ -537,8 +538,10 @@ extern "C" dsa_status dsa_kv_append(
   const bool bf16 = dtype == DSA_DTYPE_BF16;
   cudaError_t e;
   if (head_dim == 64)
-    e = bf16 ? launch<true, 64>(p, rope_style, stream_kernel, cfg) : launch<false, 64>(p, rope_style, stream_kernel, cfg);
+    e = bf16 ? launch<true, 64>(p, rope_style, stream_kernel, cfg)
+             : launch<false, 64>(p, rope_style, stream_kernel, cfg);
   else
-    e = bf16 ? launch<true, 128>(p, rope_style, stream_kernel, cfg) : launch<false, 128>(p, rope_style, stream_kernel, cfg);
+    e = bf16 ? launch<true, 128>(p, rope_style, stream_kernel, cfg)
+             : launch<false, 128>(p, rope_style, stream_kernel, cfg);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_LAUNCH;
 }

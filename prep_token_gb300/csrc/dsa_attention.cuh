@@ -1745,7 +1745,8 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, dsa_paged_attention_kernel<D, BF16, QT, TREE>, tq, tk, tv, p);
+  cudaError_t e =
+      cudaLaunchKernelEx(&cfg, dsa_paged_attention_kernel<D, BF16, QT, TREE>, tq, tk, tv, p);
   if (e != cudaSuccess || !p.split) return e;
   cfg.gridDim = dim3(kJoinCtas);
   cfg.blockDim = dim3(32 * kJoinWarps);
@@ -1803,7 +1804,8 @@ dsa_status attend(
     int64_t v_stride_page, int64_t v_stride_token, int64_t v_stride_head, int64_t num_pages,
     int32_t page_size, const int32_t* block_table, int64_t bt_stride, const int32_t* query_start,
     const int32_t* context_lens, int32_t max_context,
-    const uint32_t* tree_mask, int32_t mask_words, int64_t mask_stride, float scale, int32_t window, int32_t sinks,
+    const uint32_t* tree_mask, int32_t mask_words, int64_t mask_stride, float scale,
+    int32_t window, int32_t sinks,
     void* out, int64_t out_stride_t, int64_t out_stride_h, float* lse, int32_t T, int32_t B,
     int32_t H, int32_t Hkv, int32_t head_dim, int32_t dtype, uint32_t flags, void* workspace,
     size_t workspace_bytes, int32_t* err_flags, void* stream) {

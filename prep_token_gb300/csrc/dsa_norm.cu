@@ -178,7 +178,8 @@ extern "C" dsa_status dsa_rms_norm(
     int64_t out_stride, void* codes, int64_t codes_stride, void* scales, int64_t scales_stride,
     int32_t scale_format, int32_t group, int32_t T, int32_t N, int32_t dtype, uint32_t flags,
     void* stream) {
-  if (T < 0 || T > (1 << 30) || N < 1 || N % 8 || N > 8 * kMaxPieces * kMaxRowThreads) return DSA_ERR_SHAPE;
+  if (T < 0 || T > (1 << 30) || N < 1 || N % 8 || N > 8 * kMaxPieces * kMaxRowThreads)
+    return DSA_ERR_SHAPE;
   if (dtype != DSA_DTYPE_BF16 && dtype != DSA_DTYPE_FP16) return DSA_ERR_UNSUPPORTED;
   if (flags & ~static_cast<uint32_t>(DSA_FLAG_PDL)) return DSA_ERR_UNSUPPORTED;
   if (!(eps > 0.0f) || !std::isfinite(eps)) return DSA_ERR_UNSUPPORTED;

@@ -46,26 +46,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack2<BF16>(w[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-}
-
-template <bool BF16>
 __device__ __forceinline__ void unpack8(const uint4& v, float2 (&x)[4]) {
   x[0] = unpack2<BF16>(v.x), x[1] = unpack2<BF16>(v.y);
   x[2] = unpack2<BF16>(v.z), x[3] = unpack2<BF16>(v.w);
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]), pack2<BF16>(x[4], x[5]),
-                    pack2<BF16>(x[6], x[7]));
 }
 
 template <bool BF16>

@@ -9,7 +9,8 @@ extern "C" dsa_status dsa_tree_attention(
     int64_t v_stride_page, int64_t v_stride_token, int64_t v_stride_head, int64_t num_pages,
     int32_t page_size, const int32_t* block_table, int64_t bt_stride, const int32_t* query_start,
     const int32_t* context_lens, int32_t max_context,
-    const uint32_t* tree_mask, int32_t mask_words, int64_t mask_stride, float scale, int32_t window, int32_t sinks,
+    const uint32_t* tree_mask, int32_t mask_words, int64_t mask_stride, float scale,
+    int32_t window, int32_t sinks,
     void* out, int64_t out_stride_t, int64_t out_stride_h, float* lse, int32_t T, int32_t B,
     int32_t H, int32_t Hkv, int32_t head_dim, int32_t dtype, uint32_t flags, void* workspace,
     size_t workspace_bytes, int32_t* err_flags, void* stream) {
