@@ -61,9 +61,11 @@
 // division of the work is a product and a scan (TreeWork).  Measured: 64 x up to 16
 // drafts over up to 8192 keys, 64 heads on 8, 1.2 GB: 206 us (5.9 TB/s); 4 x 60 over
 // 32768, 32 on 4: 119 us (1080 TFLOP/s, each tile pair reads the keys anew);
-// 8 drafts over 1000: 14.7 us, of which the first scores take 4, softmax, values and
+// 8 drafts over 1000: 14.1 us, of which the first scores take 4, softmax, values and
 // parts 3, launches and join the rest; 24 x 32 with a window of 1024, 16 heads of 64 on
-// as many: 44 us, 368 items of ten blocks in two rounds of 304.
+// as many: 41 us, 368 items of ten blocks in two rounds of 304, the 32 rows' one warp
+// 1750 of a block's 2500 cycles.  Copies of those rows, a quarter of the keys to each
+// warp: 1300, latency else, but joining them took 2700 more at an item's end (47 us).
 //
 // Every wait is bounded in time; TMEM is always released before exit.
 #ifndef DSA_ATTENTION_CUH
@@ -1098,8 +1100,15 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
         // tiles all of it is done before S is waited for, as V comes sooner.
         // That takes a ring so long that the unit before V's in its place has
         // landed by now: a barrier's parity tells only its last two phases apart.
+        // Trees with one tile do it behind the first half of P, so that the softmax
+        // does not wait for V, and ask last which odd keys a row sees: 24 x 32 drafts
+        // over a window of 1024 44 -> 41 us, 8 over 1000 14.7 -> 14.0 (chunks of
+        // prompts, whose warps all have rows, lose by it: 95 -> 100).
         static_assert(QT == 1 || S >= 4 * kP, "a place of V is looked at too early");
-        if (!(key0 + kKeys <= every_hi && (key0 >= every_lo || key0 + kKeys <= p.sinks))) {
+        constexpr bool kLate = TREE && QT == 1;
+        const bool partly =
+            !(key0 + kKeys <= every_hi && (key0 >= every_lo || key0 + kKeys <= p.sinks));
+        auto look = [&]() {
           if (j == 0) {
             const int key = key0 + row;
             bool odd = false;
@@ -1140,15 +1149,25 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
               mbar_arrive(checked(edges));
             }
           }
+        };
+        // which odd keys this row sees, once all have been looked at
+        auto odd_seen = [&]() {
           ok = __all_sync(kFull, ok && wait_soon(checked(edges), (edges >> 2) & 1, abort_flag));
-          if (!ok) break;
+          if (!ok) return;
+          uint32_t odd[4], any = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int at = key0 + 32 * i;
-            const uint32_t mask = odd_keys[4 * (edges & 3) + i];
-            if (mask & keys_seen(at)) spoiled = true;
+          for (int i = 0; i < 4; ++i) any |= odd[i] = odd_keys[4 * (edges & 3) + i];
+          if (!TREE || any != 0) {  // a mask's bits are not asked for in vain
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (odd[i] & keys_seen(key0 + 32 * i)) spoiled = true;
           }
           ++edges;
+        };
+        if (!kLate && partly) {
+          look();
+          odd_seen();
+          if (!ok) break;
         }
         if (QT == 2 && !scores_done()) break;
         const uint32_t t_s = tmem_s(at_s) + lanes;
@@ -1236,9 +1255,14 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
             tmem_st16(t_s + 32 * half + 16, w + 16);
             tmem_wait_st();
           }
+          if (kLate && half == 0 && partly) look();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(pready(j, half, block));
+        }
+        if (kLate && partly) {
+          odd_seen();
+          if (!ok) break;
         }
         ++block;
         if (kLook == 3) at_s = at_s == 0 ? 2 : at_s - 1;
