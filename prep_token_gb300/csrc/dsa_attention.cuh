@@ -60,7 +60,7 @@
 // differs else is that all tiles of a sequence see the same keys, so that the
 // division of the work is a product and a scan (TreeWork).  Measured: 64 x up to 16
 // drafts over up to 8192 keys, 64 heads on 8, 1.2 GB: 206 us (5.9 TB/s); 4 x 60 over
-// 32768, 32 on 4: 119 us (1080 TFLOP/s, each tile pair reads the keys anew);
+// 32768, 32 on 4: 112 us (1150 TFLOP/s);
 // 8 drafts over 1000: 14.1 us, of which the first scores take 4, softmax, values and
 // parts 3, launches and join the rest; 24 x 32 with a window of 1024, 16 heads of 64 on
 // as many: 41 us, 368 items of ten blocks in two rounds of 304, the 32 rows' one warp
@@ -564,6 +564,17 @@ __device__ __forceinline__ int cta_of(const TreeShare& s, unsigned at) {
   return static_cast<int>(at < longer ? at / (s.each + 1) : s.extra + (at - longer) / s.each);
 }
 
+// The tiles of a tree see the same keys, and in a CTA's share time goes by the block:
+// the key block at which tile t starts (and goes round), so that what its neighbours
+// read at the same time is the same and comes from L2.  The same for all CTAs.  4 x 60
+// drafts over 32768, two tile pairs each: 117 -> 112 us.  With one tile per CTA, which
+// few calls of more than one tile take, its own instructions cost others 2%.
+__device__ __forceinline__ int first_of_tile(const TreeShare& s, int t, int blocks) {
+  if (t == 0) return 0;
+  const unsigned each = max(1u, s.each + (2 * s.extra >= gridDim.x ? 1 : 0));
+  return static_cast<unsigned>(t) * blocks % each % blocks;
+}
+
 // seek for trees: `want` does not fall from call to call.
 __device__ __forceinline__ bool seek_trees(const AParams& p, TreeWork& w, Cursor& c, unsigned want,
                                            long long budget) {
@@ -641,7 +652,8 @@ struct ASmem {
   static constexpr int kOffTurn = kOffRing + kStages * kUnitBytes;
   static constexpr int kOffSeg = kOffTurn + kTurnBytes;
   static constexpr int kOffOdd = kOffSeg + kSegments * static_cast<int>(sizeof(Segment));
-  static constexpr int kOffBar = kOffOdd + 4 * 4 * 4;
+  static constexpr int kOffFirst = kOffOdd + 4 * 4 * 4;  // of the segments, see first_of_tile
+  static constexpr int kOffBar = kOffFirst + 4 * kSegments;
   // barriers: full[S], empty[S], qfull, qempty, drain, segment[4], then per
   // query tile sfull[2], pready[2][2], ohalf, oblock, ofull; checked[4]
   static constexpr int kBars = 2 * kStages + 3 + kSegments + 9 * QT + 4;
@@ -668,6 +680,7 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
   using L = ASmem<D, QT>;
   constexpr int S = L::kStages;
   constexpr int kP = L::kPanels;
+  constexpr bool kRound = TREE && QT == 2;  // a tile's keys go round from some block on
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {  // the swizzled tiles need this alignment
@@ -700,6 +713,7 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
   volatile uint32_t* const odd_keys = reinterpret_cast<volatile uint32_t*>(smem + L::kOffOdd);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffAbort);
   Segment* const segments = reinterpret_cast<Segment*>(smem + L::kOffSeg);
+  int* const firsts = reinterpret_cast<int*>(smem + L::kOffFirst);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
@@ -781,6 +795,7 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
       uint32_t phase = 1;                    // parity of the place's last release
       bool ok = true;
       int begin = 0, end = 0, hi = 0, lo = 0, h = 0, sink_blocks = 0, skip = 0;  // of the segment
+      int first = 0, blocks = 0;
       const int* table = p.block_table;
       // box l of a block: its page, -1 if no row sees any of its keys, -2 if
       // the table names no page of the pool for it
@@ -790,7 +805,10 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
         const int page = __ldg(table + key / p.page);
         return page >= 0 && page < p.num_pages ? page : -2;
       };
-      auto first_key = [&](int k) { return (k < sink_blocks ? k : k + skip) * kKeys; };
+      auto first_key = [&](int k) {
+        if (kRound && (k += first) >= blocks) k -= blocks;
+        return (k < sink_blocks ? k : k + skip) * kKeys;
+      };
       for (int seg = 0; ok; ++seg) {
         int page = -1;
         if (keys) {
@@ -808,6 +826,8 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
           if (TREE) {  // the first block's pages are on their way while the segment is published
             begin = c.begin, end = more ? c.end : -1, hi = tile.hi, lo = tile.lo, h = c.h;
             sink_blocks = tile.sink_blocks, skip = tile.main_block - sink_blocks;
+            blocks = tile.blocks;
+            if constexpr (kRound) first = p.split && more ? first_of_tile(share, c.t, blocks) : 0;
             table = p.block_table + c.b * p.bt_stride;
             if (more) page = lookup(first_key(begin));
           }
@@ -826,6 +846,7 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
             g.h = c.h;
             g.b = c.b;
             g.last_cta = -1;
+            if (kRound) firsts[seg % kSegments] = first;
             if (more && p.split && c.begin == 0 && c.end < tile.blocks)
               g.last_cta = cta_of(share, share.end - 1 + (tile.blocks - c.end));
             mbar_arrive(segment_ready(seg));
@@ -847,6 +868,7 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
           const Segment& g = segments[seg % kSegments];
           begin = g.begin, end = g.end, hi = g.hi, lo = g.lo, h = g.h;
           sink_blocks = g.sink_blocks, skip = g.main_block - sink_blocks;
+          if (kRound) first = firsts[seg % kSegments], blocks = g.blocks;
           table = p.block_table + g.b * p.bt_stride;
           if (end >= 0) page = lookup(first_key(begin));
         }
@@ -1083,8 +1105,11 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
       const int seen_hi = g.hi, seen_lo = g.lo;  // by some row of the item
       const int every_hi = TREE ? g.pos0 : g.pos0 + 1;  // by every row
       const int every_lo = p.window ? g.pos0 + (TREE ? drafts : g.tokens) - p.window : 0;
+      int place = begin;  // of the k-th block
+      if (kRound && (place += firsts[seg % kSegments]) >= g.blocks) place -= g.blocks;
       for (int k = begin; k < end; ++k) {
-        const int key0 = (k < sink_blocks ? k : k + skip) * kKeys;
+        const int at_k = kRound ? place : k;
+        const int key0 = (at_k < sink_blocks ? at_k : at_k + skip) * kKeys;
         auto scores_done = [&]() {
           ok = __all_sync(kFull, wait_soon(sfull(j, block), turn(block), abort_flag));
           tc_fence_after();
@@ -1266,6 +1291,7 @@ __global__ void __launch_bounds__(Shape<QT>::kThreads, 2 / QT)
         }
         ++block;
         if (kLook == 3) at_s = at_s == 0 ? 2 : at_s - 1;
+        if (kRound && ++place == g.blocks) place = 0;
         slot += 2 * kP;
         if (slot >= S) slot -= S, phase ^= 1;
       }

@@ -79,6 +79,14 @@ def test_long_contexts_are_cut_and_joined():
         go([16, 1], [30000, 5], 8, 1, 64, masks=masks, poison=False, seed=2)
 
 
+@pytest.mark.parametrize("window,sinks", [(0, 0), (5000, 300)])
+def test_tiles_that_go_round(window, sinks):
+    """Several tiles of a sequence over long contexts, each from a key block of its own on."""
+    go([200, 3, 90], [17000, 200, 9001], 8, 1, 128, masks="any", window=window, sinks=sinks, seed=1)
+    go([130, 128], [20000, 12345], 16, 2, 64, masks="tree", window=window, sinks=sinks, seed=2)
+    go([70], [70 + 128 * 300], 8, 1, 64, masks="any", window=window, sinks=sinks, poison=False, seed=3)
+
+
 @pytest.mark.parametrize("batch,dim", [(33, 128), (70, 64), (100, 128)])
 def test_many_sequences_cut(batch, dim):
     """More sequences than a warp has lanes, idle ones and unequal ones among them."""
