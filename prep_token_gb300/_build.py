@@ -58,7 +58,7 @@ def _binding_command(out: str) -> list[str]:
             "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             "-o", out, BINDING_SOURCE, "-L", os.path.join(at, "lib"),
-            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:

@@ -1,7 +1,7 @@
 // The marshalling of the calls that a decode step makes eagerly, in their usual
 // form: every output allocated here, the current stream, tensors on the current
 // device.  What a call of a few microseconds waits for is its arguments' way
-// from Python to C: 20 to 35 us through ctypes, 5 to 8 here.
+// from Python to C: 20 to 35 us through ctypes, 3 to 9 here.
 //
 // Each function checks what the Python binding checks and returns NotImplemented
 // where anything is out of the ordinary; the caller then takes the Python way,
@@ -10,12 +10,13 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <optional>
 
 #include "dsa_prep.h"
 
@@ -132,8 +133,9 @@ struct Args {
     return true;
   }
   void* stream() const { return c10::cuda::getCurrentCUDAStream(device.index()).stream(); }
+  // As at::empty, but not through the dispatcher, which takes 0.2 us for each.
   at::Tensor fresh(at::IntArrayRef shape, at::ScalarType t) const {
-    return at::empty(shape, at::TensorOptions().device(device).dtype(t));
+    return at::Tensor(at::detail::empty_cuda(shape, t, device, std::nullopt));
   }
   int32_t dtype() const { return type == at::kBFloat16 ? DSA_DTYPE_BF16 : DSA_DTYPE_FP16; }
 };
