@@ -1798,7 +1798,9 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   cudaError_t e =
       cudaLaunchKernelEx(&cfg, dsa_paged_attention_kernel<D, BF16, QT, TREE>, tq, tk, tv, p);
   if (e != cudaSuccess || !p.split) return e;
-  cfg.gridDim = dim3(kJoinCtas);
+  // no more CTAs than rows: one token over 1000 keys 14.3 -> 14.0 us
+  const long long rows = static_cast<long long>(p.T) * p.Hkv * p.G;
+  cfg.gridDim = dim3(rows < kJoinCtas ? static_cast<unsigned>(rows) : kJoinCtas);
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
