@@ -656,8 +656,15 @@ dsa_status dsa_cache_compact(
  * drafts pass the row's length, whose length passes the table, or whose kept
  * are more than max_kept or drafted, not ascending or not among the drafts sets
  * DSA_DEVERR_ROW and changes nothing.  An entry on a page outside the pool sets
- * DSA_DEVERR_SLOT and is not moved.  The pages of entries that are written must be the
- * row's own (after dsa_cache_fork they are).
+ * DSA_DEVERR_SLOT and is not moved.
+ * A page that entries move to must be the row's own: where its page_refs is not 1
+ * before the call, DSA_DEVERR_REFS is set and nothing of the row changes.  A row that
+ * was forked before it was drafted into owns all of them (the fork gave it the page
+ * it ended in); one that was forked with drafts pending shares the whole pages among
+ * theirs with its copy, and neither can be kept while both are there, but where the
+ * kept drafts stay in place.  The page that a row then ends in may still be another
+ * row's as well: it is not to be appended to before that one has gone.  With no views
+ * no entry moves and no count is asked for.
  */
 #define DSA_MAX_VIEWS 256
 #define DSA_MAX_KEEPS 1024

@@ -11,10 +11,13 @@
 // A cache is described by the addresses of its entries: token t of page p at
 // base + p * page + t * token + h * head for each of its heads, `bytes` each.
 //
-// The first kernel, a CTA to a row, checks the list, writes where the entries
-// move to the workspace, and then changes the row's table and length, which
-// nobody else reads.  The second, a CTA to a row and a cache, moves: what it
-// waits for is one read of the workspace and one of the entries.
+// The first kernel, a CTA to a row, checks the list and the counts of the pages
+// that entries move to, and writes where they move to the workspace.  The second,
+// a CTA to a row and a cache, moves: what it waits for is one read of the workspace
+// and one of the entries.  One CTA more per row changes its table, counts and
+// length: behind the first kernel, so that no row's check depends on which pages
+// another row of the list has given back by then, and none is found its own while
+// that row's entries still move.  Without caches the first kernel does it.
 //
 // Bound: the moved bytes where rows and layers are many, two launches and their
 // chains of dependent reads where they are few.  Measured: up to 8 of up to 32
@@ -59,7 +62,7 @@ struct KeepParams {
   int bt_cols, rows, num_pages, page_size, n, max_kept;
   int4* moves;  // workspace [n, max_kept]: page and token of an entry and of its new place; page
                 // -1: none
-  int* runs;    // workspace [n]: how many moves a row has
+  int* runs;    // workspace [n]: how many moves a row has; -1: it stays as it is
   int* err;
 };
 
@@ -67,10 +70,33 @@ __device__ __forceinline__ void report(int* err, int bit) {
   if (err) atomicOr(err, bit);
 }
 
-// One CTA per entry of the list.
+// A row's length becomes `shorter`, and its pages behind that go back; all threads of a
+// CTA call it.
+__device__ __forceinline__ void shrink(const KeepParams& p, int row, int length, int shorter) {
+  int* const entry = p.table + row * p.bt_stride;
+  auto blocks = [&](int tokens) {
+    return static_cast<int>((static_cast<long long>(tokens) + p.page_size - 1) / p.page_size);
+  };
+  for (int j = blocks(shorter) + threadIdx.x; j < blocks(length); j += kThreads) {
+    const int e = entry[j];
+    if (e < 0) continue;
+    entry[j] = -1;
+    if (e >= p.num_pages) {
+      report(p.err, DSA_DEVERR_SLOT);
+    } else if (atomicSub(p.refs + e, 1) <= 0) {
+      atomicAdd(p.refs + e, 1);
+      report(p.err, DSA_DEVERR_REFS);
+    }
+  }
+  if (threadIdx.x == 0) p.lens[row] = shorter;
+}
+
+// One CTA per entry of the list.  MOVES: the second kernel follows; else there is
+// nothing to move, and the row shrinks here.
+template <bool MOVES>
 __global__ void __launch_bounds__(kThreads) dsa_cache_keep_plan_kernel(const KeepParams p) {
   const int i = blockIdx.x;
-  grid_launch_dependents();  // the second kernel's CTAs start, and wait for this one's end
+  if (MOVES) grid_launch_dependents();  // the second kernel's CTAs start, and wait for this one's end
   const int row = __ldg(p.which + i), d = __ldg(p.drafted + i), count = __ldg(p.n_kept + i);
   const int* const list = p.kept + i * p.kept_stride;
   bool bad = row < 0 || row >= p.rows || d < 0 || count < 0 || count > p.max_kept || count > d;
@@ -89,13 +115,18 @@ __global__ void __launch_bounds__(kThreads) dsa_cache_keep_plan_kernel(const Kee
   if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0) {
       report(p.err, DSA_DEVERR_ROW);
-      p.runs[i] = 0;
+      if (MOVES) p.runs[i] = -1;
     }
     return;
   }
   const int before = length - d;
-  int* const entry = p.table + row * p.bt_stride;
+  if (!MOVES) {
+    shrink(p, row, length, before + count);
+    return;
+  }
+  const int* const entry = p.table + row * p.bt_stride;
   int still = 0;  // entries that stay, all of them in front
+  bool shared = false;  // an entry would go to a page that is not the row's own
   int4* const moves = p.moves + static_cast<long long>(i) * p.max_kept;
   for (int j0 = 0; j0 < count; j0 += kThreads) {
     const int j = j0 + threadIdx.x;
@@ -105,29 +136,18 @@ __global__ void __launch_bounds__(kThreads) dsa_cache_keep_plan_kernel(const Kee
       const int from = before + a, to = before + j;
       const int fp = entry[from / p.page_size], tp = entry[to / p.page_size];
       const bool ok = fp >= 0 && fp < p.num_pages && tp >= 0 && tp < p.num_pages;
-      if (!ok) report(p.err, DSA_DEVERR_SLOT);
+      if (!ok)
+        report(p.err, DSA_DEVERR_SLOT);
+      else
+        shared = shared || p.refs[tp] != 1;
       moves[j - still] = make_int4(ok ? fp : -1, from % p.page_size, tp, to % p.page_size);
     }
   }
-  if (threadIdx.x == 0) p.runs[i] = count - still;
-  // the table has been read
-  const int shorter = before + count;
-  auto blocks = [&](int tokens) {
-    return static_cast<int>((static_cast<long long>(tokens) + p.page_size - 1) / p.page_size);
-  };
-  __syncthreads();
-  for (int j = blocks(shorter) + threadIdx.x; j < blocks(length); j += kThreads) {
-    const int e = entry[j];
-    if (e < 0) continue;
-    entry[j] = -1;
-    if (e >= p.num_pages) {
-      report(p.err, DSA_DEVERR_SLOT);
-    } else if (atomicSub(p.refs + e, 1) <= 0) {
-      atomicAdd(p.refs + e, 1);
-      report(p.err, DSA_DEVERR_REFS);
-    }
+  shared = __syncthreads_or(shared);
+  if (threadIdx.x == 0) {
+    if (shared) report(p.err, DSA_DEVERR_REFS);
+    p.runs[i] = shared ? -1 : count - still;
   }
-  if (threadIdx.x == 0) p.lens[row] = shorter;
 }
 
 template <class V>
@@ -149,24 +169,33 @@ __device__ __forceinline__ void move_columns(const View& view, const longlong2* 
   }
 }
 
-// blockIdx.x: the cache; blockIdx.y: the entry of the list.  The first moves are
-// read beside their number.
+// blockIdx.x: the cache, and behind the caches the row's table; blockIdx.y: the entry
+// of the list.  The first moves are read beside their number.
 template <int CAP>
 __global__ void __launch_bounds__(kThreads)
-    dsa_cache_keep_kernel(const __grid_constant__ Views<CAP> vs, const int4* moves,
-                          const int* runs, int max_kept) {
+    dsa_cache_keep_kernel(const __grid_constant__ Views<CAP> vs, const KeepParams p) {
   __shared__ longlong2 at[kThreads];  // from and to, in bytes; from < 0: not moved
-  const View view = vs.v[blockIdx.x];
   const int i = blockIdx.y;
+  if (blockIdx.x + 1 == gridDim.x) {
+    // the lists are older than the first kernel, which changes nothing that is read here
+    const int row = __ldg(p.which + i), d = __ldg(p.drafted + i), count = __ldg(p.n_kept + i);
+    grid_dependency_wait();
+    if (p.runs[i] < 0) return;
+    const int length = p.lens[row];
+    __syncthreads();  // before one thread changes it
+    shrink(p, row, length, length - d + count);
+    return;
+  }
+  const View view = vs.v[blockIdx.x];
   const long long bits = reinterpret_cast<long long>(view.base) | view.page | view.token |
                          view.head | view.bytes;
-  moves += static_cast<long long>(i) * max_kept;
+  const int4* const moves = p.moves + static_cast<long long>(i) * p.max_kept;
   grid_dependency_wait();
-  const int n = runs[i];
+  const int n = p.runs[i];
   for (int j0 = 0; j0 == 0 || j0 < n; j0 += kThreads) {
     if (j0 > 0) __syncthreads();  // the step before is done with `at`
     const int j = j0 + threadIdx.x;
-    if (j < max_kept) {
+    if (j < p.max_kept) {
       const int4 m = moves[j];
       at[threadIdx.x] =
           m.x < 0 ? make_longlong2(-1, -1)
@@ -219,12 +248,17 @@ dsa_status keep(void* const* bases, const int64_t* shapes, int32_t n_views, int6
   Views<CAP> vs;
   const dsa_status st = read_views<CAP>(bases, shapes, n_views, num_pages, p.page_size, &vs);
   if (st != DSA_OK || checked) return st;
-  dsa_cache_keep_plan_kernel<<<static_cast<unsigned>(p.n), kThreads, 0, s>>>(p);
+  const unsigned rows = static_cast<unsigned>(p.n);
+  const bool moves = n_views > 0 && p.max_kept > 0;
+  if (moves)
+    dsa_cache_keep_plan_kernel<true><<<rows, kThreads, 0, s>>>(p);
+  else
+    dsa_cache_keep_plan_kernel<false><<<rows, kThreads, 0, s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return DSA_ERR_LAUNCH;
-  if (n_views == 0 || p.max_kept == 0) return DSA_OK;
+  if (!moves) return DSA_OK;
   // waits for the first one's memory before it reads anything
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(n_views), static_cast<unsigned>(p.n));
+  cfg.gridDim = dim3(static_cast<unsigned>(n_views) + 1, rows);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -232,9 +266,7 @@ dsa_status keep(void* const* bases, const int64_t* shapes, int32_t n_views, int6
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, dsa_cache_keep_kernel<CAP>, vs,
-                                           static_cast<const int4*>(p.moves),
-                                           static_cast<const int*>(p.runs), p.max_kept);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, dsa_cache_keep_kernel<CAP>, vs, p);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_LAUNCH;
 }
 
