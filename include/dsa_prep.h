@@ -373,8 +373,9 @@ dsa_status dsa_rms_norm(
  *   x *= gamma / sqrt(mean(x^2) + norm_eps)       (where q_gamma or k_gamma is given)
  *   (a, b) -> (a c - b s, b c + a s) for the pairs of x[0:rope_dim), with the
  *     pairs and frequencies of dsa_indexer_qk_prepare_store
- * rounded once.  k and v rows go to slot out_cache_loc[t] of their caches (slot
- * s is token s % page_size of page s / page_size), q rows to q_out.
+ * rounded once (a norm's squares are summed in fp32, as dsa_rms_norm's are).  k and v
+ * rows go to slot out_cache_loc[t] of their caches (slot s is token s % page_size
+ * of page s / page_size), q rows to q_out.
  *
  *   q              bf16 or fp16 (dtype) [T, H, head_dim]; H may be 0 (K and V
  *                  only), then q and q_out may be NULL.

@@ -181,12 +181,26 @@ __device__ __forceinline__ void turn_row(uint4& u, uint4& w, const Turn& r,
   // a piece with neither stays as it is, NaN and all
   const bool first = at.turns_first || (NORM && norm), second = at.turns_second || (NORM && norm);
   if (!first || !active) return;  // without the first nor does the second
+  if (NORM && rs.x == 0.0f) {
+    // The row holds an infinity (or its squares pass fp32): that becomes NaN, what is
+    // finite 0.  Places that do not turn are no pairs: there b * -0 would make a finite
+    // value NaN beside an infinite one.
+    const float2 none = make_float2(0.0f, 0.0f);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 a = x[i], b = y[i];
-    x[i] = __ffma2_rn(a, r.xx[i], __fmul2_rn(b, r.xy[i]));
-    y[i] = __ffma2_rn(b, r.yy[i], __fmul2_rn(a, r.yx[i]));
-    if (NORM) x[i] = __fmul2_rn(x[i], rs), y[i] = __fmul2_rn(y[i], rs);
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = __fmul2_rn(x[i], rs), b = __fmul2_rn(y[i], rs);
+      const bool pair = i < 2 || STYLE == DSA_ROPE_NEOX ? at.turns_first : at.turns_second;
+      x[i] = __ffma2_rn(a, r.xx[i], pair ? __fmul2_rn(b, r.xy[i]) : none);
+      y[i] = __ffma2_rn(b, r.yy[i], pair ? __fmul2_rn(a, r.yx[i]) : none);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = x[i], b = y[i];
+      x[i] = __ffma2_rn(a, r.xx[i], __fmul2_rn(b, r.xy[i]));
+      y[i] = __ffma2_rn(b, r.yy[i], __fmul2_rn(a, r.yx[i]));
+      if (NORM) x[i] = __fmul2_rn(x[i], rs), y[i] = __fmul2_rn(y[i], rs);
+    }
   }
   if (STYLE == DSA_ROPE_NEOX) {
     u = pack8<BF16>(x);
