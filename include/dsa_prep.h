@@ -643,10 +643,11 @@ dsa_status dsa_cache_compact(
  * A cache is given by where its tokens' entries are: `bases` and `shapes` are
  * HOST arrays, read during the call; with s = shapes + 5 * v, token t of page p
  * of view v is at bases[v] + p * s[0] + t * s[1] + h * s[2], s[4] bytes for each
- * head h < s[3].  All are multiples of 4 (of 16: 16 bytes move at a time).  A
- * page-blocked index-K cache is two views, its codes and its scales.  No two
- * views share a byte.  0 <= n_views <= DSA_MAX_VIEWS; with none only the tables
- * are kept.
+ * head h < s[3].  All are multiples of 4 (of 16: 16 bytes move at a time); entries
+ * may not overlap, nor dimensions interleave (each stride passes what those of smaller
+ * strides span).  A page-blocked index-K cache is two views, its codes and its
+ * scales.  No two views share a byte.  0 <= n_views <= DSA_MAX_VIEWS; with none only
+ * the tables are kept (one launch).
  *
  *   which, drafted, n_kept  int32 [n], n <= DSA_MAX_KEEPS; every row named once.
  *   kept           int32 [n, max_kept], row stride kept_stride >= max_kept, or 0:

@@ -33,6 +33,7 @@
 
 #include "dsa_common.cuh"
 #include "dsa_prep.h"
+#include "dsa_rows.cuh"
 
 namespace {
 
@@ -210,9 +211,7 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-bool misaligned(const void* ptr, uintptr_t a) {
-  return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) != 0;
-}
+using dsa_rows::misaligned;
 
 // shapes[5 i ..]: page, token and head stride, heads and bytes; strides of one
 // entry are never used and become 0.
@@ -232,6 +231,7 @@ dsa_status read_views(void* const* bases, const int64_t* shapes, int32_t n_views
       if (extent[d] > 1 && (s[d] < s[4] || s[d] >= (1LL << 40))) return DSA_ERR_SHAPE;
       if (stride[d] % 4) return DSA_ERR_ALIGN;
     }
+    if (!dsa_rows::rows_apart(s[4], extent, stride)) return DSA_ERR_SHAPE;
     if (misaligned(bases[i], 4) || s[4] % 4) return DSA_ERR_ALIGN;
     out->v[i] = {static_cast<char*>(bases[i]), stride[0], stride[1], stride[2],
                  static_cast<int>(s[3]), static_cast<int>(s[4])};
