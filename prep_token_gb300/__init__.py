@@ -18,11 +18,14 @@ from __future__ import annotations
 import array
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
+import warnings
 
 import torch
 
-from ._build import BINDING_PATH, LIB_PATH
+from ._build import LIB_PATH, binding_path
 
 __all__ = [
     "DsaError", "NEOX", "GPTJ", "HEAD_DIM", "DEVERR_POSITION", "DEVERR_SLOT", "DEVERR_TIMEOUT",
@@ -144,36 +147,58 @@ def library() -> ctypes.CDLL:
         lib.dsa_status_string.restype = ctypes.c_char_p
         lib.dsa_prep_version.argtypes = []
         lib.dsa_prep_version.restype = ctypes.c_int32
-        _bind(lib)
         _lib = lib
     return _lib
 
 
-_usual = None  # the module of _marshal, once the library is loaded
+_usual = None  # what _marshal returns, from its first call on
 
 
-def _bind(lib):
-    """Loads the calls' marshalling in C++ and hands it their entry points."""
-    global _usual
-    try:
-        from . import _binding
-    except ImportError as e:
-        raise RuntimeError(f"{BINDING_PATH} is missing or does not fit this torch: build it first "
-                           "(python -c 'import __graft_entry__ as g; g.build()')") from e
-    _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+class _Without:
+    """In the binding's place where there is none: every call takes the way through ctypes."""
+
+    @staticmethod
+    def rms_norm(*_):
+        return NotImplemented
+
+    kv_append = tree_attention = cache_keep = rms_norm
+
+
+def _load_binding():
+    """The binding, handed the calls' entry points; ImportError if there is none for this torch
+    or it cannot be loaded."""
+    path = binding_path()
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing")
+    name = f"{__name__}._binding"
+    loader = importlib.machinery.ExtensionFileLoader(name, path)
+    module = importlib.util.module_from_spec(
+        importlib.util.spec_from_file_location(name, path, loader=loader))
+    loader.exec_module(module)
+    lib = library()
+    module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.dsa_rms_norm, lib.dsa_kv_append, lib.dsa_tree_attention,
         lib.dsa_paged_attention_workspace_bytes, lib.dsa_cache_keep,
         lib.dsa_cache_keep_workspace_bytes)))
-    _usual = _binding
+    return module
 
 
 def _marshal():
     """The marshalling in C++ of calls in their usual form (outputs allocated, the
     current stream and device).  Its functions return NotImplemented for any
     other call, which then takes the way through ctypes, and a status that is not
-    DSA_OK as an int."""
+    DSA_OK as an int.  Without the binding all calls take that way, which costs 15
+    to 25 us of the host's time more."""
+    global _usual
     if _usual is None:
         library()
+        try:
+            _usual = _load_binding()
+        except ImportError as e:
+            warnings.warn(f"eager calls are marshalled through ctypes: {e}; build the binding "
+                          "(python -c 'import __graft_entry__ as g; g.build()')", RuntimeWarning,
+                          stacklevel=3)
+            _usual = _Without
     return _usual
 
 

@@ -1,18 +1,19 @@
 """Builds libdsaprep.so in-tree with nvcc for sm_103a (no torch extension
-machinery: the library is plain C ABI over CUDA), and beside it _binding.so, the
-marshalling in C++ of the calls that a decode step makes eagerly."""
+machinery: the library is plain C ABI over CUDA), and beside it _binding-*.so, the
+marshalling in C++ of the calls that a decode step makes eagerly.  The library does
+without the binding, which fits one torch and one Python and carries their versions
+in its name."""
 from __future__ import annotations
 
 import glob
-import importlib.util
 import os
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB_PATH = os.path.join(PKG, "libdsaprep.so")
-BINDING_PATH = os.path.join(PKG, "_binding.so")
 BINDING_SOURCE = os.path.join(PKG, "csrc", "binding.cpp")
 INCLUDE = os.path.join(ROOT, "include")
 NVCC_FLAGS = [
@@ -48,36 +49,61 @@ def _stale() -> bool:
     return _older(LIB_PATH, sources() + glob.glob(os.path.join(PKG, "csrc", "*.cuh")) + _headers())
 
 
+def binding_path() -> str:
+    """The binding for this torch and this Python."""
+    import torch
+    return os.path.join(PKG, f"_binding-torch{torch.__version__}-{sys.implementation.cache_tag}.so")
+
+
+def _torch_include() -> str:
+    import torch
+    return os.path.join(os.path.dirname(torch.__file__), "include")
+
+
+def _binding_needs() -> list[str]:
+    """Headers that an installation may lack."""
+    return [os.path.join(_torch_include(), "torch", "csrc", "autograd", "python_variable.h"),
+            os.path.join(sysconfig.get_paths()["include"], "Python.h")]
+
+
 def _binding_command(out: str) -> list[str]:
     import torch
-    at = os.path.dirname(torch.__file__)
+    include = _torch_include()
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
-    return ["g++", "-O1", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
-            "-I", os.path.join(at, "include"),
-            "-I", os.path.join(at, "include", "torch", "csrc", "api", "include"),
+    return ["g++", "-O1", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-I", include,
+            "-I", os.path.join(include, "torch", "csrc", "api", "include"),
             "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-            "-o", out, BINDING_SOURCE, "-L", os.path.join(at, "lib"),
+            "-o", out, BINDING_SOURCE, "-L", os.path.join(os.path.dirname(include), "lib"),
             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
     """Compile every .cu under csrc/ (in parallel, one nvcc per file) and
-    link them into one shared library, and the binding beside them."""
+    link them into one shared library, and the binding beside them (left out, and
+    said so, where torch's or Python's headers are not installed)."""
+    import torch
     tag = f"{os.getpid()}"
-    binding = None
-    torch_file = importlib.util.find_spec("torch").origin  # another torch, another binding
-    if force or _older(BINDING_PATH, [BINDING_SOURCE, torch_file] + _headers()):
-        binding = subprocess.Popen(_binding_command(BINDING_PATH + f".tmp{tag}"))
+    path, binding = binding_path(), None
+    made = path + f".tmp{tag}"
+    if force or _older(path, [BINDING_SOURCE, torch.__file__] + _headers()):
+        missing = [h for h in _binding_needs() if not os.path.exists(h)]
+        if missing:
+            print(f"{os.path.basename(path)} is not built: no {', '.join(missing)}", file=sys.stderr)
+        else:
+            binding = subprocess.Popen(_binding_command(made))
     try:
         if force or _stale():
             _build_cuda(tag, verbose)
+        if binding:
+            if binding.wait():
+                raise subprocess.CalledProcessError(binding.returncode, "g++ binding.cpp")
+            os.replace(made, path)
     finally:
-        code = binding.wait() if binding else 0
-    if code:
-        raise subprocess.CalledProcessError(code, "g++ binding.cpp")
-    if binding:
-        os.replace(BINDING_PATH + f".tmp{tag}", BINDING_PATH)
+        if binding:
+            binding.wait()
+            if os.path.exists(made):
+                os.remove(made)
     return LIB_PATH
 
 
