@@ -351,6 +351,7 @@ dsa_status dsa_indexer_mqa_logits(
  *                  be `residual` or x itself, row for row.
  *   gamma          fp32 [N], 16-byte aligned; eps finite and > 0.
  *   out            dtype [T, N], or NULL.  May be x itself, row for row.
+ *   Rows of all of them are N or more values apart.
  *   codes, scales  e4m3 bytes [T, N], 8-byte aligned, and [T, ceil(N / group)]
  *                  scales as scale_format says (fp32: 4-byte aligned), or both
  *                  NULL.  At least one of out and codes is given.
@@ -379,8 +380,8 @@ dsa_status dsa_rms_norm(
  *
  *   q              bf16 or fp16 (dtype) [T, H, head_dim]; H may be 0 (K and V
  *                  only), then q and q_out may be NULL.
- *   k, v           the same type [T, Hkv, head_dim].  All three with strides for
- *                  tokens and heads, so they may be slices of one projection.
+ *   k, v           the same type [T, Hkv, head_dim].  All three with positive strides
+ *                  for tokens and heads, so they may be slices of one projection.
  *   positions, out_cache_loc, cos_cache, sin_cache, cs_stride, max_position
  *                  as in dsa_indexer_qk_prepare_store.
  *   q_gamma,       fp32 [head_dim], 16-byte aligned, or NULL (no norm); with
@@ -498,7 +499,9 @@ dsa_status dsa_paged_attention(
  *     [j / 32] is set (for a tree: itself and the drafts above it), and
  *   key j < before with (window == 0 or j > pos - window or j < sinks), where pos
  *     = before - 1 + the number of drafts it sees, its position in the tree.
- * The window hides no draft.  A row that sees no key gets out 0 and lse -inf.
+ * The window hides no draft: where a path may be longer than the window, clear the
+ * bits of the drafts that it hides (pos then hides every key before the drafts).
+ * A row that sees no key gets out 0 and lse -inf.
  *   tree_mask      uint32 words [T, mask_words], row stride mask_stride words,
  *                  4-byte aligned.  Drafts past 32 * mask_words are seen by none;
  *                  bits at n_b and behind are ignored.

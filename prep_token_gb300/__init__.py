@@ -666,7 +666,7 @@ def dsa_rms_norm(x, gamma, eps, *, residual=None, residual_out=None, out=None, p
                  stream=None):
     """RMS norm of rows (one launch): out = z * gamma / sqrt(mean(z^2) + eps)
     with z = x + residual, in fp32 and rounded once.  x, residual [T, N] bf16 or
-    fp16 (N a multiple of 8, rows of any stride), gamma [N] fp32.  Returns out,
+    fp16 (N a multiple of 8, rows N or more values apart), gamma [N] fp32.  Returns out,
     or (out, residual_out) with residual_out = z rounded once if a residual is
     given; residual_out may be the residual, out may be x."""
     if stream is None and out is None and residual_out is None:
@@ -786,9 +786,9 @@ def dsa_kv_append(q, k, v, positions, out_cache_loc, cos_cache, sin_cache, k_cac
     """Appends tokens to a paged K/V cache and rotates their q (one launch).
 
     q [T, H, D] (or None), k, v [T, Hkv, D] bf16 or fp16, D 64 or 128, of any
-    strides (slices of one projection); positions, out_cache_loc [T] int64;
+    positive strides (slices of one projection); positions, out_cache_loc [T] int64;
     cos/sin caches [max_position, >= rope_dim / 2] fp32; k_cache, v_cache
-    [num_pages, page_size, Hkv, D] views of any strides, written in place at
+    [num_pages, page_size, Hkv, D] views of any positive strides, written in place at
     slot out_cache_loc[t].  ``q_gamma``, ``k_gamma`` [D] fp32: an RMS norm of
     every head of q or k (with ``eps``) before the rotation.  Returns the rotated
     q [T, H, D] (``q_out``, which may be q itself)."""
@@ -1219,8 +1219,11 @@ def dsa_cache_keep(caches, page_refs, block_table, context_lens, page_size, rows
     The last drafted[i] tokens of row rows[i] are drafts, kept[i, :n_kept[i]]
     the accepted ones among them, ascending from 0.  In every cache their
     entries move to the front of the drafts' place; context_lens and the block
-    table shrink to them, and the pages behind go back to the pool.  caches: a
-    TokenViews, or a list of tensors for one; rows, drafted, n_kept [n] int32,
+    table shrink to them, and the pages behind go back to the pool.  An entry goes
+    only to a page that no other row holds: else the row stays as it is, with
+    DEVERR_REFS (a row forked with drafts pending shares pages with its copy).
+    caches: a TokenViews, or a list of tensors, of which one is made at every call (1
+    to 2 us of the host's time for each tensor); rows, drafted, n_kept [n] int32,
     kept [n, most] int32 (a list for all of them by expand)."""
     views = caches if isinstance(caches, TokenViews) else TokenViews(caches)
     if stream is None and workspace is None:

@@ -13,7 +13,8 @@
 // factors per pair, formed once, and the root is multiplied in at the end.
 //
 // Two kernels: few tokens take a warp to every pass of 512 / D rows, so that all
-// is in flight at once; many take warps that stay and load ahead.
+// is in flight at once, or nearly (1500 tokens of 72 heads of 64 are 1.85 rounds of
+// its CTAs); many take warps that stay and load ahead.
 //
 // Bound: HBM for many tokens, each row read and written once; measured (6.78 TB/s):
 // 8192 tokens of 32 + 16 heads of 128, 206 MB, 36.3 us with both norms (5.7 TB/s),

@@ -63,8 +63,10 @@
 // 32768, 32 on 4: 112 us (1150 TFLOP/s);
 // 8 drafts over 1000: 14.1 us, of which the first scores take 4, softmax, values and
 // parts 3, launches and join the rest; 24 x 32 with a window of 1024, 16 heads of 64 on
-// as many: 41 us, 368 items of ten blocks in two rounds of 304, the 32 rows' one warp
-// 1750 of a block's 2500 cycles.  Copies of those rows, a quarter of the keys to each
+// as many: 40 us, 368 items of ten blocks cut into 12.4 blocks per CTA of 2500 cycles
+// each, which is 16 us, the rest the start, the ends of two to three items per CTA and
+// the join (whole items, two rounds of 304: 42); of a block's 2500 cycles the 32 rows' one
+// warp takes 1750.  Copies of those rows, a quarter of the keys to each
 // warp: 1300, latency else, but joining them took 2700 more at an item's end (47 us).
 //
 // Every wait is bounded in time; TMEM is always released before exit.
@@ -1733,15 +1735,19 @@ Plan make_plan(int T, int B, int Hkv, int D, int q_tokens, int max_context, int 
 //           contexts of three quarters of max_context on average;
 //   join    the parts' rows, 8 bytes per value at 8 TB/s;
 //   ragged  a fifth of an item, as requests' contexts differ.
-// Either number of tiles may be cut.  In us, measured:
-//                                        whole, 1 and 2 tiles; cut, 1 and 2
-//   1 x 8 over 1000, 64 on 8                  20    19    16    16
-//   64 x 16 over up to 8192, 64 on 8         231   309   207   233
-//   32 x 16 over 8000, 64 on 8               162   199   189   191
-//   64 x 5 over 4000, 32 on 4                 89   106   101   104
-//   16 x 60, window 2048, 32 on 8             54    46    72    60
-//   16 x 30 over 8000, 32 on 4               104   104   104    71
-//   24 x 32 over 1000, 16 on 16, D 64         35    42    36    47
+// Either number of tiles may be cut.  In us, measured, and what the rule takes:
+//                                     whole, 1 and 2 tiles; cut, 1 and 2; taken
+//   1 x 8 over 1000, 64 on 8               18.9  18.4  14.0  14.7  cut, 1
+//   64 x 16 over up to 8192, 64 on 8        229   307   206   235  cut, 1
+//   32 x 16 over 8000, 64 on 8              162   207   188   200  cut, 1: 17% more
+//   64 x 5 over 4000, 32 on 4                89   106   100   103  cut, 1: 12% more
+//   16 x 60, window 2048, 32 on 8            45    41    63    55  whole, 2
+//   16 x 30 over 8000, 32 on 4              107   104   103    70  cut, 2
+//   24 x 32 over 1000, 16 on 16, D 64        34    44    34    47  whole, 1
+//   24 x up to 32, window 1024, the same     42    56    40    61  cut, 1
+// Where all contexts are equal and items nearly fill the CTAs once, the fifth of an item
+// for raggedness is not there and whole items would be the better choice: the host does
+// not know the lengths.
 Plan make_tree_plan(int T, int B, int Hkv, int G, int D, int q_tokens, int max_context, int window,
                     int sinks, bool may) {
   constexpr double kItem[2] = {3.5, 5.0}, kCut[2] = {10.0, 10.0}, kRagged = 0.2;

@@ -21,11 +21,12 @@
 //
 // Bound: the moved bytes where rows and layers are many, two launches and their
 // chains of dependent reads where they are few.  Measured: up to 8 of up to 32
-// drafts of 48 rows in the K and V caches of 40 layers (2 KB entries, 59 MB) 16 us,
-// of which the second kernel's 3840 CTAs of two round trips each take 12 (59 MB at
-// 6.78 TB/s: 8.7); one row in 21 layers 4.5 us.  One launch, a cluster of CTAs to a row with
-// the tables changed behind its barrier, took 23 and 6 us; a kernel that
-// read the lists per cache 17.  Moves read by every thread instead of through
+// drafts of 48 rows in the K and V caches of 40 layers (2 KB entries, 59 MB) 15.8 us,
+// of which the second kernel's 3888 CTAs, two rounds of two round trips each, take 12
+// (59 MB at 6.78 TB/s: 8.7); one row in 21 layers 4.3 us.  With the table changed in
+// the first kernel 16.3 and 4.5.  One launch, a cluster of CTAs to a row with the
+// tables changed behind its barrier, took 23 and 6 us; a kernel that read the lists per
+// cache 17.  Moves read by every thread instead of through
 // shared memory: the same time at twice the registers.
 #include <cuda_runtime.h>
 
